@@ -375,6 +375,163 @@ int dsa_indexer_select_noalloc(const dsa_select_plan* plan, const dsa_indexer_cf
                                const float* w, const int32_t* ends, int32_t* cand, int32_t* topk,
                                struct CUstream_st* stream);
 
+/*
+ * Paged key/value cache held in 4 bits, and the sparse attention over it.
+ *
+ * The selection above gives each query row the positions it attends to.  In a
+ * server those positions belong to many requests, whose keys and values sit in
+ * pages; the calls below keep the pages, store rows in 4 bits and attend to
+ * the selected ones.  No page describes this part: it is this library's own
+ * design.
+ *
+ * Layout.  The cache is [pages, page_size, kv_heads] records of
+ * DSA_CACHE_RECORD_BYTES = 144 bytes, one per position and key/value head
+ * (head_dim = value_dim = 128):
+ *     bytes   0 ..  63   key codes, e2m1: dim 2 i in the low nibble of byte i,
+ *                        dim 2 i + 1 in the high one
+ *     bytes  64 .. 127   value codes, the same
+ *     bytes 128 .. 135   key scales, e4m3: byte g scales dims 16 g .. 16 g + 15
+ *     bytes 136 .. 143   value scales
+ * A key element is code * scale * 2^k_shift, a value element code * scale *
+ * 2^v_shift.  slot = page * page_size + offset numbers the positions of the
+ * whole cache; request r's position p lies in page tables[r, p / page_size] at
+ * offset p % page_size.  16-byte aligned; dsa_cache_bytes() gives its size.
+ *
+ *   pages      >= 0; pages * page_size < 2^31
+ *   page_size  a power of two, 1 .. 4096
+ *   kv_heads   1 .. 64
+ *   k_shift, v_shift   -32 .. 32: a power of two that keys (values) are
+ *              divided by before they are rounded.  One e4m3 scale covers
+ *              groups whose largest element is between 0.012 and 2688; smaller
+ *              groups become zeros, larger ones are clipped, unless the shift
+ *              moves them into that range.
+ * A cfg outside these limits gives DSA_ERR_INVALID_ARG (DSA_ERR_UNSUPPORTED
+ * for more kv_heads).  Rows are bf16, f16 or f32 (DSA_BF16, DSA_F16, DSA_F32).
+ */
+#define DSA_CACHE_RECORD_BYTES 144
+#define DSA_BF16 0
+#define DSA_F16 1
+#define DSA_F32 2
+
+typedef struct dsa_cache_cfg {
+  int32_t pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t k_shift;
+  int32_t v_shift;
+} dsa_cache_cfg;
+
+int dsa_cache_bytes(const dsa_cache_cfg* cfg, size_t* bytes);
+
+/*
+ * One step's pages, block tables and slots, from request lengths on the
+ * device: for request r, lens[r] is its length after the step and fresh[r] how
+ * many of those positions are this step's tokens (the last fresh[r]).
+ *   - a request that needs more pages than it holds (ceil(lens / page_size))
+ *     takes them from the top of the free stack, in request order and then in
+ *     position order; one that needs fewer (finished: lens 0; drafts rejected)
+ *     gives its last pages back, so that a step taken back leaves the stack as
+ *     it was.  Pages given back are taken again from the next call on.
+ *   - token i of the step (request after request, position after position)
+ *     gets token_req[i], ends[i] = its position + 1 (the live end that
+ *     dsa_select_topk takes with row_repeat 1) and slots[i].  Entries past the
+ *     last token get -1, 0 and -1: a padded batch selects, stores and attends
+ *     to nothing there.
+ *   requests   R, 0 .. 8192;  table_width  P, pages a request may hold
+ *   tokens     T, entries of token_req, ends and slots
+ *   lens, fresh  int32 [R];  tables int32 [R, P] and held int32 [R] (pages each
+ *              request holds now): updated; entries of tables at or past held
+ *              are -1 once they have been given back
+ *   free_pages int32 [free_capacity], a stack of *free_count page ids, the
+ *              next one last; both updated
+ *   first      int32 [R + 1]: the requests' first tokens, first[R] their total
+ *   status     int32 [4]: code, pages short, tokens, free pages now
+ * A step that cannot be taken changes nothing (tables, held, the stack), gives
+ * every entry -1, 0 and -1 and first = 0, and leaves its reason in status[0]:
+ *   1 more pages are needed than are free (status[1]: how many), or the stack
+ *     has no room for those given back;  2 a request needs more than P pages;
+ *   3 more tokens than T;  4 a length or count is negative, fresh[r] > lens[r],
+ *     or held[r] or *free_count is out of range.
+ * Where several hold, 4 comes first, then 2, 3 and 1.  A token whose page id
+ * is not in [0, pages) gets slot -1.  One launch; the tensors must not overlap.
+ */
+int dsa_cache_plan(const dsa_cache_cfg* cfg, int32_t requests, int32_t table_width, int32_t tokens,
+                   int32_t free_capacity, const int32_t* lens, const int32_t* fresh, int32_t* tables,
+                   int32_t* held, int32_t* free_pages, int32_t* free_count, int32_t* first,
+                   int32_t* token_req, int32_t* ends, int32_t* slots, int32_t* status,
+                   struct CUstream_st* stream);
+
+/*
+ * Store rows: token i's keys and values, k and v [tokens, kv_heads, 128] with
+ * k_stride (v_stride) elements from one token to the next, go to record
+ * slots[i].  Each group of 16 dims gets scale = e4m3(min(max|x| / 6, 448)) and
+ * codes e2m1(x / scale), both rounded to nearest, ties to even, and clipped
+ * (infinities too) to the type's largest; x is the element divided by the
+ * shift's power of two.  A group that holds a NaN reads back as NaN.
+ *   slots   int32 [tokens]; one outside [0, pages * page_size) stores nothing.
+ *           A slot named twice in a call holds one of its rows, or parts of
+ *           several: give each token its own.
+ */
+int dsa_cache_write(const dsa_cache_cfg* cfg, int32_t tokens, int32_t dtype, const void* k, const void* v,
+                    int64_t k_stride, int64_t v_stride, const int32_t* slots, uint8_t* cache,
+                    struct CUstream_st* stream);
+
+/* Read rows back: k and v [tokens, kv_heads, 128], contiguous and 16-byte
+ * aligned; zeros for a slot outside [0, pages * page_size).  With shifts of 0
+ * every element is exact in bf16 and f16. */
+int dsa_cache_read(const dsa_cache_cfg* cfg, int32_t tokens, int32_t dtype, const uint8_t* cache,
+                   const int32_t* slots, void* k, void* v, struct CUstream_st* stream);
+
+/*
+ * Sparse attention over the cache: the form for decode steps and mixed
+ * batches.  heads = kv_heads * n query heads, n = 1 .. 128; query head h reads
+ * key/value head h / n.  For token t of request token_req[t], with A(t) the
+ * positions listed in idx[t],
+ *     o[t, h] = sum_{j in A(t)} softmax_j(scale * q[t, h] . k[j]) v[j]
+ *     lse[t, h] = ln sum_{j in A(t)} exp(scale * q[t, h] . k[j])
+ * and an empty A(t) (no entry, or token_req[t] outside [0, requests)) gives
+ * o = 0, lse = -inf.
+ *   idx     int32 [tokens, select] (the rows of dsa_row_topk and
+ *           dsa_combine_window qualify): positions in any order, entries below 0
+ *           anywhere among them unused.  A position at or past table_width *
+ *           page_size, or in a page whose id is not in [0, pages), is not
+ *           attended to; one listed twice counts twice.
+ *   tables  int32 [requests, table_width]
+ *   q, o    [tokens, heads, 128] of one type, DSA_BF16 or DSA_F16, 16-byte
+ *           aligned;  lse  f32 [tokens, heads]
+ * Scores and sums are held in fp32; the softmax weights and the expanded rows
+ * enter the products in f16 (the rows exactly), o is rounded once.  Few rows
+ * split their lists over a cluster of CTAs; the order of every sum is fixed,
+ * so results repeat bit for bit.
+ */
+int dsa_cache_attention(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads, int32_t select,
+                        int32_t requests, int32_t table_width, int32_t dtype, const uint8_t* cache,
+                        const void* q, const int32_t* idx, const int32_t* token_req,
+                        const int32_t* tables, float scale, void* o, float* lse,
+                        struct CUstream_st* stream);
+
+/*
+ * The same attention for the tokens of one request's prompt chunk, whose
+ * neighbours select overlapping positions: G = 128 / n adjacent tokens share
+ * the union of their selections, as in dsa_sparse_attention, so that a record
+ * is read and expanded once a group.  n = heads / kv_heads = 8 or 16 and
+ * G * select <= 49,152.
+ *   idx     int32 [tokens, select]: each row's positions strictly ascending,
+ *           then -1 (a position listed twice counts once here)
+ *   table   int32 [table_width]: the request's block table
+ *   workspace  device memory, 16-byte aligned, of at least
+ *           dsa_cache_attention_prompt_workspace() bytes
+ * Everything else is as in dsa_cache_attention.
+ */
+int dsa_cache_attention_prompt_workspace(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads,
+                                         int32_t select, size_t* bytes);
+
+int dsa_cache_attention_prompt(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads, int32_t select,
+                               int32_t table_width, int32_t dtype, const uint8_t* cache, const void* q,
+                               const int32_t* idx, const int32_t* table, float scale, void* workspace,
+                               size_t workspace_bytes, void* o, float* lse,
+                               struct CUstream_st* stream);
+
 /* Static description of a status code. */
 const char* dsa_status_string(int status);
 

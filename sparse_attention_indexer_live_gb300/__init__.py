@@ -28,4 +28,19 @@ __all__ = ["DSA_OK", "DSA_ERR_INVALID_ARG", "DSA_ERR_UNSUPPORTED", "DSA_ERR_CUDA
            "Shard", "ShardedSelector", "shard_rows", "attention_cfg", "dsa_attention_cfg",
            "dsa_group_union", "dsa_sparse_attention_workspace", "dsa_sparse_attention",
            "dsa_sparse_attention_status", "ranges_attention_cfg", "dsa_sparse_attention_ranges_workspace",
-           "dsa_group_union_ranges", "dsa_sparse_attention_ranges"]
+           "dsa_group_union_ranges", "dsa_sparse_attention_ranges", "PagedCache", "cache_cfg", "dsa_cache_cfg",
+           "dsa_cache_bytes", "dsa_cache_plan", "dsa_cache_write", "dsa_cache_read", "dsa_cache_attention",
+           "dsa_cache_attention_prompt", "dsa_cache_attention_prompt_workspace"]
+
+_CACHE = ("PagedCache", "cache_cfg", "dsa_cache_cfg", "dsa_cache_bytes", "dsa_cache_plan", "dsa_cache_write",
+          "dsa_cache_read", "dsa_cache_attention", "dsa_cache_attention_prompt",
+          "dsa_cache_attention_prompt_workspace")
+
+
+def __getattr__(name):
+    """cache.py imports torch, which the rest of the package does not need to load."""
+    if name in _CACHE:
+        from . import cache
+        globals().update({n: getattr(cache, n) for n in _CACHE})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

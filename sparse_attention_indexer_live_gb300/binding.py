@@ -40,7 +40,9 @@ EXPORTS = ("dsa_select_init", "dsa_select_destroy", "dsa_plan_describe", "dsa_ca
            "dsa_indexer_status", "dsa_indexer_select_workspace", "dsa_indexer_select",
            "dsa_indexer_select_noalloc", "dsa_sparse_attention_workspace", "dsa_group_union",
            "dsa_sparse_attention", "dsa_sparse_attention_ranges_workspace", "dsa_group_union_ranges",
-           "dsa_sparse_attention_ranges", "dsa_sparse_attention_status", "dsa_status_string")
+           "dsa_sparse_attention_ranges", "dsa_sparse_attention_status", "dsa_cache_bytes",
+           "dsa_cache_plan", "dsa_cache_write", "dsa_cache_read", "dsa_cache_attention",
+           "dsa_cache_attention_prompt_workspace", "dsa_cache_attention_prompt", "dsa_status_string")
 
 # Size of the library's fixed scratch array used by dsa_indexer_select_noalloc
 # (DSA_NOALLOC_SCRATCH_BYTES in include/dsa_select.h).
@@ -69,6 +71,8 @@ class DsaSelectError(RuntimeError):
 def load(path: str | None = None):
     """Load the CUDA library (raises OSError when it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB_PATH
@@ -124,6 +128,18 @@ def load(path: str | None = None):
             L.dsa_indexer_select_noalloc.restype = i32
             L.dsa_indexer_select_noalloc.argtypes = [vp, ctypes.POINTER(dsa_indexer_cfg), vp, vp, vp,
                                                      vp, vp, vp, vp, vp]
+            # the dsa_cache_* calls (cache.py); their cfg goes by reference
+            c32, c64, f32, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+            for name, args in (
+                    ("dsa_cache_bytes", [vp, vp]),
+                    ("dsa_cache_plan", [vp] + [c32] * 4 + [vp] * 12),
+                    ("dsa_cache_write", [vp, c32, c32, vp, vp, c64, c64, vp, vp, vp]),
+                    ("dsa_cache_read", [vp, c32, c32, vp, vp, vp, vp, vp]),
+                    ("dsa_cache_attention", [vp] + [c32] * 6 + [vp] * 5 + [f32, vp, vp, vp]),
+                    ("dsa_cache_attention_prompt_workspace", [vp, c32, c32, c32, vp]),
+                    ("dsa_cache_attention_prompt", [vp] + [c32] * 5 + [vp] * 4 + [f32, vp, size, vp, vp, vp])):
+                fn = getattr(L, name)
+                fn.restype, fn.argtypes = i32, args
             L.dsa_status_string.restype = ctypes.c_char_p
             L.dsa_status_string.argtypes = [i32]
             _lib = L

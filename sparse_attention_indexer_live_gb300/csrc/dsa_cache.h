@@ -1,0 +1,81 @@
+// dsa_cache.h -- what the translation units of the paged 4-bit cache share
+// (not part of the C ABI).  Record layout: include/dsa_select.h.
+#ifndef DSA_CACHE_H
+#define DSA_CACHE_H
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dsa_internal.h"
+
+constexpr int kRec = DSA_CACHE_RECORD_BYTES;
+constexpr int kCacheDim = 128;
+constexpr int kRecV = 64;    // value codes
+constexpr int kRecKs = 128;  // key scales
+constexpr int kRecVs = 136;  // value scales
+
+// DSA_OK when cfg is within the limits.
+inline int check_cache_cfg(const dsa_cache_cfg* c) {
+  if (!c || c->pages < 0 || c->page_size < 1 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)))
+    return DSA_ERR_INVALID_ARG;
+  if ((int64_t)c->pages * c->page_size >= ((int64_t)1 << 31) || c->kv_heads < 1) return DSA_ERR_INVALID_ARG;
+  if (c->k_shift < -32 || c->k_shift > 32 || c->v_shift < -32 || c->v_shift > 32) return DSA_ERR_INVALID_ARG;
+  return c->kv_heads > 64 ? DSA_ERR_UNSUPPORTED : DSA_OK;
+}
+
+inline int log2_of(int x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
+
+inline int launched() { return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
+
+#ifdef __CUDACC__
+
+// 2^e, |e| <= 126
+__host__ __device__ __forceinline__ float pow2f(int e) {
+#ifdef __CUDA_ARCH__
+  return __int_as_float((e + 127) << 23);
+#else
+  return ldexpf(1.0f, e);
+#endif
+}
+
+// The eight e2m1 codes of a word as four f16 pairs, the low nibble first.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+
+// Two e4m3 bytes (the low half of w) as an f16 pair.
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %1;\n cvt.rn.f16x2.e4m3x2 %0, a;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// a * b on f16 pairs.  Code times scale is exact: 2 significant bits by 4,
+// between 2^-10 and 2688.
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The two halves of an f16 pair in fp32.
+__device__ __forceinline__ float2 f16x2_f32(uint32_t v) {
+  float2 f;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}\n"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(v));
+  return f;
+}
+
+#endif  // __CUDACC__
+
+#endif  // DSA_CACHE_H
