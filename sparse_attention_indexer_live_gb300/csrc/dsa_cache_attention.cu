@@ -1,11 +1,14 @@
 // dsa_cache_attention.cu -- sparse attention over the paged 4-bit cache
 // (declared in include/dsa_select.h).
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
 
 #include "dsa_cache.h"
+
+namespace cg = cooperative_groups;
 
 namespace {
 
@@ -18,9 +21,22 @@ struct AttendParams {
   void* o;
   float* lse;
   int32_t T, H, n, kv_heads, Kc, R, P, pages, shift;
+  int32_t chunks;    // groups of query heads a key/value head's are taken in
   float scale_log2;  // softmax scale * 2^k_shift * log2(e)
   float v_mul;       // 2^v_shift
 };
+
+// One element of an output row (and its lse, by the row's first thread) from
+// the row's maximum, sum and weighted sum.
+template <bool kBf16>
+__device__ __forceinline__ void store_row(const AttendParams& p, int64_t row, int d, float m, float l, float o) {
+  const float x = l == 0.f ? 0.f : o / l * p.v_mul;
+  if (kBf16)
+    static_cast<__nv_bfloat16*>(p.o)[row * kCacheDim + d] = __float2bfloat16_rn(x);
+  else
+    static_cast<__half*>(p.o)[row * kCacheDim + d] = __float2half_rn(x);
+  if (d == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
 
 // The record number (slot) of entry e of a row of request req, or -1.
 __device__ __forceinline__ int slot_of(const AttendParams& p, int req, int e) {
@@ -30,69 +46,395 @@ __device__ __forceinline__ int slot_of(const AttendParams& p, int req, int e) {
   return (page << p.shift) + (e & ((1 << p.shift) - 1));
 }
 
-__device__ __forceinline__ float load_q(const void* q, int64_t i, bool bf16) {
-  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i])
-              : __half2float(static_cast<const __half*>(q)[i]);
+// ---------------------------------------------------------------------------
+// the form for single tokens: one CTA, or a cluster of them, per token,
+// key/value head and 8 or 16 of its query heads
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 16;        // positions a warp takes at a time
+constexpr int kStages = 4;       // tiles of a warp in flight
+constexpr int kStageBytes = kTile * kRec;
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+constexpr int kListMax = 4096;   // entries of a CTA's share of the list held at once
+constexpr int kMaxSplit = 16;    // CTAs a row is split over
+constexpr int kORow = kCacheDim + 4;  // floats of an output row in shared memory (padded)
+
+__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 
-// Expanded element d of a record's keys (off 0) or values (off kRecV).
-__device__ __forceinline__ float element(const uint8_t* rec, int off, int soff, int d) {
-  const uint32_t b = rec[off + (d >> 1)];
-  uint32_t r[4];
-  e2m1x8((d & 1) ? b >> 4 : b & 15u, r);
-  const float c = f16x2_f32(r[0]).x;
-  return c * f16x2_f32(e4m3x2(rec[soff + (d >> 4)])).x;
+// D += A B, 16 x 8 x 16, f16 operands, fp32 accumulators
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 2^x by the hardware's base-2 exponential (relative error near 2^-22).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t low2(uint32_t v) { return __byte_perm(v, 0, 0x1010); }
+__device__ __forceinline__ uint32_t high2(uint32_t v) { return __byte_perm(v, 0, 0x3232); }
+
+// Row of a stage that holds fragment row r (0 .. 15).  Any assignment of the
+// tile's records to the rows of the products is right, as long as keys and
+// values use the same one; this one keeps the 16-byte key reads (rows 2 j and
+// 2 j + 1 of a phase) and the 8-byte value reads (rows 2 t) on different banks
+// at the records' stride of 36 words.
+__device__ __forceinline__ int stage_row(int r) {
+  const int e = r & 6;  // 2 t
+  const int o = r >> 3;
+  return (r & 1) ? 8 + ((e + 4 + o) & 7) : e + o;
 }
 
-// One CTA of 128 threads per token and query head: thread j scores entry j of
-// a tile of 128, then thread d sums dim d of the tile's values.
+// Two elements of a q row (type kBf16 ? bf16 : f16).
 template <bool kBf16>
-__global__ void __launch_bounds__(128) attend_kernel(const AttendParams p) {
-  __shared__ float sq[128], sp[128], red[4];
-  __shared__ int ss[128];
-  const int t = blockIdx.x / p.H, h = blockIdx.x % p.H;
-  const int kvh = h / p.n;
-  const int tid = threadIdx.x;
-  sq[tid] = load_q(p.q, ((int64_t)t * p.H + h) * 128 + tid, kBf16);
-  const int req = p.token_req ? p.token_req[t] : 0;
-  const bool live = req >= 0 && req < p.R;
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int j0 = 0; live && j0 < p.Kc; j0 += 128) {
-    const int j = j0 + tid;
-    const int slot = j < p.Kc ? slot_of(p, req, p.idx[(int64_t)t * p.Kc + j]) : -1;
-    __syncthreads();
-    ss[tid] = slot;
-    float s = -INFINITY;
-    if (slot >= 0) {
-      const uint8_t* rec = p.cache + ((int64_t)slot * p.kv_heads + kvh) * kRec;
-      s = 0.f;
-      for (int d = 0; d < 128; ++d) s += sq[d] * element(rec, 0, kRecKs, d);
-      s *= p.scale_log2;
+__device__ __forceinline__ float2 q_pair(uint32_t w) {
+  if (kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return f16x2_f32(w);
+}
+
+template <int kNT>
+struct Partial {  // one warp's or CTA's share of kNT * 8 heads' rows
+  float m[kNT * 8];
+  float l[kNT * 8];
+  float o[kNT * 8][kORow];
+};
+
+template <int kNT>
+constexpr int attend_smem() {
+  const int ring = kRingBytes, join = (kWarps + 1) * (int)sizeof(Partial<kNT>);
+  return (ring > join ? ring : join) + kListMax * 4;
+}
+
+// S^T = K Q^T and O^T = V^T P^T by mma.sync m16n8k16, so that the 16 rows are
+// positions (then dims) and the 8 columns query heads: a key/value head that
+// serves 8 heads fills the instruction.  Each fragment is made in registers
+// from the record's codes: a thread's key fragment is 16 bytes of one record
+// (32 dims, any order that q shares), its value fragment 8 bytes (one scale's
+// 16 dims) of four records, whose nibbles are interleaved so that one
+// conversion gives the pair of positions that the product wants in a register.
+template <int kNT, bool kBf16>
+__global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(const AttendParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  int32_t* list = reinterpret_cast<int32_t*>(smem);
+  uint8_t* work = smem + kListMax * 4;
+  __shared__ int s_n;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t4 = lane & 3;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int split = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  int unit = (int)blockIdx.x / split;
+  const int chunk = unit % p.chunks;
+  unit /= p.chunks;
+  const int kvh = unit % p.kv_heads;
+  const int tok = unit / p.kv_heads;
+  const int h0 = chunk * kNT * 8;                        // first of the key/value head's n query heads
+  const int nh = min(kNT * 8, p.n - h0);
+  const int64_t row0 = (int64_t)tok * p.H + kvh * p.n + h0;  // its row of q, o and lse
+  const int req = p.token_req ? p.token_req[tok] : 0;
+  const int Kc = req >= 0 && req < p.R ? p.Kc : 0;
+
+  // q as the B operand: thread (g, t4) holds head g's dims 32 t4 .. 32 t4 + 31,
+  // scaled by a power of two that puts the row's largest element at 2^12, so
+  // that bf16 rows of any magnitude are exact in f16
+  uint32_t qf[kNT][16];
+  float sc[kNT][2];  // exponent factor of heads 2 t4 and 2 t4 + 1
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+    uint4 w[4] = {};
+    const int h = nt * 8 + g;
+    if (h < nh) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (row0 + h) * kCacheDim + 32 * t4);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] = __ldg(src + u);
     }
-    float mx = s;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
+    float f[32];
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      const float2 v = q_pair<kBf16>(reinterpret_cast<const uint32_t*>(w)[u]);
+      f[2 * u] = v.x;
+      f[2 * u + 1] = v.y;
+      top = max(top, max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu));
+    }
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const int e = max((int)(top >> 23) - 127, -114);
+    const float mul = pow2f(12 - e);
+#pragma unroll
+    for (int u = 0; u < 16; ++u) qf[nt][u] = pack_f16x2(f[2 * u] * mul, f[2 * u + 1] * mul);
+    const float s = p.scale_log2 * pow2f(e - 12);
+    sc[nt][0] = __shfl_sync(0xFFFFFFFFu, s, 8 * t4);
+    sc[nt][1] = __shfl_sync(0xFFFFFFFFu, s, 8 * t4 + 4);
+  }
+
+  // this lane's 16-byte pieces of a tile: piece lane + 32 j is chunk c of record r
+  int piece_r[5];
+  int64_t piece_c[5];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) {
+    const int i = lane + 32 * j;
+    piece_r[j] = i / 9;
+    piece_c[j] = (i - 9 * (i / 9)) * 16;
+  }
+  uint8_t* ring = work + warp * (kStages * kStageBytes);
+  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring) + 16 * lane;
+  const uint8_t* base = p.cache + (int64_t)kvh * kRec;
+  const int64_t rec_stride = (int64_t)p.kv_heads * kRec;
+  const int rk0 = stage_row(g), rk1 = stage_row(g + 8);
+  const int rv[4] = {stage_row(2 * t4), stage_row(2 * t4 + 1), stage_row(2 * t4 + 8), stage_row(2 * t4 + 9)};
+
+  float m[kNT][2], l[kNT][2], o[kNT][8][4];
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      m[nt][c] = -INFINITY;
+      l[nt][c] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
+  }
+
+  // the row's tiles of 16 entries go to the cluster's CTAs in turn; a CTA
+  // takes its share kListMax entries at a time
+  const int64_t ntiles = ((int64_t)Kc + kTile - 1) / kTile;
+  const int64_t share = (ntiles - rank + split - 1) / split;  // tiles of this CTA (<= 0: none)
+  const int32_t* idx = p.idx + (int64_t)tok * p.Kc;
+  for (int64_t t0 = 0; t0 < share; t0 += kListMax / kTile) {
+    const int nt_here = (int)min(share - t0, (int64_t)(kListMax / kTile));
     __syncthreads();
-    const float m_new = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float base = m_new == -INFINITY ? 0.f : m_new;
-    const float pr = slot >= 0 ? exp2f(s - base) : 0.f;
-    sp[tid] = pr;
-    const float alpha = m == -INFINITY ? 0.f : exp2f(m - base);
-    m = m_new;
+    if (tid == 0) s_n = 0;
     __syncthreads();
-    l *= alpha;
-    acc *= alpha;
-    for (int i = 0; i < 128; ++i) {
-      if (ss[i] < 0) continue;
-      l += sp[i];
-      acc += sp[i] * element(p.cache + ((int64_t)ss[i] * p.kv_heads + kvh) * kRec, kRecV, kRecVs, tid);
+    int last = 0;
+    for (int i = tid; i < nt_here * kTile; i += kThreads) {
+      const int64_t e = ((t0 + i / kTile) * split + rank) * kTile + (i & (kTile - 1));
+      const int slot = e < Kc ? slot_of(p, req, __ldg(idx + e)) : -1;
+      list[i] = slot;
+      if (slot >= 0) last = i / kTile + 1;
+    }
+    last = __reduce_max_sync(0xFFFFFFFFu, last);
+    if (lane == 0 && last) atomicMax(&s_n, last);
+    __syncthreads();
+    const int n = s_n;  // tiles up to the last one with a position
+
+    auto issue = [&](int i, int st) {
+      if (i < n) {
+        const int32_t* e = list + i * kTile;
+#pragma unroll
+        for (int j = 0; j < 5; ++j) {
+          if (j < 4 || lane < 16) {
+            const int slot = e[piece_r[j]];
+            cp16z(ring_s + st * kStageBytes + 512 * j, base + max(slot, 0) * rec_stride + piece_c[j], slot >= 0);
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int st = 0;
+#pragma unroll
+    for (int u = 0; u < kStages - 1; ++u) issue(warp + u * kWarps, u);
+    for (int i = warp; i < n; i += kWarps) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();
+      issue(i + (kStages - 1) * kWarps, st == 0 ? kStages - 1 : st - 1);
+      const uint8_t* rec = ring + st * kStageBytes;
+      st = st == kStages - 1 ? 0 : st + 1;
+
+      // scores of rows g and g + 8
+      float s[kNT][4];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
+      {
+        const uint8_t* r0 = rec + rk0 * kRec;
+        const uint8_t* r1 = rec + rk1 * kRec;
+        const uint4 k0 = *reinterpret_cast<const uint4*>(r0 + 16 * t4);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(r1 + 16 * t4);
+        const uint32_t s0 = e4m3x2(*reinterpret_cast<const uint16_t*>(r0 + kRecKs + 2 * t4));
+        const uint32_t s1 = e4m3x2(*reinterpret_cast<const uint16_t*>(r1 + kRecKs + 2 * t4));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a[4], b[4];
+          e2m1x8(reinterpret_cast<const uint32_t*>(&k0)[w], a);
+          e2m1x8(reinterpret_cast<const uint32_t*>(&k1)[w], b);
+          const uint32_t sa = w < 2 ? low2(s0) : high2(s0), sb = w < 2 ? low2(s1) : high2(s1);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            a[u] = hmul2(a[u], sa);
+            b[u] = hmul2(b[u], sb);
+          }
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            mma16816(s[nt], a[0], b[0], a[1], b[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
+            mma16816(s[nt], a[2], b[2], a[3], b[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+          }
+        }
+      }
+      const bool v0 = list[i * kTile + rk0] >= 0, v1 = list[i * kTile + rk1] >= 0;
+      bool above = false;
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          s[nt][c] = (c < 2 ? v0 : v1) ? s[nt][c] * sc[nt][c & 1] : -INFINITY;
+          above |= s[nt][c] > m[nt][c & 1] + 8.f;  // a first position: above -inf
+        }
+      // The maximum that weights are taken against moves only when a score is
+      // above it by more than 8 (weights then stay below 2^8, within f16).
+      if (__any_sync(0xFFFFFFFFu, above)) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = fmaxf(s[nt][c], s[nt][c + 2]);
+            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+            if (x > m[nt][c] + 8.f) {
+              const float alpha = ex2(m[nt][c] - x);  // 0 from -inf
+              m[nt][c] = x;
+              l[nt][c] *= alpha;
+#pragma unroll
+              for (int i8 = 0; i8 < 8; ++i8) {
+                o[nt][i8][c] *= alpha;
+                o[nt][i8][c + 2] *= alpha;
+              }
+            }
+          }
+      }
+      uint32_t pf[kNT][2];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        float w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          // a head whose scores are all -inf has weights of 2^-inf = 0
+          const float mm = m[nt][c & 1] == -INFINITY ? 0.f : m[nt][c & 1];
+          w[c] = ex2(s[nt][c] - mm);
+        }
+        l[nt][0] += w[0] + w[2];
+        l[nt][1] += w[1] + w[3];
+        pf[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+        pf[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+      }
+      // O^T: dims 16 g + 2 i (row g) and 16 g + 2 i + 1 (row g + 8) of product i
+      {
+        uint2 c[4];
+        uint32_t sv[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint8_t* r = rec + rv[u] * kRec;
+          c[u] = *reinterpret_cast<const uint2*>(r + kRecV + 8 * g);
+          sv[u] = r[kRecVs + g];
+        }
+        const uint32_t sa = e4m3x2(sv[0] | sv[1] << 8), sb = e4m3x2(sv[2] | sv[3] << 8);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t x0 = w ? c[0].y : c[0].x, x1 = w ? c[1].y : c[1].x;
+          const uint32_t x2 = w ? c[2].y : c[2].x, x3 = w ? c[3].y : c[3].x;
+          const uint32_t kLo = 0x0F0F0F0Fu;
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          e2m1x8((x0 & kLo) | (x1 << 4 & ~kLo), a0);
+          e2m1x8((x0 >> 4 & kLo) | (x1 & ~kLo), a1);
+          e2m1x8((x2 & kLo) | (x3 << 4 & ~kLo), a2);
+          e2m1x8((x2 >> 4 & kLo) | (x3 & ~kLo), a3);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            a0[u] = hmul2(a0[u], sa);
+            a1[u] = hmul2(a1[u], sa);
+            a2[u] = hmul2(a2[u], sb);
+            a3[u] = hmul2(a3[u], sb);
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+              mma16816(o[nt][4 * w + u], a0[u], a1[u], a2[u], a3[u], pf[nt][0], pf[nt][1]);
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  __syncthreads();  // the ring is free
+
+  // join the warps' shares: part[w], then this CTA's in part[kWarps]
+  Partial<kNT>* part = reinterpret_cast<Partial<kNT>*>(work);
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float x = l[nt][c];
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
+      const int h = nt * 8 + 2 * t4 + c;
+      if (g == 0) {
+        part[warp].m[h] = m[nt][c];
+        part[warp].l[h] = x;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i += 2)
+        *reinterpret_cast<float4*>(&part[warp].o[h][16 * g + 2 * i]) =
+            make_float4(o[nt][i][c], o[nt][i][c + 2], o[nt][i + 1][c], o[nt][i + 1][c + 2]);
+    }
+  __syncthreads();
+  for (int h = 0; h < nh; ++h) {
+    float mx = part[0].m[h];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, part[w].m[h]);
+    const float b = mx == -INFINITY ? 0.f : mx;
+    float ls = 0.f, os = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float a = ex2(part[w].m[h] - b);
+      ls += a * part[w].l[h];
+      os += a * part[w].o[h][tid];
+    }
+    if (split == 1) {
+      store_row<kBf16>(p, row0 + h, tid, mx, ls, os);
+    } else {
+      part[kWarps].o[h][tid] = os;
+      if (tid == 0) {
+        part[kWarps].m[h] = mx;
+        part[kWarps].l[h] = ls;
+      }
     }
   }
-  const float o = l == 0.f ? 0.f : acc / l * p.v_mul;
-  const int64_t at = ((int64_t)t * p.H + h) * 128 + tid;
-  if (kBf16) static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(o);
-  else static_cast<__half*>(p.o)[at] = __float2half_rn(o);
-  if (tid == 0) p.lse[(int64_t)t * p.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  if (split == 1) return;
+  // join the CTAs' shares: CTA `rank` takes every split-th head
+  cluster.sync();
+  for (int h = rank; h < nh; h += split) {
+    float mx = -INFINITY;
+    for (int r = 0; r < split; ++r) mx = fmaxf(mx, cluster.map_shared_rank(part, r)[kWarps].m[h]);
+    const float b = mx == -INFINITY ? 0.f : mx;
+    float ls = 0.f, os = 0.f;
+    for (int r = 0; r < split; ++r) {
+      const Partial<kNT>* q = cluster.map_shared_rank(part, r) + kWarps;
+      const float a = ex2(q->m[h] - b);
+      ls += a * q->l[h];
+      os += a * q->o[h][tid];
+    }
+    store_row<kBf16>(p, row0 + h, tid, mx, ls, os);
+  }
+  cluster.sync();  // the peers' shares stay until everyone has read them
 }
 
 int check_attention(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads, int32_t select, int32_t requests,
@@ -132,12 +474,53 @@ AttendParams make_params(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads
   return p;
 }
 
-int launch_attend(const AttendParams& p, int32_t dtype, cudaStream_t s) {
-  if (dtype == DSA_BF16)
-    attend_kernel<true><<<(unsigned)(p.T * p.H), 128, 0, s>>>(p);
-  else
-    attend_kernel<false><<<(unsigned)(p.T * p.H), 128, 0, s>>>(p);
+// SMs of the current device, 0 on an error; kernels' attributes are set on its first use.
+template <int kNT, bool kBf16>
+int launch_one(AttendParams p, int split, cudaStream_t s) {
+  static bool done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  if (dev >= 64 || !done[dev]) {
+    if (cudaFuncSetAttribute(attend_kernel<kNT, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attend_smem<kNT>()) != cudaSuccess ||
+        cudaFuncSetAttribute(attend_kernel<kNT, kBf16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess) {
+      cudaGetLastError();
+      return DSA_ERR_CUDA;
+    }
+    if (dev < 64) done[dev] = true;
+  }
+  p.chunks = (p.n + kNT * 8 - 1) / (kNT * 8);
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)((int64_t)p.T * p.kv_heads * p.chunks * split));
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = attend_smem<kNT>();
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, attend_kernel<kNT, kBf16>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return DSA_ERR_CUDA;
+  }
   return launched();
+}
+
+int launch_attend(const AttendParams& p, int32_t dtype, cudaStream_t s) {
+  // Split rows until the CTAs fill the SMs about four times, while each CTA
+  // keeps a tile for every warp.
+  const int wide = p.n <= 8 ? 8 : 16;
+  const int64_t units = (int64_t)p.T * p.kv_heads * ((p.n + wide - 1) / wide);
+  int split = 1;
+  while (split < kMaxSplit && units * split * 2 <= 4 * 152 && (int64_t)p.Kc >= (int64_t)split * 2 * kTile * kWarps)
+    split *= 2;
+  if (units * split >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
+  if (wide == 8) return dtype == DSA_BF16 ? launch_one<1, true>(p, split, s) : launch_one<1, false>(p, split, s);
+  return dtype == DSA_BF16 ? launch_one<2, true>(p, split, s) : launch_one<2, false>(p, split, s);
 }
 
 bool aligned16(const void* a, const void* b, const void* c) {
