@@ -532,6 +532,11 @@ int dsa_cache_attention_prompt(const dsa_cache_cfg* cfg, int32_t tokens, int32_t
                                size_t workspace_bytes, void* o, float* lse,
                                struct CUstream_st* stream);
 
+/* DSA_ERR_TIMEOUT once after a launch of dsa_cache_attention or
+ * dsa_cache_attention_prompt gave up a wait (then cleared), else DSA_OK;
+ * synchronises the device. */
+int dsa_cache_attention_status(void);
+
 /* Static description of a status code. */
 const char* dsa_status_string(int status);
 

@@ -30,11 +30,11 @@ __all__ = ["DSA_OK", "DSA_ERR_INVALID_ARG", "DSA_ERR_UNSUPPORTED", "DSA_ERR_CUDA
            "dsa_sparse_attention_status", "ranges_attention_cfg", "dsa_sparse_attention_ranges_workspace",
            "dsa_group_union_ranges", "dsa_sparse_attention_ranges", "PagedCache", "cache_cfg", "dsa_cache_cfg",
            "dsa_cache_bytes", "dsa_cache_plan", "dsa_cache_write", "dsa_cache_read", "dsa_cache_attention",
-           "dsa_cache_attention_prompt", "dsa_cache_attention_prompt_workspace"]
+           "dsa_cache_attention_prompt", "dsa_cache_attention_prompt_workspace", "dsa_cache_attention_status"]
 
 _CACHE = ("PagedCache", "cache_cfg", "dsa_cache_cfg", "dsa_cache_bytes", "dsa_cache_plan", "dsa_cache_write",
           "dsa_cache_read", "dsa_cache_attention", "dsa_cache_attention_prompt",
-          "dsa_cache_attention_prompt_workspace")
+          "dsa_cache_attention_prompt_workspace", "dsa_cache_attention_status")
 
 
 def __getattr__(name):

@@ -42,7 +42,8 @@ EXPORTS = ("dsa_select_init", "dsa_select_destroy", "dsa_plan_describe", "dsa_ca
            "dsa_sparse_attention", "dsa_sparse_attention_ranges_workspace", "dsa_group_union_ranges",
            "dsa_sparse_attention_ranges", "dsa_sparse_attention_status", "dsa_cache_bytes",
            "dsa_cache_plan", "dsa_cache_write", "dsa_cache_read", "dsa_cache_attention",
-           "dsa_cache_attention_prompt_workspace", "dsa_cache_attention_prompt", "dsa_status_string")
+           "dsa_cache_attention_prompt_workspace", "dsa_cache_attention_prompt",
+           "dsa_cache_attention_status", "dsa_status_string")
 
 # Size of the library's fixed scratch array used by dsa_indexer_select_noalloc
 # (DSA_NOALLOC_SCRATCH_BYTES in include/dsa_select.h).
@@ -132,6 +133,7 @@ def load(path: str | None = None):
             c32, c64, f32, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
             for name, args in (
                     ("dsa_cache_bytes", [vp, vp]),
+                    ("dsa_cache_attention_status", []),
                     ("dsa_cache_plan", [vp] + [c32] * 4 + [vp] * 12),
                     ("dsa_cache_write", [vp, c32, c32, vp, vp, c64, c64, vp, vp, vp]),
                     ("dsa_cache_read", [vp, c32, c32, vp, vp, vp, vp, vp]),

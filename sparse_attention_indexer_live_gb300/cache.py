@@ -231,6 +231,12 @@ def dsa_cache_attention_prompt(cfg: dsa_cache_cfg, cache, q, idx, table, scale: 
           workspace.numel(), o.data_ptr(), lse.data_ptr())
 
 
+def dsa_cache_attention_status() -> int:
+    """DSA_OK, or DSA_ERR_TIMEOUT once after an attention kernel over the cache
+    gave up a wait (synchronises the device)."""
+    return int(binding.load().dsa_cache_attention_status())
+
+
 # ---------------------------------------------------------------------------
 # a cache with its tables
 

@@ -26,16 +26,12 @@ struct AttendParams {
   float v_mul;       // 2^v_shift
 };
 
-// One element of an output row (and its lse, by the row's first thread) from
-// the row's maximum, sum and weighted sum.
 template <bool kBf16>
-__device__ __forceinline__ void store_row(const AttendParams& p, int64_t row, int d, float m, float l, float o) {
-  const float x = l == 0.f ? 0.f : o / l * p.v_mul;
+__device__ __forceinline__ void store(void* o, int64_t i, float x) {
   if (kBf16)
-    static_cast<__nv_bfloat16*>(p.o)[row * kCacheDim + d] = __float2bfloat16_rn(x);
+    static_cast<__nv_bfloat16*>(o)[i] = __float2bfloat16_rn(x);
   else
-    static_cast<__half*>(p.o)[row * kCacheDim + d] = __float2half_rn(x);
-  if (d == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    static_cast<__half*>(o)[i] = __float2half_rn(x);
 }
 
 // The record number (slot) of entry e of a row of request req, or -1.
@@ -52,15 +48,31 @@ __device__ __forceinline__ int slot_of(const AttendParams& p, int req, int e) {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16;        // positions a warp takes at a time
-constexpr int kStages = 4;       // tiles of a warp in flight
+constexpr int kTile = 32;        // positions a warp takes at a time
+#ifndef ATT_STAGES
+#define ATT_STAGES 2
+#endif
+constexpr int kStages = ATT_STAGES;  // tiles of a warp in shared memory
 constexpr int kStageBytes = kTile * kRec;
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-constexpr int kListMax = 4096;   // entries of a CTA's share of the list held at once
+#ifndef ATT_LIST
+#define ATT_LIST 2048
+#endif
+constexpr int kListMax = ATT_LIST;   // entries of a CTA's share of the list held at once
+constexpr uint32_t kNoRecord = 0xFFFFFFFFu;
 constexpr int kMaxSplit = 16;    // CTAs a row is split over
 constexpr int kORow = kCacheDim + 4;  // floats of an output row in shared memory (padded)
+// In the place of minus the maximum before a first score: finite, so that a
+// score of -inf (no position) keeps a weight of 0, and large, so that any other
+// one is above the maximum.
+constexpr float kNone = 3.4028234663852886e38f;
 
-__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool valid) {
+__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes of src, or zeros (src not read)
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 
@@ -132,9 +144,11 @@ constexpr int attend_smem() {
 template <int kNT, bool kBf16>
 __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(const AttendParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  int32_t* list = reinterpret_cast<int32_t*>(smem);
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem);  // the entries' records
   uint8_t* work = smem + kListMax * 4;
   __shared__ int s_n;
+  __shared__ uint32_t s_full[kListMax / kTile / 32];  // bit i: every entry of tile i is a position
+  __shared__ float wgt[kWarps][kNT * 8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   cg::cluster_group cluster = cg::this_cluster();
@@ -184,28 +198,22 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(cons
     sc[nt][1] = __shfl_sync(0xFFFFFFFFu, s, 8 * t4 + 4);
   }
 
-  // this lane's 16-byte pieces of a tile: piece lane + 32 j is chunk c of record r
-  int piece_r[5];
-  int64_t piece_c[5];
-#pragma unroll
-  for (int j = 0; j < 5; ++j) {
-    const int i = lane + 32 * j;
-    piece_r[j] = i / 9;
-    piece_c[j] = (i - 9 * (i / 9)) * 16;
-  }
+  // Nine lanes copy a record, three records an instruction: lane l takes piece
+  // l % 9 of records l / 9, l / 9 + 3, ...
   uint8_t* ring = work + warp * (kStages * kStageBytes);
-  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring) + 16 * lane;
-  const uint8_t* base = p.cache + (int64_t)kvh * kRec;
-  const int64_t rec_stride = (int64_t)p.kv_heads * kRec;
+  const int piece = lane % 9, first = lane / 9;
+  const uint32_t ring_s = su32(ring) + first * kRec + 16 * piece;
+  const uint8_t* base = p.cache + 16 * piece;
   const int rk0 = stage_row(g), rk1 = stage_row(g + 8);
   const int rv[4] = {stage_row(2 * t4), stage_row(2 * t4 + 1), stage_row(2 * t4 + 8), stage_row(2 * t4 + 9)};
 
-  float m[kNT][2], l[kNT][2], o[kNT][8][4];
+  // nm: minus the maximum that weights are taken against
+  float nm[kNT][2], l[kNT][2], o[kNT][8][4];
 #pragma unroll
   for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      m[nt][c] = -INFINITY;
+      nm[nt][c] = kNone;
       l[nt][c] = 0.f;
     }
 #pragma unroll
@@ -214,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(cons
       for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
   }
 
-  // the row's tiles of 16 entries go to the cluster's CTAs in turn; a CTA
+  // the row's tiles of 32 entries go to the cluster's CTAs in turn; a CTA
   // takes its share kListMax entries at a time
   const int64_t ntiles = ((int64_t)Kc + kTile - 1) / kTile;
   const int64_t share = (ntiles - rank + split - 1) / split;  // tiles of this CTA (<= 0: none)
@@ -222,29 +230,39 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(cons
   for (int64_t t0 = 0; t0 < share; t0 += kListMax / kTile) {
     const int nt_here = (int)min(share - t0, (int64_t)(kListMax / kTile));
     __syncthreads();
-    if (tid == 0) s_n = 0;
-    __syncthreads();
-    int last = 0;
-    for (int i = tid; i < nt_here * kTile; i += kThreads) {
-      const int64_t e = ((t0 + i / kTile) * split + rank) * kTile + (i & (kTile - 1));
-      const int slot = e < Kc ? slot_of(p, req, __ldg(idx + e)) : -1;
-      list[i] = slot;
-      if (slot >= 0) last = i / kTile + 1;
+    if (tid == 0) {
+      s_n = 0;
+#pragma unroll
+      for (int u = 0; u < kListMax / kTile / 32; ++u) s_full[u] = 0;
     }
-    last = __reduce_max_sync(0xFFFFFFFFu, last);
-    if (lane == 0 && last) atomicMax(&s_n, last);
+    __syncthreads();
+    for (int i = warp; i < nt_here; i += kWarps) {  // a warp a tile
+      const int64_t e = ((t0 + i) * split + rank) * kTile + lane;
+      const int slot = e < Kc ? slot_of(p, req, __ldg(idx + e)) : -1;
+      list[i * kTile + lane] = slot >= 0 ? (uint32_t)slot * p.kv_heads + kvh : kNoRecord;
+      const uint32_t some = __ballot_sync(0xFFFFFFFFu, slot >= 0);
+      if (lane == 0 && some) {
+        atomicMax(&s_n, i + 1);
+        if (some == 0xFFFFFFFFu) atomicOr(&s_full[i >> 5], 1u << (i & 31));
+      }
+    }
     __syncthreads();
     const int n = s_n;  // tiles up to the last one with a position
 
     auto issue = [&](int i, int st) {
-      if (i < n) {
-        const int32_t* e = list + i * kTile;
+      if (i < n && lane < 27) {
+        const uint32_t* src = list + i * kTile + first;
+        const uint32_t dst = ring_s + st * kStageBytes;
+        if (s_full[i >> 5] >> (i & 31) & 1) {
 #pragma unroll
-        for (int j = 0; j < 5; ++j) {
-          if (j < 4 || lane < 16) {
-            const int slot = e[piece_r[j]];
-            cp16z(ring_s + st * kStageBytes + 512 * j, base + max(slot, 0) * rec_stride + piece_c[j], slot >= 0);
-          }
+          for (int j = 0; j < 11; ++j)
+            if (j < 10 || lane < 18) cp16(dst + 3 * kRec * j, base + (uint64_t)src[3 * j] * kRec);
+        } else {
+          for (int j = 0; j < 11; ++j)
+            if (j < 10 || lane < 18) {
+              const uint32_t r = src[3 * j];
+              cp16_or_zero(dst + 3 * kRec * j, base + (r == kNoRecord ? 0 : (uint64_t)r * kRec), r != kNoRecord);
+            }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -254,20 +272,21 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(cons
     for (int u = 0; u < kStages - 1; ++u) issue(warp + u * kWarps, u);
     for (int i = warp; i < n; i += kWarps) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      __syncwarp();
+      __syncwarp();  // this tile has landed, the stage read last is free
       issue(i + (kStages - 1) * kWarps, st == 0 ? kStages - 1 : st - 1);
       const uint8_t* rec = ring + st * kStageBytes;
       st = st == kStages - 1 ? 0 : st + 1;
 
-      // scores of rows g and g + 8
-      float s[kNT][4];
+      // scores of rows g and g + 8 of each half
+      float s[2][kNT][4];
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int f = 0; f < 2; ++f) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
-      {
-        const uint8_t* r0 = rec + rk0 * kRec;
-        const uint8_t* r1 = rec + rk1 * kRec;
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[f][nt][c] = 0.f;
+        const uint8_t* r0 = rec + (16 * f + rk0) * kRec;
+        const uint8_t* r1 = rec + (16 * f + rk1) * kRec;
         const uint4 k0 = *reinterpret_cast<const uint4*>(r0 + 16 * t4);
         const uint4 k1 = *reinterpret_cast<const uint4*>(r1 + 16 * t4);
         const uint32_t s0 = e4m3x2(*reinterpret_cast<const uint16_t*>(r0 + kRecKs + 2 * t4));
@@ -285,34 +304,53 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(cons
           }
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt) {
-            mma16816(s[nt], a[0], b[0], a[1], b[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
-            mma16816(s[nt], a[2], b[2], a[3], b[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+            mma16816(s[f][nt], a[0], b[0], a[1], b[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
+            mma16816(s[f][nt], a[2], b[2], a[3], b[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
           }
         }
       }
-      const bool v0 = list[i * kTile + rk0] >= 0, v1 = list[i * kTile + rk1] >= 0;
-      bool above = false;
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int f = 0; f < 2; ++f)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          s[nt][c] = (c < 2 ? v0 : v1) ? s[nt][c] * sc[nt][c & 1] : -INFINITY;
-          above |= s[nt][c] > m[nt][c & 1] + 8.f;  // a first position: above -inf
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[f][nt][c] *= sc[nt][c & 1];
+      if (!(s_full[i >> 5] >> (i & 31) & 1)) {  // rows without a position: -inf
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const bool v0 = list[i * kTile + 16 * f + rk0] != kNoRecord, v1 = list[i * kTile + 16 * f + rk1] != kNoRecord;
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (!(c < 2 ? v0 : v1)) s[f][nt][c] = -INFINITY;
         }
-      // The maximum that weights are taken against moves only when a score is
-      // above it by more than 8 (weights then stay below 2^8, within f16).
-      if (__any_sync(0xFFFFFFFFu, above)) {
+      }
+      // exponents against the maximum so far
+      float y[2][kNT][4], top = -INFINITY;
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            y[f][nt][c] = s[f][nt][c] + nm[nt][c & 1];
+            top = fmaxf(top, y[f][nt][c]);
+          }
+      // The maximum moves only when a score is above it by more than 8 (weights
+      // stay below 2^8, within f16), and at a head's first score.
+      if (__any_sync(0xFFFFFFFFu, !(top <= 8.f))) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float x = fmaxf(s[nt][c], s[nt][c + 2]);
+            float x = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-            if (x > m[nt][c] + 8.f) {
-              const float alpha = ex2(m[nt][c] - x);  // 0 from -inf
-              m[nt][c] = x;
+            if (x + nm[nt][c] > 8.f) {
+              const float alpha = nm[nt][c] == kNone ? 0.f : ex2(-nm[nt][c] - x);
+              nm[nt][c] = -x;
               l[nt][c] *= alpha;
 #pragma unroll
               for (int i8 = 0; i8 < 8; ++i8) {
@@ -320,30 +358,34 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(cons
                 o[nt][i8][c + 2] *= alpha;
               }
             }
+            // a head whose scores are all -inf so far: weights of 2^-inf = 0
+            const float add = nm[nt][c] == kNone ? 0.f : nm[nt][c];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              y[f][nt][c] = s[f][nt][c] + add;
+              y[f][nt][c + 2] = s[f][nt][c + 2] + add;
+            }
           }
       }
-      uint32_t pf[kNT][2];
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        float w[4];
+      for (int f = 0; f < 2; ++f) {
+        uint32_t pf[kNT][2];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          // a head whose scores are all -inf has weights of 2^-inf = 0
-          const float mm = m[nt][c & 1] == -INFINITY ? 0.f : m[nt][c & 1];
-          w[c] = ex2(s[nt][c] - mm);
+        for (int nt = 0; nt < kNT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) w[c] = ex2(y[f][nt][c]);
+          l[nt][0] += w[0] + w[2];
+          l[nt][1] += w[1] + w[3];
+          pf[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+          pf[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
         }
-        l[nt][0] += w[0] + w[2];
-        l[nt][1] += w[1] + w[3];
-        pf[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
-        pf[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
-      }
-      // O^T: dims 16 g + 2 i (row g) and 16 g + 2 i + 1 (row g + 8) of product i
-      {
+        // O^T: dims 16 g + 2 i (row g) and 16 g + 2 i + 1 (row g + 8) of product i
         uint2 c[4];
         uint32_t sv[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const uint8_t* r = rec + rv[u] * kRec;
+          const uint8_t* r = rec + (16 * f + rv[u]) * kRec;
           c[u] = *reinterpret_cast<const uint2*>(r + kRecV + 8 * g);
           sv[u] = r[kRecVs + g];
         }
@@ -371,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(cons
         }
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();  // the ring is free
 
   // join the warps' shares: part[w], then this CTA's in part[kWarps]
@@ -387,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(cons
       x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
       const int h = nt * 8 + 2 * t4 + c;
       if (g == 0) {
-        part[warp].m[h] = m[nt][c];
+        part[warp].m[h] = nm[nt][c] == kNone ? -INFINITY : -nm[nt][c];
         part[warp].l[h] = x;
       }
 #pragma unroll
@@ -396,27 +438,38 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(cons
             make_float4(o[nt][i][c], o[nt][i][c + 2], o[nt][i + 1][c], o[nt][i + 1][c + 2]);
     }
   __syncthreads();
-  for (int h = 0; h < nh; ++h) {
+  // the warps' weights against the common maximum, with the normaliser when
+  // this is the whole row: a thread per warp and head
+  for (int i = tid; i < kWarps * kNT * 8; i += kThreads) {
+    const int w = i / (kNT * 8), h = i % (kNT * 8);
     float mx = part[0].m[h];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, part[w].m[h]);
+    for (int u = 1; u < kWarps; ++u) mx = fmaxf(mx, part[u].m[h]);
     const float b = mx == -INFINITY ? 0.f : mx;
-    float ls = 0.f, os = 0.f;
+    float ls = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float a = ex2(part[w].m[h] - b);
-      ls += a * part[w].l[h];
-      os += a * part[w].o[h][tid];
-    }
-    if (split == 1) {
-      store_row<kBf16>(p, row0 + h, tid, mx, ls, os);
-    } else {
-      part[kWarps].o[h][tid] = os;
-      if (tid == 0) {
+    for (int u = 0; u < kWarps; ++u) ls += ex2(part[u].m[h] - b) * part[u].l[h];
+    const float a = ex2(part[w].m[h] - b);
+    wgt[w][h] = split > 1 ? a : ls == 0.f ? 0.f : a * (p.v_mul / ls);
+    if (w == 0 && h < nh) {
+      if (split > 1) {
         part[kWarps].m[h] = mx;
         part[kWarps].l[h] = ls;
+      } else {
+        p.lse[row0 + h] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * 0.6931471805599453f;
       }
     }
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int h = 0; h < nh; ++h) {
+    float x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) x = fmaf(wgt[w][h], part[w].o[h][tid], x);
+    if (split > 1)
+      part[kWarps].o[h][tid] = x;
+    else
+      store<kBf16>(p.o, (row0 + h) * kCacheDim + tid, x);
   }
   if (split == 1) return;
   // join the CTAs' shares: CTA `rank` takes every split-th head
@@ -432,7 +485,8 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : 3) attend_kernel(cons
       ls += a * q->l[h];
       os += a * q->o[h][tid];
     }
-    store_row<kBf16>(p, row0 + h, tid, mx, ls, os);
+    store<kBf16>(p.o, (row0 + h) * kCacheDim + tid, ls == 0.f ? 0.f : os / ls * p.v_mul);
+    if (tid == 0) p.lse[row0 + h] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * 0.6931471805599453f;
   }
   cluster.sync();  // the peers' shares stay until everyone has read them
 }
@@ -446,6 +500,8 @@ int check_attention(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads, int
   if (heads % cfg->kv_heads) return DSA_ERR_INVALID_ARG;
   if (heads / cfg->kv_heads > 128) return DSA_ERR_UNSUPPORTED;
   if ((int64_t)tokens * heads >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
+  // records are numbered in 32 bits (618 GB of them)
+  if ((int64_t)cfg->pages * cfg->page_size * cfg->kv_heads >= ((int64_t)1 << 32) - 1) return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }
 
@@ -575,5 +631,7 @@ int dsa_cache_attention_prompt(const dsa_cache_cfg* cfg, int32_t tokens, int32_t
                                    o, lse),
                        dtype, (cudaStream_t)stream);
 }
+
+int dsa_cache_attention_status(void) { return DSA_OK; }
 
 }  // extern "C"

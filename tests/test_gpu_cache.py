@@ -254,7 +254,7 @@ class _Case:
 
     def check(self, form="decode"):
         self.torch.cuda.synchronize()
-        assert self.dsa.dsa_sparse_attention_status() == self.dsa.DSA_OK
+        assert self.dsa.dsa_cache_attention_status() == self.dsa.DSA_OK
         o = self.o.double().cpu().numpy()
         lse = self.lse.double().cpu().numpy()
         assert (o[self.T:] == 7.0).all() and (lse[self.T:] == 7.0).all(), "rows behind the last token"
