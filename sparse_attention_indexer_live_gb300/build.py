@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = [os.path.join(PKG, "csrc", "dsa_select.cu"), os.path.join(PKG, "csrc", "dsa_indexer.cu"),
            os.path.join(PKG, "csrc", "dsa_attention.cu"), os.path.join(PKG, "csrc", "dsa_cache.cu"),
-           os.path.join(PKG, "csrc", "dsa_cache_attention.cu")]
+           os.path.join(PKG, "csrc", "dsa_cache_attention.cu"), os.path.join(PKG, "csrc", "dsa_cache_tile.cu")]
 HEADERS = [os.path.join(INCLUDE, "dsa_select.h"), os.path.join(PKG, "csrc", "dsa_internal.h"),
            os.path.join(PKG, "csrc", "dsa_cache.h")]
 BUILD_DIR = os.path.join(PKG, "_build")

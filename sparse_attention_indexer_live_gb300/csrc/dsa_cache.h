@@ -32,6 +32,29 @@ inline int log2_of(int x) {
 
 inline int launched() { return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
 
+// What both forms of the attention take.
+struct AttendParams {
+  const uint8_t* cache;
+  const void* q;
+  const int32_t* idx;
+  const int32_t* token_req;  // NULL: every token is of request 0
+  const int32_t* tables;
+  void* o;
+  float* lse;
+  int32_t T, H, n, kv_heads, Kc, R, P, pages, shift;
+  int32_t chunks;    // groups of query heads a key/value head's are taken in
+  float scale_log2;  // softmax scale * 2^k_shift * log2(e)
+  float v_mul;       // 2^v_shift
+};
+
+// The tensor-core form on tiles of 128 rows (dsa_cache_tile.cu).  records:
+// union records of groups of 128 / n tokens (dsa_group_union), whose keys are
+// positions of request 0; NULL: a token a tile, its own list.  n <= 128 rows.
+DSA_HIDDEN int dsa_cache_tile(const AttendParams& p, const uint8_t* records, bool bf16, cudaStream_t stream);
+
+// SMs of the device.
+constexpr int kSms = 152;
+
 #ifdef __CUDACC__
 
 // 2^e, |e| <= 126

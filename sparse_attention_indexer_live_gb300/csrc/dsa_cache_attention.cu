@@ -12,20 +12,6 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-struct AttendParams {
-  const uint8_t* cache;
-  const void* q;
-  const int32_t* idx;
-  const int32_t* token_req;  // NULL: every token is of request 0
-  const int32_t* tables;
-  void* o;
-  float* lse;
-  int32_t T, H, n, kv_heads, Kc, R, P, pages, shift;
-  int32_t chunks;    // groups of query heads a key/value head's are taken in
-  float scale_log2;  // softmax scale * 2^k_shift * log2(e)
-  float v_mul;       // 2^v_shift
-};
-
 template <bool kBf16>
 __device__ __forceinline__ void store(void* o, int64_t i, float x) {
   if (kBf16)
@@ -47,7 +33,6 @@ constexpr int kListTiles = 16;   // tiles of a warp listed at once
 constexpr int kListBytes = kWarps * kListTiles * kTile * 4 + 16;  // a tile's last read passes its end by 8 bytes
 constexpr uint32_t kNoRecord = 0xFFFFFFFFu;
 constexpr int kMaxSplit = 16;    // CTAs a row is split over: a power of two
-constexpr int kSms = 152;
 constexpr int kORow = kCacheDim + 4;  // floats of an output row in shared memory (padded)
 // In the place of minus the maximum before a first score: finite, so that a
 // score of -inf (no position) keeps a weight of 0, and large, so that any other
@@ -404,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[f][nt][c] *= sc[nt][c & 1];
+          for (int c = 0; c < 4; ++c) s[f][nt][c] = __fmul_rn(s[f][nt][c], sc[nt][c & 1]);
       if (!(full >> i & 1)) {  // rows without a position: -inf
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
@@ -634,6 +619,11 @@ int launch_staged(const AttendParams& p, int64_t ctas, int split, cudaStream_t s
   return ctas <= 2 * kSms ? launch_one<kNT, kBf16, 4>(p, split, s) : launch_one<kNT, kBf16, 2>(p, split, s);
 }
 
+#ifndef ATT_WARP_HEADS
+#define ATT_WARP_HEADS 16
+#endif
+constexpr int kMaxWarpHeads = ATT_WARP_HEADS;
+
 int launch_attend(const AttendParams& p, int32_t dtype, cudaStream_t s) {
   const int wide = p.n <= 8 ? 8 : 16;
   const int64_t units = (int64_t)p.T * p.kv_heads * ((p.n + wide - 1) / wide);
@@ -671,9 +661,10 @@ int dsa_cache_attention(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads,
   if (!q || !token_req || !o || !lse || !aligned16(cache, q, o)) return DSA_ERR_INVALID_ARG;
   if ((select > 0 && !idx) || (requests > 0 && table_width > 0 && !tables) || (cfg->pages > 0 && !cache))
     return DSA_ERR_INVALID_ARG;
-  return launch_attend(make_params(cfg, tokens, heads, select, requests, table_width, cache, q, idx, token_req,
-                                   tables, scale, o, lse),
-                       dtype, (cudaStream_t)stream);
+  const AttendParams p = make_params(cfg, tokens, heads, select, requests, table_width, cache, q, idx, token_req, tables,
+                                     scale, o, lse);
+  if (p.n > kMaxWarpHeads) return dsa_cache_tile(p, nullptr, dtype == DSA_BF16, (cudaStream_t)stream);
+  return launch_attend(p, dtype, (cudaStream_t)stream);
 }
 
 int dsa_cache_attention_prompt_workspace(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads,
@@ -700,11 +691,13 @@ int dsa_cache_attention_prompt(const dsa_cache_cfg* cfg, int32_t tokens, int32_t
   if (!q || !o || !lse || !aligned16(cache, q, o)) return DSA_ERR_INVALID_ARG;
   if ((select > 0 && !idx) || (table_width > 0 && !table) || (cfg->pages > 0 && !cache)) return DSA_ERR_INVALID_ARG;
   if (!workspace || ((uintptr_t)workspace & 15u) || workspace_bytes < need) return DSA_ERR_INVALID_ARG;
-  return launch_attend(make_params(cfg, tokens, heads, select, 1, table_width, cache, q, idx, nullptr, table, scale,
-                                   o, lse),
-                       dtype, (cudaStream_t)stream);
+  dsa_attention_cfg u = {tokens, heads / cfg->kv_heads, (int32_t)std::min<int64_t>((int64_t)table_width * cfg->page_size, INT32_MAX),
+                         kCacheDim, kCacheDim, select};
+  st = dsa_group_union(&u, idx, workspace, workspace_bytes, stream);
+  if (st != DSA_OK) return st;
+  return dsa_cache_tile(make_params(cfg, tokens, heads, select, 1, table_width, cache, q, idx, nullptr, table, scale, o,
+                                    lse),
+                        static_cast<const uint8_t*>(workspace), dtype == DSA_BF16, (cudaStream_t)stream);
 }
-
-int dsa_cache_attention_status(void) { return DSA_OK; }
 
 }  // extern "C"
