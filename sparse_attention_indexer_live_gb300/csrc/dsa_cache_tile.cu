@@ -65,6 +65,7 @@ constexpr uint32_t kIdescPV = kIdesc | (1u << 16);
 constexpr int kMaxSplit = 8;
 constexpr uint32_t kNoRecord = 0xFFFFFFFFu;
 constexpr long long kWaitCycles = 4000000000ll;  // ~2 s
+constexpr uint32_t kSuspendNs = 1000000;  // a try of a wait may sleep this long: less polling
 
 __device__ int g_cache_attn_error;
 __shared__ int s_abort;
@@ -88,9 +89,9 @@ __device__ __forceinline__ void bar_arrive(uint64_t* b) {
 __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(su32(b)), "r"(parity)
+      : "r"(su32(b)), "r"(parity), "r"(kSuspendNs)
       : "memory");
   return ok != 0;
 }
@@ -109,6 +110,15 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
     if (*(volatile int*)&s_abort) return false;
   }
   return true;
+}
+// All lanes of the warp wait.
+__device__ __forceinline__ bool wait_all(uint64_t* b, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(b, parity));
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
+  return x != 0;
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -136,25 +146,31 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t a, uint32_t leading) {
   d |= (uint64_t)2 << 61;            // 128-byte swizzle
   return d;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+template <bool kAcc>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u));
+      "r"(a), "l"(b), "r"(idesc), "n"(kAcc ? 1 : 0));
 }
-// S = Q K^T over the 128 dims: Q in TMEM, dims 2 c and 2 c + 1 in column c.
-__device__ __forceinline__ void mma_qk(uint32_t s, uint32_t q, uint32_t k) {
+// The issuing thread's own instructions can bound a tile's period: a step's
+// descriptor is one addition to the tile's.
+// S = Q K^T over the 128 dims: Q in TMEM, dims 2 c and 2 c + 1 in column c; k:
+// the key tile's descriptor.
+__device__ __forceinline__ void mma_qk(uint32_t s, uint32_t q, uint64_t k) {
+  mma_ts<false>(s, q, k, kIdesc);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    mma_ts(s, q + 8 * kk, sdesc(k + (uint32_t)((kk >> 2) * kBlk + (kk & 3) * 32), 16), kIdesc, kk > 0);
+  for (int kk = 1; kk < 8; ++kk)
+    mma_ts<true>(s, q + 8 * kk, k + (uint32_t)(((kk >> 2) * kBlk + (kk & 3) * 32) >> 4), kIdesc);
 }
 // O (+)= P V over 128 positions: P in the S buffer it came from, positions 2 c
 // and 2 c + 1 of the first half in column c, of the second in column 64 + c.
-__device__ __forceinline__ void mma_pv(uint32_t o, uint32_t p, uint32_t v, bool acc) {
+template <bool kAcc>
+__device__ __forceinline__ void mma_pv(uint32_t o, uint32_t p, uint64_t v) {
+  mma_ts<kAcc>(o, p, v, kIdescPV);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    mma_ts(o, p + (kk < 4 ? 8 * kk : 64 + 8 * (kk - 4)), sdesc(v + (uint32_t)(kk * 16 * 128), kBlk), kIdescPV,
-           acc || kk > 0);
+  for (int kk = 1; kk < 8; ++kk)
+    mma_ts<true>(o, p + (kk < 4 ? 8 * kk : 64 + 8 * (kk - 4)), v + (uint32_t)((kk * 16 * 128) >> 4), kIdescPV);
 }
 __device__ __forceinline__ void mma_commit(uint64_t* b) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(b))
@@ -373,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
       const int st = i % (is_k ? kKStages : kVStages), use = i / (is_k ? kKStages : kVStages);
       const int key3 = key_of(i + 3);
       const int page2 = page_of(key2);
-      if (use > 0 && !__all_sync(0xFFFFFFFFu, bar_wait(is_k ? &kempty[st] : &vempty[st], (use & 1) ^ 1))) break;
+      if (use > 0 && !wait_all(is_k ? &kempty[st] : &vempty[st], (use & 1) ^ 1)) break;
       const uint32_t dst = dst0 + st * 2 * kBlk;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -415,49 +431,68 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
     if (warp == 9 && kUnion) {
       // ---- mask warp: the tile's token masks, one 128-bit row per token
       const uint32_t* masks = reinterpret_cast<const uint32_t*>(rec + tp.masks_off);
-      for (int i = 0; i < ntiles; ++i) {
-        uint32_t m[4];
+      uint32_t m[4], m1[4];  // this tile's and the next one's
+      auto read = [&](int i, uint32_t (&x)[4]) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const int64_t e = ((int64_t)i * split + rank) * kTile + 32 * w + lane;
-          m[w] = e < n ? masks[e] : 0u;
+          x[w] = e < n ? masks[e] : 0u;
         }
+      };
+      read(0, m);
+      for (int i = 0; i < ntiles; ++i) {
+        read(i + 1, m1);
         const int ms = i % kMaskStages;
-        if (i >= kMaskStages && !__all_sync(0xFFFFFFFFu, bar_wait(&mempty[ms], ((i / kMaskStages) & 1) ^ 1))) break;
+        if (i >= kMaskStages && !wait_all(&mempty[ms], ((i / kMaskStages) & 1) ^ 1)) break;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t mine = 0;
-          for (int g = 0; g < tp.G; ++g) {
+#pragma unroll
+          for (int g = 0; g < 16; ++g) {  // tokens past G have no bits
             const uint32_t bits = __ballot_sync(0xFFFFFFFFu, (m[w] >> g) & 1u);
             if (lane == g) mine = bits;
           }
-          if (lane < tp.G) maskrow[(ms * 16 + lane) * 4 + w] = mine;
+          if (lane < 16) maskrow[(ms * 16 + lane) * 4 + w] = mine;
+          m[w] = m1[w];
         }
         __syncwarp();
         if (lane == 0) bar_arrive(&mfull[ms]);
       }
-    } else if (warp == 8 && lane == 0 && ntiles > 0 && bar_wait(qfull, 0)) {
-      // ---- MMA issuer: S of a tile before P V of the one before it
+    } else if (warp == 8 && ntiles > 0 && wait_all(qfull, 0)) {
+      // ---- MMA warp: S of a tile before P V of the one before it.  The whole
+      // warp walks the tiles, so that addresses and descriptors stay in uniform
+      // registers, and one elected lane issues.
       fence_after();
       bool ok = true;
+      const uint64_t kdesc = sdesc(sb + kOffK, 16), vdesc = sdesc(sb + kOffV, kBlk);
       auto pv = [&](int j) {
         const int vs = j % kVStages;
-        if (!bar_wait(&vfull[vs], (j / kVStages) & 1)) return false;
-        if (!bar_wait(&pfull[j & 1], (j >> 1) & 1)) return false;
+        if (!wait_all(&vfull[vs], (j / kVStages) & 1)) return false;
+        if (!wait_all(&pfull[j & 1], (j >> 1) & 1)) return false;
         fence_after();
-        mma_pv(tmem + kTmemO, tmem + (j & 1) * 128, sb + kOffV + vs * 2 * kBlk, j > 0);
-        mma_commit(&pvdone[j & 1]);
-        mma_commit(&vempty[vs]);
+        const uint64_t v = vdesc + (uint32_t)((vs * 2 * kBlk) >> 4);
+        if (elect_one()) {
+          if (j == 0)
+            mma_pv<false>(tmem + kTmemO, tmem, v);
+          else
+            mma_pv<true>(tmem + kTmemO, tmem + (j & 1) * 128, v);
+          mma_commit(&pvdone[j & 1]);
+          mma_commit(&vempty[vs]);
+        }
+        __syncwarp();
         return true;
       };
       for (int i = 0; i < ntiles && ok; ++i) {
         const int st = i & 1;
-        if (!bar_wait(&kfull[st], (i >> 1) & 1)) break;
-        if (i >= 2 && !bar_wait(&pvdone[st], ((i >> 1) & 1) ^ 1)) break;
+        if (!wait_all(&kfull[st], (i >> 1) & 1)) break;
+        if (i >= 2 && !wait_all(&pvdone[st], ((i >> 1) & 1) ^ 1)) break;
         fence_after();
-        mma_qk(tmem + st * 128, tmem + kTmemQ, sb + kOffK + st * 2 * kBlk);
-        mma_commit(&sfull[st]);
-        mma_commit(&kempty[st]);
+        if (elect_one()) {
+          mma_qk(tmem + st * 128, tmem + kTmemQ, kdesc + (uint32_t)((st * 2 * kBlk) >> 4));
+          mma_commit(&sfull[st]);
+          mma_commit(&kempty[st]);
+        }
+        __syncwarp();
         if (i >= 1) ok = pv(i - 1);
       }
       if (ok) pv(ntiles - 1);
@@ -517,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
     }
     for (int i = 0; i < ntiles; ++i) {
       const int ss = i & 1;
-      const bool okw = __all_sync(0xFFFFFFFFu, bar_wait(&sfull[ss], (i >> 1) & 1));
+      const bool okw = wait_all(&sfull[ss], (i >> 1) & 1);
       fence_after();
       uint32_t sc[2][32];
       if (okw) {
@@ -525,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
         for (int c = 0; c < 2; ++c) tld32(lane_base + ss * 128 + 64 * hf + 32 * c, sc[c]);
         tld_wait();
       }
-      __all_sync(0xFFFFFFFFu, bar_wait(&mfull[i % kMaskStages], (i / kMaskStages) & 1));
+      wait_all(&mfull[i % kMaskStages], (i / kMaskStages) & 1);
       uint32_t words[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -608,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
         weights(m_used == -INFINITY ? 0.f : m_used, false);
         if (__any_sync(0xFFFFFFFFu, alpha != 1.f) && i >= 1) {
           // rescale this half of the row of O once the previous P V is done
-          __all_sync(0xFFFFFFFFu, bar_wait(&pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1));
+          wait_all(&pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1);
           fence_after();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -627,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
       bar_arrive(&pfull[ss]);
     }
     if (ntiles > 0) {
-      done = __all_sync(0xFFFFFFFFu, bar_wait(&pvdone[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1));
+      done = wait_all(&pvdone[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1);
       fence_after();
     }
     // the row's sum: its halves' (added in the same order by both)
