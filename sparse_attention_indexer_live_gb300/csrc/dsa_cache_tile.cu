@@ -35,17 +35,20 @@ constexpr int kThreads = 640;  // warps 0-3 keys, 4-7 values, 8 MMA, 9 masks, 10
 // Registers (setmaxnreg): 96 a thread at launch; 256 x 80 + 128 x 32 + 256 x 144
 // = 61,440 = 640 x 96.
 constexpr int kLaunchRegs = 96;
-constexpr int kLoadRegs = 80;
-constexpr int kSideRegs = 32;
-constexpr int kSoftRegs = 144;
+constexpr int kLoadRegs = 64;
+constexpr int kSideRegs = 40;
+constexpr int kSoftRegs = 152;
 static_assert(256 * kLoadRegs + 128 * kSideRegs + 256 * kSoftRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr int kTile = 128;
 constexpr int kBlk = 128 * 128;  // one 128-row x 128-byte swizzled block
-constexpr int kKStages = 2, kVStages = 3, kMaskStages = 4;
+constexpr int kKStages = 2, kVStages = 2, kMaskStages = 4;
+constexpr int kRaw = 4;                      // tiles of codes and scales in flight or in use
+constexpr int kRawBytes = 128 * (64 + 64 + 16 + 16);
 constexpr int kOffK = 0;
 constexpr int kOffV = kOffK + kKStages * 2 * kBlk;
-constexpr int kOffMask = kOffV + kVStages * 2 * kBlk;            // [stage][token][4 words]
+constexpr int kOffRaw = kOffV + kVStages * 2 * kBlk;
+constexpr int kOffMask = kOffRaw + kRaw * kRawBytes;            // [stage][token][4 words]
 constexpr int kOffValid = kOffMask + kMaskStages * 16 * 4 * 4;   // [stage][4 words]
 constexpr int kOffXch = kOffValid + kMaskStages * 4 * 4;         // [parity][half][row]
 constexpr int kOffBars = kOffXch + 2 * 2 * 128 * 4;
@@ -89,9 +92,9 @@ __device__ __forceinline__ void bar_arrive(uint64_t* b) {
 __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(su32(b)), "r"(parity), "r"(kSuspendNs)
+      : "r"(su32(b)), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -101,7 +104,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
   if (bar_try(b, parity)) return true;
   if (*(volatile int*)&s_abort) return false;
   const long long t0 = clock64();
-  while (!bar_try(b, parity)) {
+  while (true) {
+    // the clock and the flag are looked at now and then: a poll is a few
+    // instructions, and they are other warps' issue slots
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (bar_try(b, parity)) return true;
     if (clock64() - t0 > kWaitCycles) {
       *(volatile int*)&s_abort = 1;
       atomicExch(&g_cache_attn_error, 1);
@@ -109,7 +117,6 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
     }
     if (*(volatile int*)&s_abort) return false;
   }
-  return true;
 }
 // All lanes of the warp wait.
 __device__ __forceinline__ bool wait_all(uint64_t* b, uint32_t parity) {
@@ -256,6 +263,15 @@ __device__ __forceinline__ float2 q_pair(uint32_t w) {
   if (kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   return f16x2_f32(w);
 }
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+// 16 bytes of src, or zeros (src not read)
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
 // Whether one of two e4m3 bytes is a NaN, and the pair with zeros for those.
 __device__ __forceinline__ bool has_nan(uint32_t s) { return (s & 0x7F) == 0x7F || (s & 0x7F00) == 0x7F00; }
 __device__ __forceinline__ uint32_t without_nan(uint32_t s) {
@@ -277,8 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
   uint64_t* qfull = bars;                   // Q in TMEM (softmax)
   uint64_t* kfull = qfull + 1;              // [2] key tile expanded (its 4 warps)
   uint64_t* kempty = kfull + kKStages;      // [2] S of that tile done (MMA commit)
-  uint64_t* vfull = kempty + kKStages;      // [3] value tile expanded
-  uint64_t* vempty = vfull + kVStages;      // [3] P V of that tile done
+  uint64_t* vfull = kempty + kKStages;      // [2] value tile expanded
+  uint64_t* vempty = vfull + kVStages;      // [2] P V of that tile done
   uint64_t* mfull = vempty + kVStages;      // [4] valid words (and token masks) written
   uint64_t* mempty = mfull + kMaskStages;   // [4] read (softmax warps)
   uint64_t* sfull = mempty + kMaskStages;   // [2] S in its TMEM buffer
@@ -339,9 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
   if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     // ---- loaders: keys (warps 0-3) and values (4-7), 32 rows of a tile each.
-    // Lane l looks up row l's record; lanes r, r + 8, r + 16 and r + 24 expand
-    // 32 dims each of rows r, 8 + r, ... (a phase of eight lanes then stores one
-    // chunk of eight rows, on eight different banks).
+    // Lane l looks up row l's record; lanes r, r + 8, r + 16 and r + 24 copy and
+    // expand 32 dims each of rows r, 8 + r, ... (a phase of eight lanes then
+    // stores one chunk of eight rows, on eight different banks).  Codes and
+    // scales of kRaw - 1 tiles ahead are on their way into shared memory, lookups
+    // of two more in registers.
     const bool is_k = warp < 4;
     const int w4 = warp & 3;
     const int r8 = lane & 7, quarter = lane >> 3;
@@ -358,48 +376,67 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
       const uint32_t slot = ((uint32_t)page << p.shift) + (key & ((1u << p.shift) - 1));
       return slot * p.kv_heads + kvh;
     };
-    uint4 code[4];
-    uint32_t sk[4], sv[4];  // scale pairs of this lane's 32 dims
+    // raw stages: 64 bytes of codes a row, 16-byte pieces swizzled by the row's
+    // pair so that eight rows' pieces lie on different banks; 16 of scales
+    const uint32_t raw_code = sb + kOffRaw + (is_k ? 0 : 8192) + (32 * w4 + r8) * 64 + ((quarter ^ (r8 >> 1 & 3)) << 4);
+    const uint32_t raw_scale = sb + kOffRaw + 16384 + (is_k ? 0 : 2048) + 32 * w4 * 16;
     const uint8_t* code_from = p.cache + (is_k ? 0 : kRecV) + 16 * quarter;
-    const uint8_t* scale_from = p.cache + kRecKs + 2 * quarter;
-    auto load = [&](int q, uint32_t mine) {
-      const uint32_t r = __shfl_sync(0xFFFFFFFFu, mine, 8 * q + r8);
-      code[q] = make_uint4(0, 0, 0, 0);
-      sk[q] = sv[q] = 0;
-      if (r != kNoRecord) {
-        const uint64_t off = (uint64_t)r * kRec;
-        code[q] = __ldg(reinterpret_cast<const uint4*>(code_from + off));
-        if (is_k) sk[q] = __ldg(reinterpret_cast<const uint16_t*>(scale_from + off));
-        sv[q] = __ldg(reinterpret_cast<const uint16_t*>(scale_from + off + 8));
-      }
-    };
-    const int key0 = key_of(0), key1 = key_of(1);
-    int key2 = key_of(2);
-    const int page0 = page_of(key0), page1 = page_of(key1);
-    const uint32_t rec0 = record_of(key0, page0);
-    uint32_t have = __ballot_sync(0xFFFFFFFFu, rec0 != kNoRecord);  // this tile's rows with a record
+    uint32_t have[kRaw];  // rows with a record, of the tiles in flight
+    auto copy = [&](int slot, uint32_t mine) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) load(q, rec0);
-    uint32_t next = record_of(key1, page1);
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t x = __shfl_sync(0xFFFFFFFFu, mine, 8 * q + r8);
+        cp16_or_zero(raw_code + slot * kRawBytes + 8 * q * 64, code_from + (x == kNoRecord ? 0 : (uint64_t)x * kRec),
+                     x != kNoRecord);
+      }
+      cp16_or_zero(raw_scale + slot * kRawBytes + lane * 16,
+                   p.cache + kRecKs + (mine == kNoRecord ? 0 : (uint64_t)mine * kRec), mine != kNoRecord);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int key[kRaw + 1], page[kRaw];
+#pragma unroll
+    for (int j = 0; j <= kRaw; ++j) key[j] = key_of(j);
+#pragma unroll
+    for (int j = 0; j < kRaw; ++j) page[j] = page_of(key[j]);
+#pragma unroll
+    for (int j = 0; j < kRaw - 1; ++j) {
+      const uint32_t x = record_of(key[j], page[j]);
+      have[j] = __ballot_sync(0xFFFFFFFFu, x != kNoRecord);
+      copy(j, x);
+    }
+    int key_a = key[kRaw - 1], page_a = page[kRaw - 1], key_b = key[kRaw];
     const uint32_t dst0 = sb + (is_k ? kOffK : kOffV) + (32 * w4 + r8) * 128;
     uint32_t chunk[4];  // offsets of this lane's four 16-byte chunks in a row
 #pragma unroll
     for (int j = 0; j < 4; ++j) chunk[j] = sw_off(r8, 4 * quarter + j) - r8 * 128;
     for (int i = 0; i < ntiles; ++i) {
       const int st = i % (is_k ? kKStages : kVStages), use = i / (is_k ? kKStages : kVStages);
-      const int key3 = key_of(i + 3);
-      const int page2 = page_of(key2);
+      const int slot = i % kRaw;
+      // tile i + kRaw - 1 into the stage read last; the lookups after it
+      const uint32_t x = record_of(key_a, page_a);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 2) : "memory");
+      __syncwarp();
+      copy((i + kRaw - 1) % kRaw, x);
+      const uint32_t next = __ballot_sync(0xFFFFFFFFu, x != kNoRecord);
+      key_a = key_b;
+      page_a = page_of(key_b);
+      key_b = key_of(i + kRaw + 1);
       if (use > 0 && !wait_all(is_k ? &kempty[st] : &vempty[st], (use & 1) ^ 1)) break;
       const uint32_t dst = dst0 + st * 2 * kBlk;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(raw_code + slot * kRawBytes + 8 * q * 64));
+        const uint32_t sa = raw_scale + slot * kRawBytes + (8 * q + r8) * 16 + 2 * quarter;
         // A NaN among a record's scales goes to the scores of the rows that
         // attend to it, through its keys: 0 times a NaN value would reach the
         // others of the tile.
-        uint32_t s = is_k ? (has_nan(sv[q]) ? 0x7F7Fu : sk[q]) : without_nan(sv[q]);
+        const uint32_t sv = lds16(sa + 8);
+        uint32_t s = is_k ? (has_nan(sv) ? 0x7F7Fu : lds16(sa)) : without_nan(sv);
         s = e4m3x2(s);
         const uint32_t lo = __byte_perm(s, 0, 0x1010), hi = __byte_perm(s, 0, 0x3232);
-        const uint32_t w[4] = {code[q].x, code[q].y, code[q].z, code[q].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t e[4];
@@ -407,25 +444,21 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
           const uint32_t f = j < 2 ? lo : hi;
           st16(dst + 8 * q * 128 + chunk[j], hmul2(e[0], f), hmul2(e[1], f), hmul2(e[2], f), hmul2(e[3], f));
         }
-        load(q, next);
       }
       // (this stage's last words were read: the softmax four tiles ago came
       // before the S two tiles ago, whose end this warp has waited for)
-      if (is_k && lane == 0) valid[(i % kMaskStages) * 4 + w4] = have;
+      if (is_k && lane == 0) valid[(i % kMaskStages) * 4 + w4] = have[0];
+#pragma unroll
+      for (int j = 0; j < kRaw - 2; ++j) have[j] = have[j + 1];
+      have[kRaw - 2] = next;
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
         bar_arrive(is_k ? &kfull[st] : &vfull[st]);
         if (is_k) bar_arrive(&mfull[i % kMaskStages]);
       }
-      have = __ballot_sync(0xFFFFFFFFu, next != kNoRecord);
-      next = record_of(key2, page2);
-      if (next != kNoRecord) {  // its lines on their way into L2
-        const uint8_t* line = p.cache + (uint64_t)next * kRec + (is_k ? 0 : kRec - 1);
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
-      }
-      key2 = key3;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
     if (warp == 9 && kUnion) {
@@ -446,13 +479,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
         if (i >= kMaskStages && !wait_all(&mempty[ms], ((i / kMaskStages) & 1) ^ 1)) break;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          uint32_t mine = 0;
+          // a transpose of 32 x 32 bits over the warp: lane g gets token g's word
+          uint32_t x = m[w];
 #pragma unroll
-          for (int g = 0; g < 16; ++g) {  // tokens past G have no bits
-            const uint32_t bits = __ballot_sync(0xFFFFFFFFu, (m[w] >> g) & 1u);
-            if (lane == g) mine = bits;
+          for (int s = 16; s > 0; s >>= 1) {
+            const uint32_t low = s == 16 ? 0x0000FFFFu : s == 8 ? 0x00FF00FFu : s == 4 ? 0x0F0F0F0Fu : s == 2 ? 0x33333333u : 0x55555555u;
+            const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, x, s);
+            x = lane & s ? (x & ~low) | (y >> s & low) : (x & low) | (y << s & ~low);
           }
-          if (lane < 16) maskrow[(ms * 16 + lane) * 4 + w] = mine;
+          if (lane < 16) maskrow[(ms * 16 + lane) * 4 + w] = x;
           m[w] = m1[w];
         }
         __syncwarp();
@@ -558,7 +593,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
       if (okw) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) tld32(lane_base + ss * 128 + 64 * hf + 32 * c, sc[c]);
-        tld_wait();
       }
       wait_all(&mfull[i % kMaskStages], (i / kMaskStages) & 1);
       uint32_t words[2];
@@ -571,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
         __syncwarp();
         if (lane == 0) bar_arrive(&mempty[i % kMaskStages]);
       }
+      tld_wait();
       // masked scores: -inf where the row does not attend to the position
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
