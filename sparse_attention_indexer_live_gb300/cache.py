@@ -45,30 +45,47 @@ def dsa_cache_bytes(cfg: dsa_cache_cfg) -> int:
 
 # ---------------------------------------------------------------------------
 # argument checks
+#
+# A decode step's kernels take a few microseconds, and so do checks made one
+# call a tensor: the functions below test what they need in line and leave the
+# reason to _refuse.
 
-def _need(name, t, dtype, numel, dev=None):
-    """t: a contiguous CUDA tensor of `dtype` on device `dev` (any, if None)
-    with at least `numel` elements.  Returns its device index."""
+def _refuse(name, t, dtype, numel, dev):
+    """Raise for `t`, which is not a contiguous CUDA tensor of `dtype` on
+    device `dev` (any, if None) with at least `numel` elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor (got device {t.device})")
-    at = t.get_device()
-    if dev is not None and at != dev:
-        raise ValueError(f"{name}: on cuda:{at}, the other tensors are on cuda:{dev}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, the other tensors are on cuda:{dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     if t.numel() < numel:
         raise ValueError(f"{name}: {t.numel()} elements, at least {numel} needed")
-    return at
+    raise ValueError(f"{name}: not usable")
+
+
+def _need(name, t, dtype, numel, dev):
+    """Check `t` (see _refuse; `dev` >= 0)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+            and t.numel() >= numel):
+        _refuse(name, t, dtype, numel, dev)
+
+
+def _device_of(name, t, dtype):
+    """The device of `t`, a contiguous CUDA tensor of `dtype`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+        _refuse(name, t, dtype, 0, None)
+    return t.get_device()
 
 
 def _cache(cfg, cache, dev):
-    if not isinstance(cfg, dsa_cache_cfg):
+    if type(cfg) is not dsa_cache_cfg:
         raise TypeError(f"cfg: expected a dsa_cache_cfg, got {type(cfg).__name__}")
-    need = max(cfg.pages, 0) * max(cfg.page_size, 0) * max(cfg.kv_heads, 0) * RECORD_BYTES
+    need = cfg.pages * cfg.page_size * cfg.kv_heads * RECORD_BYTES  # limits: the C ABI's
     _need("cache", cache, torch.uint8, need, dev)
 
 
@@ -82,21 +99,33 @@ def _row_type(name, t, types):
     return code
 
 
-def _call(fn, dev, stream, *args):
-    """fn(*args, stream) with `dev` current; the C ABI launches on the current device."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_functions = {}
+
+
+def _fn(name):
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(binding.load(), name)
+    return f
+
+
+def _call(name, dev, stream, *args):
+    """The library's `name`(*args, stream) with `dev` current: the C ABI launches on the current device."""
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(dev)
+        s = _raw_stream(dev)
     else:
         if stream.device.index != dev:
             raise ValueError(f"stream: of cuda:{stream.device.index}, the tensors are on cuda:{dev}")
         s = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    fn = _functions.get(name) or _fn(name)
+    if torch._C._cuda_getDevice() == dev:
         rc = fn(*args, s)
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, s)
     if rc:
-        raise binding.DsaSelectError(rc, fn.__name__)
+        raise binding.DsaSelectError(rc, name)
 
 
 # ---------------------------------------------------------------------------
@@ -109,9 +138,9 @@ def dsa_cache_plan(cfg: dsa_cache_cfg, lens, fresh, tables, held, free_pages, fr
     updated; first [R + 1], token_req, ends and slots [T] and status [4]
     written.  status[0] is one of the PLAN_* codes; a step that cannot be taken
     changes no state."""
-    if not isinstance(cfg, dsa_cache_cfg):
+    if type(cfg) is not dsa_cache_cfg:
         raise TypeError(f"cfg: expected a dsa_cache_cfg, got {type(cfg).__name__}")
-    dev = _need("lens", lens, _I32, 0)
+    dev = _device_of("lens", lens, _I32)
     R = lens.numel()
     _need("fresh", fresh, _I32, R, dev)
     _need("tables", tables, _I32, 0, dev)
@@ -126,7 +155,7 @@ def dsa_cache_plan(cfg: dsa_cache_cfg, lens, fresh, tables, held, free_pages, fr
     _need("ends", ends, _I32, T, dev)
     _need("slots", slots, _I32, T, dev)
     _need("status", status, _I32, 4, dev)
-    _call(binding.load().dsa_cache_plan, dev, stream, ctypes.byref(cfg), R, tables.shape[1], T, free_pages.numel(),
+    _call("dsa_cache_plan", dev, stream, ctypes.byref(cfg), R, tables.shape[1], T, free_pages.numel(),
           lens.data_ptr(), fresh.data_ptr(), tables.data_ptr(), held.data_ptr(), free_pages.data_ptr(),
           free_count.data_ptr(), first.data_ptr(), token_req.data_ptr(), ends.data_ptr(), slots.data_ptr(),
           status.data_ptr())
@@ -134,11 +163,11 @@ def dsa_cache_plan(cfg: dsa_cache_cfg, lens, fresh, tables, held, free_pages, fr
 
 def _strided_rows(name, t, T, H, dev):
     """[T, H, 128] rows whose heads and dims are packed; returns the token stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor (got device {t.device})")
     if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: must be a CUDA tensor (got device {t.device})")
         raise ValueError(f"{name}: on cuda:{t.get_device()}, the other tensors are on cuda:{dev}")
-    if t.dim() != 3 or t.shape[0] != T or t.shape[1] != H or t.shape[2] != _DIM:
+    if t.shape != (T, H, _DIM):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{T}, {H}, {_DIM}]")
     st = t.stride()
     if T and (st[2] != 1 or (H > 1 and st[1] != _DIM)):
@@ -156,12 +185,12 @@ def dsa_cache_write(cfg: dsa_cache_cfg, k, v, slots, cache, stream=None):
     code = _row_type("k", k, 3)
     if not isinstance(v, torch.Tensor) or v.dtype is not k.dtype:
         raise TypeError(f"v: expected a tensor of {k.dtype} like k")
-    dev = _need("slots", slots, _I32, 0)
+    dev = _device_of("slots", slots, _I32)
     _cache(cfg, cache, dev)
     T = slots.numel()
     ks = _strided_rows("k", k, T, cfg.kv_heads, dev)
     vs = _strided_rows("v", v, T, cfg.kv_heads, dev)
-    _call(binding.load().dsa_cache_write, dev, stream, ctypes.byref(cfg), T, code, k.data_ptr(), v.data_ptr(), ks, vs,
+    _call("dsa_cache_write", dev, stream, ctypes.byref(cfg), T, code, k.data_ptr(), v.data_ptr(), ks, vs,
           slots.data_ptr(), cache.data_ptr())
 
 
@@ -169,22 +198,23 @@ def dsa_cache_read(cfg: dsa_cache_cfg, cache, slots, k, v, stream=None):
     """Read the records slots [T] int32 names into k and v [T, kv_heads, 128]
     (bf16, f16 or f32); zeros for a slot outside the cache."""
     code = _row_type("k", k, 3)
-    dev = _need("slots", slots, _I32, 0)
+    dev = _device_of("slots", slots, _I32)
     _cache(cfg, cache, dev)
     T = slots.numel()
-    n = T * max(cfg.kv_heads, 0) * _DIM
+    n = T * cfg.kv_heads * _DIM
     _need("k", k, k.dtype, n, dev)
     _need("v", v, k.dtype, n, dev)
-    _call(binding.load().dsa_cache_read, dev, stream, ctypes.byref(cfg), T, code, cache.data_ptr(), slots.data_ptr(),
+    _call("dsa_cache_read", dev, stream, ctypes.byref(cfg), T, code, cache.data_ptr(), slots.data_ptr(),
           k.data_ptr(), v.data_ptr())
 
 
 def _attention_args(cfg, cache, q, idx, o, lse):
     code = _row_type("q", q, 2)
-    if q.dim() != 3 or q.shape[2] != _DIM:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected [tokens, heads, {_DIM}]")
-    T, H = q.shape[0], q.shape[1]
-    dev = _need("q", q, q.dtype, 0)
+    dev = _device_of("q", q, q.dtype)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != _DIM:
+        raise ValueError(f"q: shape {tuple(shape)}, expected [tokens, heads, {_DIM}]")
+    T, H = shape[0], shape[1]
     _cache(cfg, cache, dev)
     _need("idx", idx, _I32, 0, dev)
     if idx.dim() != 2 or idx.shape[0] != T:
@@ -204,9 +234,9 @@ def dsa_cache_attention(cfg: dsa_cache_cfg, cache, q, idx, token_req, tables, sc
     _need("tables", tables, _I32, 0, dev)
     if tables.dim() != 2:
         raise ValueError(f"tables: shape {tuple(tables.shape)}, expected [requests, pages per request]")
-    _call(binding.load().dsa_cache_attention, dev, stream, ctypes.byref(cfg), T, H, Kc, tables.shape[0],
-          tables.shape[1], code, cache.data_ptr(), q.data_ptr(), idx.data_ptr(), token_req.data_ptr(),
-          tables.data_ptr(), scale, o.data_ptr(), lse.data_ptr())
+    R, P = tables.shape
+    _call("dsa_cache_attention", dev, stream, ctypes.byref(cfg), T, H, Kc, R, P, code, cache.data_ptr(),
+          q.data_ptr(), idx.data_ptr(), token_req.data_ptr(), tables.data_ptr(), scale, o.data_ptr(), lse.data_ptr())
 
 
 def dsa_cache_attention_prompt_workspace(cfg: dsa_cache_cfg, q, idx) -> int:
@@ -226,7 +256,7 @@ def dsa_cache_attention_prompt(cfg: dsa_cache_cfg, cache, q, idx, table, scale: 
     code, T, H, Kc, dev = _attention_args(cfg, cache, q, idx, o, lse)
     _need("table", table, _I32, 0, dev)
     _need("workspace", workspace, torch.uint8, 0, dev)
-    _call(binding.load().dsa_cache_attention_prompt, dev, stream, ctypes.byref(cfg), T, H, Kc, table.numel(), code,
+    _call("dsa_cache_attention_prompt", dev, stream, ctypes.byref(cfg), T, H, Kc, table.numel(), code,
           cache.data_ptr(), q.data_ptr(), idx.data_ptr(), table.data_ptr(), scale, workspace.data_ptr(),
           workspace.numel(), o.data_ptr(), lse.data_ptr())
 
