@@ -619,25 +619,35 @@ int launch_staged(const AttendParams& p, int64_t ctas, int split, cudaStream_t s
   return ctas <= 2 * kSms ? launch_one<kNT, kBf16, 4>(p, split, s) : launch_one<kNT, kBf16, 2>(p, split, s);
 }
 
-#ifndef ATT_WARP_HEADS
-#define ATT_WARP_HEADS 16
-#endif
-constexpr int kMaxWarpHeads = ATT_WARP_HEADS;
+// CTAs of a row of this form: 8 heads a CTA, or 16.
+int64_t warp_units(const AttendParams& p) {
+  const int wide = p.n <= 8 ? 8 : 16;
+  return (int64_t)p.T * p.kv_heads * ((p.n + wide - 1) / wide);
+}
+
+// Whether tiles of 128 rows serve a call better.  They expand a record once for
+// all of a key/value head's query heads, this form once for every 16; but with
+// few CTAs this form splits further.  Lists of 2,048, this form against tiles:
+// 64 heads 8.8 against 12.7 us (1 token), 15.2 / 15.4 (16), 28.8 / 20.4 (64),
+// 92 / 54 (256); 24 heads 11.3 / 15.1 (16), 22.3 / 19.2 (64).
+bool wants_tiles(const AttendParams& p) { return p.n > 16 && warp_units(p) > 64; }
 
 int launch_attend(const AttendParams& p, int32_t dtype, cudaStream_t s) {
-  const int wide = p.n <= 8 ? 8 : 16;
-  const int64_t units = (int64_t)p.T * p.kv_heads * ((p.n + wide - 1) / wide);
-  // Rows are split while the CTAs run at once (4 an SM for 8 heads, 2 for 16)
-  // and every warp has a tile.  Measured: 96 rows of 8 heads over 2,176 entries
-  // 20.3 / 18.2 / 15.0 us in 1 / 2 / 4 CTAs a row; 256 of 16 heads 28.7 us
-  // whole, 44.9 in halves (a second wave).
+  const bool wide = p.n > 8;
+  const int64_t units = warp_units(p);
+  // Rows are split while the CTAs run at once (4 an SM for 8 heads, 2 for 16;
+  // clusters of 16 find room only while each CTA has an SM of its own) and every
+  // warp has a tile.  Measured, 2,048 entries: one row of 8 heads 16.3 / 13.2 /
+  // 8.9 / 7.1 / 6.4 us over 1 / 2 / 4 / 8 / 16 CTAs, 16 rows 8.4 us over 8 and
+  // 13.5 over 16, 96 rows (2,176) 20.3 / 18.2 / 15.0 over 1 / 2 / 4; 256 rows of
+  // 16 heads 28.7 us whole, 44.9 in halves (a second wave).
   int split = 1;
-  while (split < kMaxSplit && units * split * 2 <= (wide == 8 ? 4 : 2) * kSms &&
+  while (split < kMaxSplit && units * split * 2 <= (split * 2 == 16 ? 1 : wide ? 2 : 4) * kSms &&
          (int64_t)p.Kc >= (int64_t)split * 2 * kTile * kWarps)
     split *= 2;
   const int64_t ctas = units * split;
   if (ctas >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
-  if (wide == 8)
+  if (!wide)
     return dtype == DSA_BF16 ? launch_staged<1, true>(p, ctas, split, s) : launch_staged<1, false>(p, ctas, split, s);
   return dtype == DSA_BF16 ? launch_staged<2, true>(p, ctas, split, s) : launch_staged<2, false>(p, ctas, split, s);
 }
@@ -663,7 +673,7 @@ int dsa_cache_attention(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads,
     return DSA_ERR_INVALID_ARG;
   const AttendParams p = make_params(cfg, tokens, heads, select, requests, table_width, cache, q, idx, token_req, tables,
                                      scale, o, lse);
-  if (p.n > kMaxWarpHeads) return dsa_cache_tile(p, nullptr, dtype == DSA_BF16, (cudaStream_t)stream);
+  if (wants_tiles(p)) return dsa_cache_tile(p, nullptr, dtype == DSA_BF16, (cudaStream_t)stream);
   return launch_attend(p, dtype, (cudaStream_t)stream);
 }
 

@@ -68,7 +68,6 @@ constexpr uint32_t kIdescPV = kIdesc | (1u << 16);
 constexpr int kMaxSplit = 8;
 constexpr uint32_t kNoRecord = 0xFFFFFFFFu;
 constexpr long long kWaitCycles = 4000000000ll;  // ~2 s
-constexpr uint32_t kSuspendNs = 1000000;  // a try of a wait may sleep this long: less polling
 
 __device__ int g_cache_attn_error;
 __shared__ int s_abort;
@@ -860,9 +859,13 @@ int dsa_cache_tile(const AttendParams& p, const uint8_t* records, bool bf16, cud
   if (tp.negate) tp.a.scale_log2 = -p.scale_log2;
   const int64_t units = (int64_t)((p.T + tp.G - 1) / tp.G) * p.kv_heads;
   // Few units: their tiles go over a cluster while every CTA has an SM of its
-  // own and two tiles or more (of a list as long as one token's).
+  // own and four tiles or more (of a list as long as one token's).  Clusters of
+  // eight such CTAs, an SM each, find room for about half of the SMs: 64 heads,
+  // 2,048 entries, 4 tokens 15.4 / 13.0 us over 4 / 8 CTAs, 16 tokens 15.4 / 23.8.
   int split = 1;
-  while (split < kMaxSplit && units * split * 2 <= kSms && (int64_t)p.Kc >= (int64_t)split * 4 * kTile) split *= 2;
+  while (split < kMaxSplit && units * split * 2 <= (split * 2 == 8 ? kSms / 2 : kSms) &&
+         (int64_t)p.Kc >= (int64_t)split * 4 * kTile)
+    split *= 2;
   if (units * split >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
   if (records)
     return bf16 ? launch_tile<true, true>(tp, units, split, stream) : launch_tile<false, true>(tp, units, split, stream);

@@ -261,8 +261,9 @@ class _Case:
         req = self.req if form == "decode" else np.zeros(self.T, int)
         tables = self.tables if form == "decode" else self.tables[:1]
         c = self.cfg
-        wo, wl, vmax, amax = ref.attention(self.cache, self.page, self.q.double().numpy(), self.idx, req, tables,
-                                           self.scale, c.k_shift, c.v_shift, distinct=form != "decode")
+        with np.errstate(invalid="ignore"):
+            wo, wl, vmax, amax = ref.attention(self.cache, self.page, self.q.double().numpy(), self.idx, req, tables,
+                                               self.scale, c.k_shift, c.v_shift, distinct=form != "decode")
         o, lse = o[:self.T], lse[:self.T]
         empty = np.isneginf(wl)
         assert (lse[empty] == -np.inf).all() and (o[empty] == 0).all(), "rows without a position"
@@ -287,6 +288,11 @@ SHAPES = [  # T, H, kv_heads, select, page, context, type
     (2, 96, 2, 70, 1, 150, "f16"), (9, 7, 7, 50, 4, 90, "bf16"), (40, 8, 1, 300, 64, 1000, "bf16"),
     (33, 20, 1, 31, 128, 200, "bf16"), (1, 8, 1, 5000, 64, 6000, "f16"), (2, 34, 2, 700, 16, 1000, "bf16"),
     (200, 8, 2, 40, 16, 64, "f16"), (1, 128, 1, 2048, 64, 3000, "f16"), (300, 16, 1, 64, 64, 300, "bf16"),
+    (6, 8, 1, 3000, 64, 4000, "bf16"), (20, 16, 1, 2100, 16, 2500, "f16"),
+    # more than 16 heads a key/value head and many tokens: tiles of 128 rows, whole and split over 2 and 4 CTAs
+    (70, 17, 1, 1, 16, 40, "bf16"), (34, 24, 1, 129, 16, 300, "f16"), (40, 64, 1, 130, 8, 500, "bf16"),
+    (160, 32, 1, 65, 64, 300, "f16"), (20, 128, 1, 2050, 64, 3000, "bf16"), (34, 96, 2, 1100, 16, 1500, "f16"),
+    (9, 128, 1, 1030, 32, 1200, "bf16"),
 ]
 
 
@@ -295,9 +301,9 @@ def test_attention(T, H, KV, Kc, page, ctx, dtype):
     _Case(T, H, KV, Kc, page=page, ctx=ctx, dtype=dtype, seed=T + H + Kc).device().launch().check()
 
 
-@pytest.mark.parametrize("H,KV", [(8, 1), (16, 2), (64, 1), (128, 1)])
-def test_attention_edge_rows(H, KV):
-    c = _Case(14, H, KV, 150, page=16, ctx=200, R=5, sort=False, seed=H)
+@pytest.mark.parametrize("H,KV,T", [(8, 1, 14), (16, 2, 14), (64, 1, 14), (64, 1, 40), (128, 1, 14)])
+def test_attention_edge_rows(H, KV, T):
+    c = _Case(T, H, KV, 150, page=16, ctx=200, R=5, sort=False, seed=H)
     c.idx[0] = -1                                   # nothing
     c.idx[1, :] = -1
     c.idx[1, 149] = 199                             # one position, in the last entry
@@ -314,12 +320,14 @@ def test_attention_edge_rows(H, KV):
     c.device().launch().check()
 
 
-@pytest.mark.parametrize("H", [8, 64])
-def test_attention_ignores_what_is_not_selected(H):
-    # NaN and infinite queries elsewhere, NaN scales and -1 pages in places no row lists
-    c = _Case(6, H, 1, 60, page=8, ctx=80, R=2, seed=3)
+@pytest.mark.parametrize("H,T", [(8, 6), (64, 6), (128, 12)])
+def test_attention_ignores_what_is_not_selected(H, T):
+    # NaN scales in places no row lists
+    c = _Case(T, H, 1, 60, page=8, ctx=80, R=2, seed=3)
+    c.idx[:, 40:] = -1
+    c.idx[:, :40] = np.where(c.idx[:, :40] % 8 == 7, -1, c.idx[:, :40])
     listed = np.zeros((c.pages, 8), bool)
-    for t in range(6):
+    for t in range(T):
         p = c.idx[t][c.idx[t] >= 0]
         listed[c.tables[c.req[t]][p // 8], p % 8] = True
     assert not listed.all()
@@ -327,15 +335,16 @@ def test_attention_ignores_what_is_not_selected(H):
     o, _ = c.device().launch().check()
     assert np.isfinite(o).all()
     # a NaN record makes the rows that list it NaN, no others
-    p = int(c.idx[2][5])
+    p = int(c.idx[2][c.idx[2] >= 0][5])
     c.cache[c.tables[c.req[2], p // 8], p % 8, 0, 128:] = 0x7F
-    c.device().launch().check()
+    o, _ = c.device().launch().check()
+    assert np.isnan(o[2]).all() and np.isfinite(o).any()
 
 
-@pytest.mark.parametrize("H", [8, 24, 128])
-def test_attention_query_magnitudes(H):
+@pytest.mark.parametrize("H,T", [(8, 7), (24, 7), (128, 12)])
+def test_attention_query_magnitudes(H, T):
     rng = np.random.default_rng(8)
-    q = rng.standard_normal((7, H, 128))
+    q = rng.standard_normal((T, H, 128))
     q[0] *= 1e30
     q[1] *= 1e-30
     q[2] = 0
@@ -343,14 +352,15 @@ def test_attention_query_magnitudes(H):
     q[4, 0] = np.inf
     q[5, H - 1, 3] = np.nan
     q[6] *= 2.0 ** -120
-    c = _Case(7, H, 1, 90, ctx=120, q=q, seed=9)
+    c = _Case(T, H, 1, 90, ctx=120, q=q, seed=9)
     # scores of 1e30 leave one position; infinite and NaN queries give NaN rows
     c.device().launch()
     c.torch.cuda.synchronize()
     got_o, got_l = c.o.double().cpu().numpy(), c.lse.double().cpu().numpy()
     assert np.isnan(got_l[4, 0]) and np.isnan(got_o[4, 0]).all() and np.isnan(got_l[5, H - 1])
     assert np.isfinite(got_o[4, 1:]).all() and np.isfinite(got_o[5, :H - 1]).all()
-    wo, wl, vmax, _ = ref.attention(c.cache, c.page, c.q.double().numpy(), c.idx, c.req, c.tables, c.scale)
+    with np.errstate(invalid="ignore"):
+        wo, wl, vmax, _ = ref.attention(c.cache, c.page, c.q.double().numpy(), c.idx, c.req, c.tables, c.scale)
     assert np.abs(got_o[0] - wo[0]).max() <= 2.0 ** -7 * vmax[0].max()
     assert (np.abs(got_l[0] - wl[0]) <= 2.0 ** -16 * np.abs(wl[0])).all()
     for x in (c.q, c.idx, c.req):
@@ -360,8 +370,8 @@ def test_attention_query_magnitudes(H):
 
 def test_attention_scores_that_rise():
     # keys that grow with the position: the running maximum moves in every tile
-    for H in (8, 128):
-        c = _Case(2, H, 1, 3000, page=64, ctx=4000, R=2, dtype="f16", seed=1)
+    for T, H in ((2, 8), (2, 128), (20, 128)):
+        c = _Case(T, H, 1, 3000, page=64, ctx=4000, R=2, dtype="f16", seed=1)
         pos = np.zeros((c.pages, 64))
         for r in range(2):
             for j in range(c.tables.shape[1]):
@@ -375,8 +385,13 @@ def test_attention_scores_that_rise():
 
 
 def test_attention_shifts():
-    for H in (8, 64):
-        _Case(4, H, 1, 100, ctx=150, k_shift=5, v_shift=-7, seed=4).device().launch().check()
+    for T, H in ((4, 8), (4, 64), (20, 64)):
+        _Case(T, H, 1, 100, ctx=150, k_shift=5, v_shift=-7, seed=4).device().launch().check()
+        # no scale: every weight is the same; a negative one
+        for scale in (0.0, -0.05):
+            c = _Case(T, H, 1, 100, ctx=150, seed=4)
+            c.scale = scale
+            c.device().launch().check()
 
 
 def test_attention_past_32_bits():
@@ -394,21 +409,22 @@ def test_attention_past_32_bits():
     tables = torch.arange(pages, dtype=torch.int32, device=DEV)[None, :].contiguous()
     rec = ref.pack(kv[0].astype(np.float64), kv[1].astype(np.float64))
     for H in (8, 128):
-        q = torch.randn(2, H, 128, generator=torch.Generator().manual_seed(1)).bfloat16()
-        idx = torch.from_numpy(np.stack([slots, slots]).astype(np.int32)).to(DEV)
-        o = torch.empty(2, H, 128, dtype=torch.bfloat16, device=DEV)
-        lse = torch.empty(2, H, device=DEV)
-        dsa.dsa_cache_attention(cfg, cache, q.to(DEV), idx, torch.zeros(2, dtype=torch.int32, device=DEV), tables,
+        T = 2 if H == 8 else 10
+        q = torch.randn(T, H, 128, generator=torch.Generator().manual_seed(1)).bfloat16()
+        idx = torch.from_numpy(np.tile(slots.astype(np.int32), (T, 1))).to(DEV)
+        o = torch.empty(T, H, 128, dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty(T, H, device=DEV)
+        dsa.dsa_cache_attention(cfg, cache, q.to(DEV), idx, torch.zeros(T, dtype=torch.int32, device=DEV), tables,
                                 128 ** -0.5, o, lse)
         small = rec.reshape(1, 64, 1, 144)
-        wo, wl, vmax, amax = ref.attention(small, 64, q.double().numpy(), np.tile(np.arange(64), (2, 1)), [0, 0],
+        wo, wl, vmax, amax = ref.attention(small, 64, q.double().numpy(), np.tile(np.arange(64), (T, 1)), [0] * T,
                                            np.zeros((1, 1), int), 128 ** -0.5)
         assert (np.abs(lse.double().cpu().numpy() - wl) <= 2.0 ** -16 * amax + 2.0 ** -22 * (8 + np.abs(wl))).all()
         assert (np.abs(o.double().cpu().numpy() - wo) <= 2.0 ** -8 * np.abs(wo) + 2.0 ** -10 * vmax[..., None]).all()
 
 
 def test_attention_repeats_bit_for_bit():
-    for H, T in ((8, 1), (8, 100), (128, 2)):
+    for H, T in ((8, 1), (8, 100), (128, 2), (128, 20)):
         c = _Case(T, H, 1, 900, page=64, ctx=1500, seed=5).device().launch()
         o, lse = c.o.clone(), c.lse.clone()
         for _ in range(3):
@@ -463,6 +479,8 @@ PROMPTS = [  # T, H, kv_heads, select, page, context, type
     (1, 8, 1, 1, 16, 30, "bf16"), (1, 16, 1, 200, 16, 300, "f16"), (37, 8, 1, 64, 64, 500, "bf16"),
     (29, 16, 1, 100, 8, 333, "f16"), (40, 8, 1, 300, 16, 6000, "bf16"), (17, 32, 2, 130, 32, 400, "bf16"),
     (50, 16, 2, 257, 64, 700, "f16"), (130, 8, 1, 33, 128, 4000, "f16"),
+    # few groups: their tiles over 8, 4 and 2 CTAs
+    (20, 8, 1, 2100, 64, 5000, "bf16"), (100, 16, 1, 1100, 64, 3000, "f16"), (300, 16, 2, 520, 64, 2000, "bf16"),
 ]
 
 
@@ -498,6 +516,9 @@ def test_prompt_rising_and_odd_queries():
     q[4] = 0
     q[5] *= 1e-6
     _Case(20, 8, 1, 90, ctx=120, q=q, R=1, k_shift=4, v_shift=3, seed=9).device().launch("prompt").check("prompt")
+    c = _Case(20, 8, 1, 90, ctx=120, R=1, seed=9)
+    c.scale = -0.05
+    c.device().launch("prompt").check("prompt")
 
 
 def test_prompt_nan_stays_in_its_rows():
