@@ -1,5 +1,11 @@
 // dsa_cache.cu -- the paged 4-bit key/value cache: page plans from request
 // lengths, rows stored and rows read back (declared in include/dsa_select.h).
+//
+// Plans are latency: one launch, a prefix sum over the requests and a look-up a
+// token; 2.8 us for 96 tokens of 48 requests, 7 us for 66,016 tokens of 512.
+// Rows are bandwidth: 65,536 tokens x 2 heads of f16 stored and read back in 28.7
+// us (6.0 TB/s, 0.88 of the measured copy), 262,144 rows read as bf16 in 30.5 us
+// (5.7 TB/s, 0.84).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>

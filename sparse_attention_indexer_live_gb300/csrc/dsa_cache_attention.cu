@@ -1,5 +1,22 @@
-// dsa_cache_attention.cu -- sparse attention over the paged 4-bit cache
-// (declared in include/dsa_select.h).
+// dsa_cache_attention.cu -- sparse attention over the paged 4-bit cache: the form
+// for single tokens, and the entry points of both forms (declared in
+// include/dsa_select.h; dsa_cache_tile.cu has the other form).
+//
+// For token t and head h of key/value head h / n, over the positions j of t's
+// list: s_j = scale q . k_j, o = sum_j 2^(c s_j - m) v_j / sum_j 2^(c s_j - m)
+// with c = log2 e and m a running maximum.  A list is one pass: 144 bytes a
+// position, of which every scale and code is expanded once for 8 (or 16) heads.
+//
+// What bounds it: a batch (512 tokens x 4 key/value heads x 8 heads, 1,001
+// entries) takes 75 us against 45 us for its bytes at the measured copy rate:
+// 290 instructions a 16 positions (134 of them conversions and scalings) keep
+// the schedulers 77 % busy in the loop, and a third of a CTA's life is the
+// look-ups before and the join after it.  One token (6.4 us) is launch, three
+// dependent reads (entry, page, record), two tiles a warp and the cluster's join.
+// Measured: records by cp.async.bulk, one 144-byte copy a lane, 122 us against
+// 100 for 16-byte cp.async pieces; look-ups one tile at a time 95 us against 79
+// in batches of eight; 3 / 4 CTAs an SM 108 / 96 us, 5 with their spills no
+// faster than 4; q's fragments in shared memory no difference.
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -20,13 +37,12 @@ __device__ __forceinline__ void store(void* o, int64_t i, float x) {
     static_cast<__half*>(o)[i] = __float2half_rn(x);
 }
 
-// ---------------------------------------------------------------------------
-// the form for single tokens: one CTA, or a cluster of them, per token,
-// key/value head and 8 or 16 of its query heads
+// One CTA of four warps, or a cluster of them, per token, key/value head and 8
+// or 16 of its query heads.
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 32;        // positions a warp takes at a time
+constexpr int kTile = 32;        // positions a warp takes at a time (two products of 16 rows)
 constexpr int kStageBytes = kTile * kRec;
 constexpr int kBatch = 8;        // tiles of a warp whose entries are looked up at once
 constexpr int kListTiles = 16;   // tiles of a warp listed at once
@@ -635,14 +651,15 @@ bool wants_tiles(const AttendParams& p) { return p.n > 16 && warp_units(p) > 64;
 int launch_attend(const AttendParams& p, int32_t dtype, cudaStream_t s) {
   const bool wide = p.n > 8;
   const int64_t units = warp_units(p);
-  // Rows are split while the CTAs run at once (4 an SM for 8 heads, 2 for 16;
-  // clusters of 16 find room only while each CTA has an SM of its own) and every
-  // warp has a tile.  Measured, 2,048 entries: one row of 8 heads 16.3 / 13.2 /
-  // 8.9 / 7.1 / 6.4 us over 1 / 2 / 4 / 8 / 16 CTAs, 16 rows 8.4 us over 8 and
-  // 13.5 over 16, 96 rows (2,176) 20.3 / 18.2 / 15.0 over 1 / 2 / 4; 256 rows of
-  // 16 heads 28.7 us whole, 44.9 in halves (a second wave).
+  // Rows are split while the clusters run at once (3.5 CTAs an SM for 8 heads, 2
+  // for 16; clusters of 16 find room only while each CTA has an SM of its own)
+  // and every warp has a tile.  Measured, 2,048 entries: one row of 8 heads 16.3 /
+  // 13.2 / 8.9 / 7.1 / 6.4 us over 1 / 2 / 4 / 8 / 16 CTAs, 16 rows 8.4 us over 8
+  // and 13.5 over 16, 96 rows (2,176) 20.3 / 18.2 / 15.0 over 1 / 2 / 4, 152 rows
+  // 21.6 over 2 and 29.4 over 4 (a second wave); 256 rows of 16 heads 28.7 us
+  // whole, 44.9 in halves.
   int split = 1;
-  while (split < kMaxSplit && units * split * 2 <= (split * 2 == 16 ? 1 : wide ? 2 : 4) * kSms &&
+  while (split < kMaxSplit && units * split * 2 <= (split * 2 == 16 ? 2 : wide ? 4 : 7) * kSms / 2 &&
          (int64_t)p.Kc >= (int64_t)split * 2 * kTile * kWarps)
     split *= 2;
   const int64_t ctas = units * split;

@@ -7,17 +7,26 @@
 // and the positions its list.
 //
 //   * eight loader warps gather the tile's records and expand their codes to
-//     f16 key and value tiles in the 128B-swizzled layout the tensor cores
-//     read: four lanes a record, codes of the next tile in registers while this
-//     one's are expanded, records after that on their way into L2;
-//   * one thread issues tcgen05.mma (f16, fp32 accumulators in TMEM):
-//     S = Q K^T with Q in TMEM as the A operand, into one of two buffers, and
-//     O += P V with P in TMEM over the scores it came from and V as an N-major
-//     operand;
-//   * two softmax warpgroups, each half of the columns of every row, as in
-//     dsa_attention.cu; weights are rounded to f16.
+//     f16 key and value tiles (exactly) in the 128B-swizzled layout the tensor
+//     cores read: four lanes a record; codes and scales reach a shared-memory
+//     ring by cp.async, four tiles deep, so that no register waits for them;
+//   * one warp issues tcgen05.mma (f16, fp32 accumulators in TMEM): S = Q K^T
+//     with Q in TMEM as the A operand, into one of two buffers, and O += P V with
+//     P in TMEM over the scores it came from and V as an N-major operand;
+//   * two softmax warpgroups, each half of the columns of every row: one pass
+//     against a running maximum that moves rarely; weights are rounded to f16,
+//     the sum takes them unrounded.
 // Splits of a row's tiles over a cluster are joined through distributed shared
 // memory.  Every mbarrier wait is bounded by a clock limit.
+//
+// What bounds it: neither HBM (2,048 tokens of 8 heads over a million positions:
+// 90 MB read in 52 us) nor the tensor cores (16 products of 128 x 128 x 16 a
+// tile, 68 cycles each at the peak rate: 1,090 of a tile's 3,500 cycles), but
+// the softmax's chain within a tile -- TMEM load, masks, maximum, exponentials,
+// TMEM store, each 150 to 900 cycles -- at five warps a scheduler.  Measured for
+// the same chunk, with the union's 18 us: 71.2 us; codes through registers in
+// place of the ring 79.9; sixteen softmax warps of 32 columns 77.6; a warpgroup a
+// tile with an O each 74.2, with tiles of 64 and four S buffers 73.0.
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -32,8 +41,8 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int kThreads = 640;  // warps 0-3 keys, 4-7 values, 8 MMA, 9 masks, 10-11 idle, 12-19 softmax
-// Registers (setmaxnreg): 96 a thread at launch; 256 x 80 + 128 x 32 + 256 x 144
-// = 61,440 = 640 x 96.
+// Registers (setmaxnreg): 96 a thread at launch; 256 x 64 + 128 x 40 + 256 x 152
+// = 60,416 of 640 x 96 = 61,440.
 constexpr int kLaunchRegs = 96;
 constexpr int kLoadRegs = 64;
 constexpr int kSideRegs = 40;

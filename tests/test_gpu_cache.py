@@ -472,6 +472,43 @@ def test_attention_in_a_graph_and_on_a_stream():
         c.check()
 
 
+def test_calls_on_two_streams_at_once():
+    """Nothing is shared between calls: decode and prompt calls that overlap in
+    time, each with its own outputs (and workspace), give what they give alone."""
+    torch, dsa = _mods()
+    a = _Case(64, 8, 1, 600, page=16, ctx=900, R=1, seed=41).device()
+    b = _Case(40, 64, 1, 500, page=32, ctx=800, R=3, seed=42).device()
+    c = _Case(64, 16, 1, 500, page=32, ctx=800, R=1, seed=43).device()
+    ws = torch.empty(dsa.dsa_cache_attention_prompt_workspace(c.cfg, c.d["q"], c.d["idx"]), dtype=torch.uint8,
+                     device=DEV)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, x, form in zip(streams, (a, b, c), ("decode", "decode", "prompt")):
+            with torch.cuda.stream(s):
+                x.launch(form, ws)
+    a.check()
+    b.check()
+    c.check("prompt")
+
+
+def test_explicit_stream():
+    torch, dsa = _mods()
+    c = _Case(5, 8, 1, 60, ctx=100, seed=44).device()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    d = c.d
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(2000000)  # what the call must queue behind
+        late = d["q"].clone()
+        d["q"].zero_()
+        d["q"].copy_(late)
+    dsa.dsa_cache_attention(c.cfg, d["cache"], d["q"], d["idx"], d["req"], d["tables"], c.scale, c.o[:5], c.lse[:5],
+                            stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    c.check()
+
+
 # ---------------------------------------------------------------------------
 # the prompt form
 
