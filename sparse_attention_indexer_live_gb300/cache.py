@@ -22,6 +22,7 @@ PLAN_OK, PLAN_NO_PAGES, PLAN_TABLE_WIDTH, PLAN_TOKENS, PLAN_BAD_LENGTHS = range(
 _DIM = 128
 _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _I32 = torch.int32
+_Tensor = torch.Tensor
 
 
 class dsa_cache_cfg(ctypes.Structure):
@@ -70,7 +71,7 @@ def _refuse(name, t, dtype, numel, dev):
 
 def _need(name, t, dtype, numel, dev):
     """Check `t` (see _refuse; `dev` >= 0)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
             and t.numel() >= numel):
         _refuse(name, t, dtype, numel, dev)
 
@@ -100,6 +101,7 @@ def _row_type(name, t, types):
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _functions = {}
 
 
@@ -119,7 +121,7 @@ def _call(name, dev, stream, *args):
             raise ValueError(f"stream: of cuda:{stream.device.index}, the tensors are on cuda:{dev}")
         s = stream.cuda_stream
     fn = _functions.get(name) or _fn(name)
-    if torch._C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         rc = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -142,19 +144,32 @@ def dsa_cache_plan(cfg: dsa_cache_cfg, lens, fresh, tables, held, free_pages, fr
         raise TypeError(f"cfg: expected a dsa_cache_cfg, got {type(cfg).__name__}")
     dev = _device_of("lens", lens, _I32)
     R = lens.numel()
-    _need("fresh", fresh, _I32, R, dev)
-    _need("tables", tables, _I32, 0, dev)
+    try:
+        T = token_req.numel()
+        fine = (
+            fresh.dtype is _I32 and fresh.get_device() == dev and fresh.is_contiguous() and fresh.numel() >= R
+            and tables.dtype is _I32 and tables.get_device() == dev and tables.is_contiguous()
+            and held.dtype is _I32 and held.get_device() == dev and held.is_contiguous() and held.numel() >= R
+            and free_pages.dtype is _I32 and free_pages.get_device() == dev and free_pages.is_contiguous()
+            and free_count.dtype is _I32 and free_count.get_device() == dev and free_count.numel() >= 1
+            and first.dtype is _I32 and first.get_device() == dev and first.is_contiguous() and first.numel() > R
+            and token_req.dtype is _I32 and token_req.get_device() == dev and token_req.is_contiguous()
+            and ends.dtype is _I32 and ends.get_device() == dev and ends.is_contiguous() and ends.numel() >= T
+            and slots.dtype is _I32 and slots.get_device() == dev and slots.is_contiguous() and slots.numel() >= T
+            and status.dtype is _I32 and status.get_device() == dev and status.is_contiguous()
+            and status.numel() >= 4)
+    except AttributeError:
+        fine = False
+    if not fine:  # one by one, for the reason
+        _need("token_req", token_req, _I32, 0, dev)
+        for name, x, n in (("fresh", fresh, R), ("tables", tables, 0), ("held", held, R),
+                           ("free_pages", free_pages, 0), ("free_count", free_count, 1), ("first", first, R + 1),
+                           ("ends", ends, token_req.numel()), ("slots", slots, token_req.numel()),
+                           ("status", status, 4)):
+            _need(name, x, _I32, n, dev)
+        raise ValueError("a tensor changed while it was checked")
     if tables.dim() != 2 or tables.shape[0] != R:
         raise ValueError(f"tables: shape {tuple(tables.shape)}, expected [{R}, pages per request]")
-    _need("held", held, _I32, R, dev)
-    _need("free_pages", free_pages, _I32, 0, dev)
-    _need("free_count", free_count, _I32, 1, dev)
-    _need("first", first, _I32, R + 1, dev)
-    _need("token_req", token_req, _I32, 0, dev)
-    T = token_req.numel()
-    _need("ends", ends, _I32, T, dev)
-    _need("slots", slots, _I32, T, dev)
-    _need("status", status, _I32, 4, dev)
     _call("dsa_cache_plan", dev, stream, ctypes.byref(cfg), R, tables.shape[1], T, free_pages.numel(),
           lens.data_ptr(), fresh.data_ptr(), tables.data_ptr(), held.data_ptr(), free_pages.data_ptr(),
           free_count.data_ptr(), first.data_ptr(), token_req.data_ptr(), ends.data_ptr(), slots.data_ptr(),
@@ -214,14 +229,15 @@ def _attention_args(cfg, cache, q, idx, o, lse):
     shape = q.shape
     if len(shape) != 3 or shape[2] != _DIM:
         raise ValueError(f"q: shape {tuple(shape)}, expected [tokens, heads, {_DIM}]")
-    T, H = shape[0], shape[1]
+    T, H, _ = shape
     _cache(cfg, cache, dev)
     _need("idx", idx, _I32, 0, dev)
-    if idx.dim() != 2 or idx.shape[0] != T:
-        raise ValueError(f"idx: shape {tuple(idx.shape)}, expected [{T}, select]")
+    shape = idx.shape
+    if len(shape) != 2 or shape[0] != T:
+        raise ValueError(f"idx: shape {tuple(shape)}, expected [{T}, select]")
     _need("o", o, q.dtype, T * H * _DIM, dev)
     _need("lse", lse, torch.float32, T * H, dev)
-    return code, T, H, idx.shape[1], dev
+    return code, T, H, shape[1], dev
 
 
 def dsa_cache_attention(cfg: dsa_cache_cfg, cache, q, idx, token_req, tables, scale: float, o, lse, stream=None):
@@ -232,9 +248,10 @@ def dsa_cache_attention(cfg: dsa_cache_cfg, cache, q, idx, token_req, tables, sc
     code, T, H, Kc, dev = _attention_args(cfg, cache, q, idx, o, lse)
     _need("token_req", token_req, _I32, T, dev)
     _need("tables", tables, _I32, 0, dev)
-    if tables.dim() != 2:
-        raise ValueError(f"tables: shape {tuple(tables.shape)}, expected [requests, pages per request]")
-    R, P = tables.shape
+    shape = tables.shape
+    if len(shape) != 2:
+        raise ValueError(f"tables: shape {tuple(shape)}, expected [requests, pages per request]")
+    R, P = shape
     _call("dsa_cache_attention", dev, stream, ctypes.byref(cfg), T, H, Kc, R, P, code, cache.data_ptr(),
           q.data_ptr(), idx.data_ptr(), token_req.data_ptr(), tables.data_ptr(), scale, o.data_ptr(), lse.data_ptr())
 
