@@ -499,6 +499,7 @@ int dsa_cache_read(const dsa_cache_cfg* cfg, int32_t tokens, int32_t dtype, cons
  *   tables  int32 [requests, table_width]
  *   q, o    [tokens, heads, 128] of one type, DSA_BF16 or DSA_F16, 16-byte
  *           aligned;  lse  f32 [tokens, heads]
+ *   scale   of any sign; scale * 2^k_shift * log2(e) is finite in f32
  * Scores and sums are held in fp32; the softmax weights and the expanded rows
  * enter the products in f16 (the rows exactly), o is rounded once.  Few rows
  * split their lists over a cluster of CTAs; the order of every sum is fixed,

@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "dsa_cache.h"
 
@@ -554,10 +555,14 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
   }
 }
 
+// What a score is multiplied by to be an exponent of 2.
+float scale_log2_of(const dsa_cache_cfg* cfg, float scale) { return scale * pow2f(cfg->k_shift) * 1.4426950408889634f; }
+
 int check_attention(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads, int32_t select, int32_t requests,
-                    int32_t table_width, int32_t dtype) {
+                    int32_t table_width, int32_t dtype, float scale) {
   const int st = check_cache_cfg(cfg);
   if (st != DSA_OK) return st;
+  if (!std::isfinite(scale_log2_of(cfg, scale))) return DSA_ERR_INVALID_ARG;
   if (tokens < 0 || heads < 1 || select < 0 || requests < 0 || table_width < 0) return DSA_ERR_INVALID_ARG;
   if (dtype != DSA_BF16 && dtype != DSA_F16) return DSA_ERR_INVALID_ARG;
   if (heads % cfg->kv_heads) return DSA_ERR_INVALID_ARG;
@@ -588,7 +593,7 @@ AttendParams make_params(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads
   p.P = table_width;
   p.pages = cfg->pages;
   p.shift = log2_of(cfg->page_size);
-  p.scale_log2 = scale * pow2f(cfg->k_shift) * 1.4426950408889634f;
+  p.scale_log2 = scale_log2_of(cfg, scale);
   p.v_mul = pow2f(cfg->v_shift);
   return p;
 }
@@ -682,7 +687,7 @@ int dsa_cache_attention(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads,
                         const void* q, const int32_t* idx, const int32_t* token_req,
                         const int32_t* tables, float scale, void* o, float* lse,
                         struct CUstream_st* stream) {
-  const int st = check_attention(cfg, tokens, heads, select, requests, table_width, dtype);
+  const int st = check_attention(cfg, tokens, heads, select, requests, table_width, dtype, scale);
   if (st != DSA_OK) return st;
   if (tokens == 0) return DSA_OK;
   if (!q || !token_req || !o || !lse || !aligned16(cache, q, o)) return DSA_ERR_INVALID_ARG;
@@ -698,7 +703,7 @@ int dsa_cache_attention_prompt_workspace(const dsa_cache_cfg* cfg, int32_t token
                                          int32_t select, size_t* bytes) {
   if (!bytes) return DSA_ERR_INVALID_ARG;
   *bytes = 0;
-  const int st = check_attention(cfg, tokens, heads, select, 1, 0, DSA_BF16);
+  const int st = check_attention(cfg, tokens, heads, select, 1, 0, DSA_BF16, 1.0f);
   if (st != DSA_OK) return st;
   dsa_attention_cfg u = {tokens, heads / cfg->kv_heads, 0, kCacheDim, kCacheDim, select};
   return dsa_sparse_attention_workspace(&u, bytes);
@@ -709,7 +714,7 @@ int dsa_cache_attention_prompt(const dsa_cache_cfg* cfg, int32_t tokens, int32_t
                                const int32_t* idx, const int32_t* table, float scale, void* workspace,
                                size_t workspace_bytes, void* o, float* lse,
                                struct CUstream_st* stream) {
-  int st = check_attention(cfg, tokens, heads, select, 1, table_width, dtype);
+  int st = check_attention(cfg, tokens, heads, select, 1, table_width, dtype, scale);
   if (st != DSA_OK) return st;
   size_t need = 0;
   st = dsa_cache_attention_prompt_workspace(cfg, tokens, heads, select, &need);

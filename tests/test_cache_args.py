@@ -125,6 +125,15 @@ def test_abi_refusals(lib):
     assert pr(size=16) == 1 and pr(w=None) == 1 and pr(w=odd) == 1 and pr(t=2) == 1 and pr(tab=None) == 1
 
 
+@pytest.mark.parametrize("scale,k_shift", [(float("nan"), 0), (float("inf"), 0), (-float("inf"), 3), (1e30, 32)])
+def test_scale_has_to_be_finite(lib, scale, k_shift):
+    c = cfg(k_shift=k_shift)
+    r, p = ctypes.byref(c), VP(256)
+    assert lib.dsa_cache_attention(r, 0, 8, 4, 1, 1, 0, *[p] * 5, scale, p, p, None) == 1
+    assert lib.dsa_cache_attention_prompt(r, 0, 16, 4, 1, 0, *[p] * 4, scale, p, 1 << 20, p, p, None) == 1
+    assert lib.dsa_cache_attention(r, 0, 8, 4, 1, 1, 0, *[p] * 5, -0.1, p, p, None) == 0
+
+
 def test_binding_plan():
     R, P, T = 3, 4, 5
     good = dict(lens=i32(R), fresh=i32(R), tables=i32(R, P), held=i32(R), free=i32(7), count=i32(1), first=i32(R + 1),
