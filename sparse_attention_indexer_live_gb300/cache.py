@@ -308,15 +308,20 @@ class PagedCache:
         self.free_count = torch.full((1,), pages, **i32)
         self.first = torch.zeros(requests + 1, **i32)
         self.status = torch.zeros(4, **i32)
-        self.token_req = self.ends = self.slots = torch.empty(0, **i32)
+        self._maps = [torch.empty((3, 0), **i32)]
+        self.token_req, self.ends, self.slots = self._maps[0].unbind(0)
 
     def step(self, lens, fresh, tokens: int):
         """Plan a step of at most `tokens` tokens: lens [requests] int32 after
         it, the last fresh[r] of them new.  Sets token_req, ends and slots
-        [tokens], first and status."""
+        [tokens], first and status.  A graph that captured steps of one size
+        stays good when other sizes follow: steps share one memory, and what
+        they have outgrown is kept."""
         if tokens != self.slots.numel():
-            maps = torch.empty((3, tokens), dtype=_I32, device=self.tables.device)
-            self.token_req, self.ends, self.slots = maps.unbind(0)
+            if tokens > self._maps[-1].shape[1]:
+                room = max(tokens, 2 * self._maps[-1].shape[1])
+                self._maps.append(torch.empty((3, (room + 63) // 64 * 64), dtype=_I32, device=self.tables.device))
+            self.token_req, self.ends, self.slots = self._maps[-1][:, :tokens].unbind(0)
         dsa_cache_plan(self.cfg, lens, fresh, self.tables, self.held, self.free_pages, self.free_count, self.first,
                        self.token_req, self.ends, self.slots, self.status)
 

@@ -685,3 +685,54 @@ def test_a_decode_step_with_the_selection():
     with pytest.raises(RuntimeError, match="pages short"):
         c.step(dev([256, 256, 256, 0]), dev(np.zeros(R)), 0)
         c.ok()
+
+
+def test_captured_steps_of_several_sizes():
+    """A graph of a step stays good when larger steps follow: plan, store and
+    attend captured for 3 tokens, then run again after a step of 400."""
+    torch, dsa = _mods()
+    R, page = 3, 16
+    c = dsa.PagedCache(requests=R, pages=64, pages_per_request=32, page_size=page)
+    lens = torch.tensor([5, 9, 2], dtype=torch.int32, device=DEV)
+    fresh = lens.clone()
+    gen = torch.Generator(DEV).manual_seed(41)
+    c.step(lens, fresh, 16)
+    c.ok()
+    c.store(*torch.randn(2, 16, 1, 128, device=DEV, generator=gen).bfloat16().unbind(0))
+    kv = torch.randn(2, R, 1, 128, device=DEV, generator=gen).bfloat16()
+    q = torch.randn(R, 8, 128, device=DEV, generator=gen).bfloat16()
+    idx = torch.arange(16, device=DEV, dtype=torch.int32).repeat(R, 1)
+
+    def decode():
+        lens.add_(1)
+        c.step(lens, fresh, R)
+        c.store(kv[0], kv[1])
+        return c.attend(q, torch.where(idx < c.ends[:, None], idx, -1), 0.1)
+
+    fresh.fill_(1)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        decode()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = decode()
+    maps = (c.token_req, c.ends, c.slots)
+    # a step of another size, which outgrows the first one's memory, and rows
+    # of the same sizes as its maps to fall into memory that was given up
+    c.step(lens, torch.zeros_like(lens), 400)
+    c.ok()
+    others = [torch.full((n,), 12345, dtype=torch.int32, device=DEV) for n in (3, 9, 64, 192, 400) for _ in range(8)]
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+        assert maps[0].tolist() == [0, 1, 2] and maps[1].tolist() == lens.tolist()
+        assert all((x == 12345).all() for x in others)
+        # the same answer from a fresh call on the same state
+        c.step(lens, fresh, R)
+        c.ok()
+        assert torch.equal(c.slots, maps[2])
+        want = c.attend(q, torch.where(idx < c.ends[:, None], idx, -1), 0.1)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        c.step(lens, torch.zeros_like(lens), 400)
