@@ -1241,14 +1241,16 @@ int dsa_group_union(const dsa_attention_cfg* cfg, const int32_t* idx, void* work
   const int G = kRows / cfg->heads;
   const int groups = (cfg->tokens + G - 1) / G;
   const UnionShape U = union_shape(G, cfg->select, cfg->keys);
-  static bool configured = false;
-  if (!configured) {
+  static bool configured[64];  // by device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  if (dev >= 64 || !configured[dev]) {
     if (cudaFuncSetAttribute(union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kUSmemBudget) !=
         cudaSuccess) {
       cudaGetLastError();
       return DSA_ERR_CUDA;
     }
-    configured = true;
+    if (dev < 64) configured[dev] = true;
   }
   union_kernel<<<groups, kUThreads, U.smem, (cudaStream_t)stream>>>(
       idx, cfg->tokens, cfg->select, cfg->keys, G, static_cast<uint8_t*>(workspace), union_layout(G, cfg->select), U);
