@@ -21,7 +21,7 @@ PLAN_OK, PLAN_NO_PAGES, PLAN_TABLE_WIDTH, PLAN_TOKENS, PLAN_BAD_LENGTHS = range(
 
 _DIM = 128
 _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_I32 = torch.int32
+_I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
 _Tensor = torch.Tensor
 
 
@@ -87,7 +87,7 @@ def _cache(cfg, cache, dev):
     if type(cfg) is not dsa_cache_cfg:
         raise TypeError(f"cfg: expected a dsa_cache_cfg, got {type(cfg).__name__}")
     need = cfg.pages * cfg.page_size * cfg.kv_heads * RECORD_BYTES  # limits: the C ABI's
-    _need("cache", cache, torch.uint8, need, dev)
+    _need("cache", cache, _U8, need, dev)
 
 
 def _row_type(name, t, types):
@@ -198,13 +198,17 @@ def dsa_cache_write(cfg: dsa_cache_cfg, k, v, slots, cache, stream=None):
     """Store k and v [T, kv_heads, 128] (bf16, f16 or f32; any token stride) in
     4 bits at the records slots [T] int32 names; -1 stores nothing."""
     code = _row_type("k", k, 3)
-    if not isinstance(v, torch.Tensor) or v.dtype is not k.dtype:
+    if not isinstance(v, _Tensor) or v.dtype is not k.dtype:
         raise TypeError(f"v: expected a tensor of {k.dtype} like k")
     dev = _device_of("slots", slots, _I32)
     _cache(cfg, cache, dev)
-    T = slots.numel()
-    ks = _strided_rows("k", k, T, cfg.kv_heads, dev)
-    vs = _strided_rows("v", v, T, cfg.kv_heads, dev)
+    T, heads = slots.numel(), cfg.kv_heads
+    shape = (T, heads, _DIM)
+    if (k.get_device() == dev and v.get_device() == dev and k.shape == shape and v.shape == shape
+            and k.is_contiguous() and v.is_contiguous()):
+        ks = vs = heads * _DIM
+    else:
+        ks, vs = _strided_rows("k", k, T, heads, dev), _strided_rows("v", v, T, heads, dev)
     _call("dsa_cache_write", dev, stream, ctypes.byref(cfg), T, code, k.data_ptr(), v.data_ptr(), ks, vs,
           slots.data_ptr(), cache.data_ptr())
 
@@ -224,20 +228,37 @@ def dsa_cache_read(cfg: dsa_cache_cfg, cache, slots, k, v, stream=None):
 
 
 def _attention_args(cfg, cache, q, idx, o, lse):
-    code = _row_type("q", q, 2)
-    dev = _device_of("q", q, q.dtype)
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != _DIM:
-        raise ValueError(f"q: shape {tuple(shape)}, expected [tokens, heads, {_DIM}]")
-    T, H, _ = shape
+    """(type code, tokens, heads, select, device) of an attention call's tensors."""
+    if type(cfg) is not dsa_cache_cfg:
+        raise TypeError(f"cfg: expected a dsa_cache_cfg, got {type(cfg).__name__}")
+    dtype = q.dtype if isinstance(q, _Tensor) else None
+    code, dev = _ROW_TYPES.get(dtype, 99), -1
+    try:
+        T, H, D = q.shape
+        rows, Kc = idx.shape
+        dev = q.get_device()
+        if (code < 2 and dev >= 0 and D == _DIM and rows == T and q.is_contiguous()
+                and cache.dtype is _U8 and cache.get_device() == dev and cache.is_contiguous()
+                and cache.numel() >= cfg.pages * cfg.page_size * cfg.kv_heads * RECORD_BYTES
+                and idx.dtype is _I32 and idx.get_device() == dev and idx.is_contiguous()
+                and o.dtype is dtype and o.get_device() == dev and o.is_contiguous() and o.numel() >= T * H * _DIM
+                and lse.dtype is _F32 and lse.get_device() == dev and lse.is_contiguous() and lse.numel() >= T * H):
+            return code, T, H, Kc, dev
+    except (AttributeError, ValueError):
+        pass
+    # one by one, for the reason
+    _row_type("q", q, 2)
+    dev = _device_of("q", q, dtype)
+    if q.dim() != 3 or q.shape[2] != _DIM:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [tokens, heads, {_DIM}]")
+    T, H, _ = q.shape
     _cache(cfg, cache, dev)
     _need("idx", idx, _I32, 0, dev)
-    shape = idx.shape
-    if len(shape) != 2 or shape[0] != T:
-        raise ValueError(f"idx: shape {tuple(shape)}, expected [{T}, select]")
-    _need("o", o, q.dtype, T * H * _DIM, dev)
-    _need("lse", lse, torch.float32, T * H, dev)
-    return code, T, H, shape[1], dev
+    if idx.dim() != 2 or idx.shape[0] != T:
+        raise ValueError(f"idx: shape {tuple(idx.shape)}, expected [{T}, select]")
+    _need("o", o, dtype, T * H * _DIM, dev)
+    _need("lse", lse, _F32, T * H, dev)
+    raise ValueError("a tensor changed while it was checked")
 
 
 def dsa_cache_attention(cfg: dsa_cache_cfg, cache, q, idx, token_req, tables, scale: float, o, lse, stream=None):
@@ -272,7 +293,7 @@ def dsa_cache_attention_prompt(cfg: dsa_cache_cfg, cache, q, idx, table, scale: 
     idx rows strictly ascending, then -1; table [P] int32 the request's pages."""
     code, T, H, Kc, dev = _attention_args(cfg, cache, q, idx, o, lse)
     _need("table", table, _I32, 0, dev)
-    _need("workspace", workspace, torch.uint8, 0, dev)
+    _need("workspace", workspace, _U8, 0, dev)
     _call("dsa_cache_attention_prompt", dev, stream, ctypes.byref(cfg), T, H, Kc, table.numel(), code,
           cache.data_ptr(), q.data_ptr(), idx.data_ptr(), table.data_ptr(), scale, workspace.data_ptr(),
           workspace.numel(), o.data_ptr(), lse.data_ptr())
