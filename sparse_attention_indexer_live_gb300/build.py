@@ -1,13 +1,18 @@
 """Compile the sm_103a CUDA library in-tree (nvcc, no torch extension machinery).
 
 Output: sparse_attention_indexer_live_gb300/_build/libdsa_select.so, plus the
-ptxas resource report (registers, spills, shared memory) next to it.
+ptxas resource report (registers, spills, shared memory) next to it; and, where
+torch is installed, the module through which cache.py makes its ordinary calls
+(calls_path(): host code, for one Python and one torch).
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +24,7 @@ HEADERS = [os.path.join(INCLUDE, "dsa_select.h"), os.path.join(PKG, "csrc", "dsa
            os.path.join(PKG, "csrc", "dsa_cache.h")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libdsa_select.so")
+CALLS_SOURCE = os.path.join(PKG, "csrc", "cache_calls.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,21 +38,62 @@ def nvcc_path() -> str:
     return found
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+def calls_path() -> str | None:
+    """The module built from cache_calls.cpp (None without torch)."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+    return os.path.join(BUILD_DIR, f"cache_calls.torch{version}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def _older(target, sources) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(f) > t for f in SOURCES + HEADERS)
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(f) > t for f in sources)
+
+
+def stale() -> bool:
+    return _older(LIB_PATH, SOURCES + HEADERS)
+
+
+def _build_calls(target, cuda_home) -> None:
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    include = [INCLUDE, os.path.join(torch_dir, "include"),
+               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda_home, "include")]
+    tmp = f"{target}.tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{d}" for d in include), "-o", tmp, CALLS_SOURCE,
+           "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stderr[-4000:])
+    os.replace(tmp, target)
 
 
 def build(force: bool = False) -> str:
     """Compile every translation unit in parallel, then link the library."""
     from concurrent.futures import ThreadPoolExecutor
-    if not force and not stale():
+    calls = calls_path()
+    if calls and not force and not _older(calls, [CALLS_SOURCE, HEADERS[0]]):
+        calls = None
+    if not calls and not force and not stale():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = nvcc_path()
     pid = os.getpid()
+    with ThreadPoolExecutor(1) as other:
+        job = other.submit(_build_calls, calls, os.path.dirname(os.path.dirname(nvcc))) if calls else None
+        if force or stale():
+            _build_library(nvcc, pid)
+        if job:
+            job.result()
+    return LIB_PATH
+
+
+def _build_library(nvcc, pid) -> None:
+    from concurrent.futures import ThreadPoolExecutor
 
     def compile_one(src):
         obj = os.path.join(BUILD_DIR, os.path.basename(src) + f".{pid}.o")
@@ -70,7 +117,6 @@ def build(force: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError("nvcc link failed:\n" + res.stderr[-4000:])
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

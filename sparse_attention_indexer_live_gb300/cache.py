@@ -7,22 +7,32 @@ As in binding.py, every argument is checked here before a pointer reaches the
 C ABI: TypeError for a wrong type, ValueError for a wrong device, layout or
 size.  The work runs on the current stream of the tensors' own device unless a
 stream of that device is given.
+
+A decode step's kernels take a few microseconds, and so do a dozen tensors looked
+at from Python.  Once the library is loaded an ordinary call -- nothing wrong with
+it, the tensors on the current device, no stream given -- is checked and made by
+the module built from csrc/cache_calls.cpp (two plans 17 -> 5.7 us, an attention
+call 7.9 -> 2.8, a read 5.8 -> 2.6); what that returns None for is checked and made, or refused with
+the reason, here.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
 from . import binding
+from .build import calls_path
 
 RECORD_BYTES = 144
 PLAN_OK, PLAN_NO_PAGES, PLAN_TABLE_WIDTH, PLAN_TOKENS, PLAN_BAD_LENGTHS = range(5)
 
 _DIM = 128
 _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
-_Tensor = torch.Tensor
+_I32 = torch.int32
 
 
 class dsa_cache_cfg(ctypes.Structure):
@@ -46,10 +56,6 @@ def dsa_cache_bytes(cfg: dsa_cache_cfg) -> int:
 
 # ---------------------------------------------------------------------------
 # argument checks
-#
-# A decode step's kernels take a few microseconds, and so do checks made one
-# call a tensor: the functions below test what they need in line and leave the
-# reason to _refuse.
 
 def _refuse(name, t, dtype, numel, dev):
     """Raise for `t`, which is not a contiguous CUDA tensor of `dtype` on
@@ -71,7 +77,7 @@ def _refuse(name, t, dtype, numel, dev):
 
 def _need(name, t, dtype, numel, dev):
     """Check `t` (see _refuse; `dev` >= 0)."""
-    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
             and t.numel() >= numel):
         _refuse(name, t, dtype, numel, dev)
 
@@ -83,11 +89,15 @@ def _device_of(name, t, dtype):
     return t.get_device()
 
 
-def _cache(cfg, cache, dev):
+def _cfg(cfg):
     if type(cfg) is not dsa_cache_cfg:
         raise TypeError(f"cfg: expected a dsa_cache_cfg, got {type(cfg).__name__}")
+
+
+def _cache(cfg, cache, dev):
+    _cfg(cfg)
     need = cfg.pages * cfg.page_size * cfg.kv_heads * RECORD_BYTES  # limits: the C ABI's
-    _need("cache", cache, _U8, need, dev)
+    _need("cache", cache, torch.uint8, need, dev)
 
 
 def _row_type(name, t, types):
@@ -100,34 +110,53 @@ def _row_type(name, t, types):
     return code
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-_functions = {}
+_calls = None  # the module of ordinary calls, once the library is loaded
 
 
-def _fn(name):
-    f = _functions.get(name)
-    if f is None:
-        f = _functions[name] = getattr(binding.load(), name)
-    return f
+def _load_calls(functions=None, host=False):
+    """The module of ordinary calls, bound to the library's functions (or those
+    given, with tensors of the host in place of a device's)."""
+    path = calls_path()
+    if path is None or not os.path.exists(path):
+        raise OSError(f"{path} has not been built: run build()")
+    loader = importlib.machinery.ExtensionFileLoader("cache_calls", path)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("cache_calls", path, loader=loader))
+    loader.exec_module(m)
+    if functions is None:
+        L = binding.load()
+        functions = [getattr(L, "dsa_cache_" + n) for n in ("bytes", "plan", "write", "read", "attention",
+                                                            "attention_prompt")]
+    m.bind(dsa_cache_cfg, host, *(ctypes.cast(f, ctypes.c_void_p).value for f in functions))
+    return m
+
+
+def _made(rc, name):
+    """Whether the module of ordinary calls made the call (rc: None or a status)."""
+    if rc:
+        raise binding.DsaSelectError(rc, name)
+    return rc is not None
+
+
+def _count(name, n):
+    if n >= 1 << 31:
+        raise ValueError(f"{name}: {n} is more than 32 bits hold")
+    return n
 
 
 def _call(name, dev, stream, *args):
     """The library's `name`(*args, stream) with `dev` current: the C ABI launches on the current device."""
+    global _calls
     if stream is None:
-        s = _raw_stream(dev)
+        s = torch.cuda.current_stream(dev).cuda_stream
     else:
         if stream.device.index != dev:
             raise ValueError(f"stream: of cuda:{stream.device.index}, the tensors are on cuda:{dev}")
         s = stream.cuda_stream
-    fn = _functions.get(name) or _fn(name)
-    if _current_device() == dev:
-        rc = fn(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, s)
-    if rc:
-        raise binding.DsaSelectError(rc, name)
+    fn = getattr(binding.load(), name)
+    if _calls is None:
+        _calls = _load_calls()
+    with torch.cuda.device(dev):
+        binding._check(fn(*args, s), name)
 
 
 # ---------------------------------------------------------------------------
@@ -140,37 +169,23 @@ def dsa_cache_plan(cfg: dsa_cache_cfg, lens, fresh, tables, held, free_pages, fr
     updated; first [R + 1], token_req, ends and slots [T] and status [4]
     written.  status[0] is one of the PLAN_* codes; a step that cannot be taken
     changes no state."""
-    if type(cfg) is not dsa_cache_cfg:
-        raise TypeError(f"cfg: expected a dsa_cache_cfg, got {type(cfg).__name__}")
+    if stream is None and _calls and _made(
+            _calls.plan(cfg, lens, fresh, tables, held, free_pages, free_count, first, token_req, ends, slots, status),
+            "dsa_cache_plan"):
+        return
+    _cfg(cfg)
     dev = _device_of("lens", lens, _I32)
     R = lens.numel()
-    try:
-        T = token_req.numel()
-        fine = (
-            fresh.dtype is _I32 and fresh.get_device() == dev and fresh.is_contiguous() and fresh.numel() >= R
-            and tables.dtype is _I32 and tables.get_device() == dev and tables.is_contiguous()
-            and held.dtype is _I32 and held.get_device() == dev and held.is_contiguous() and held.numel() >= R
-            and free_pages.dtype is _I32 and free_pages.get_device() == dev and free_pages.is_contiguous()
-            and free_count.dtype is _I32 and free_count.get_device() == dev and free_count.numel() >= 1
-            and first.dtype is _I32 and first.get_device() == dev and first.is_contiguous() and first.numel() > R
-            and token_req.dtype is _I32 and token_req.get_device() == dev and token_req.is_contiguous()
-            and ends.dtype is _I32 and ends.get_device() == dev and ends.is_contiguous() and ends.numel() >= T
-            and slots.dtype is _I32 and slots.get_device() == dev and slots.is_contiguous() and slots.numel() >= T
-            and status.dtype is _I32 and status.get_device() == dev and status.is_contiguous()
-            and status.numel() >= 4)
-    except AttributeError:
-        fine = False
-    if not fine:  # one by one, for the reason
-        _need("token_req", token_req, _I32, 0, dev)
-        for name, x, n in (("fresh", fresh, R), ("tables", tables, 0), ("held", held, R),
-                           ("free_pages", free_pages, 0), ("free_count", free_count, 1), ("first", first, R + 1),
-                           ("ends", ends, token_req.numel()), ("slots", slots, token_req.numel()),
-                           ("status", status, 4)):
-            _need(name, x, _I32, n, dev)
-        raise ValueError("a tensor changed while it was checked")
+    _need("token_req", token_req, _I32, 0, dev)
+    T = token_req.numel()
+    for name, x, n in (("fresh", fresh, R), ("tables", tables, 0), ("held", held, R), ("free_pages", free_pages, 0),
+                       ("free_count", free_count, 1), ("first", first, R + 1), ("ends", ends, T), ("slots", slots, T),
+                       ("status", status, 4)):
+        _need(name, x, _I32, n, dev)
     if tables.dim() != 2 or tables.shape[0] != R:
         raise ValueError(f"tables: shape {tuple(tables.shape)}, expected [{R}, pages per request]")
-    _call("dsa_cache_plan", dev, stream, ctypes.byref(cfg), R, tables.shape[1], T, free_pages.numel(),
+    _call("dsa_cache_plan", dev, stream, ctypes.byref(cfg), _count("lens", R), _count("tables", tables.shape[1]),
+          _count("token_req", T), _count("free_pages", free_pages.numel()),
           lens.data_ptr(), fresh.data_ptr(), tables.data_ptr(), held.data_ptr(), free_pages.data_ptr(),
           free_count.data_ptr(), first.data_ptr(), token_req.data_ptr(), ends.data_ptr(), slots.data_ptr(),
           status.data_ptr())
@@ -197,18 +212,16 @@ def _strided_rows(name, t, T, H, dev):
 def dsa_cache_write(cfg: dsa_cache_cfg, k, v, slots, cache, stream=None):
     """Store k and v [T, kv_heads, 128] (bf16, f16 or f32; any token stride) in
     4 bits at the records slots [T] int32 names; -1 stores nothing."""
+    if stream is None and _calls and _made(_calls.write(cfg, k, v, slots, cache), "dsa_cache_write"):
+        return
     code = _row_type("k", k, 3)
-    if not isinstance(v, _Tensor) or v.dtype is not k.dtype:
+    if not isinstance(v, torch.Tensor) or v.dtype is not k.dtype:
         raise TypeError(f"v: expected a tensor of {k.dtype} like k")
     dev = _device_of("slots", slots, _I32)
     _cache(cfg, cache, dev)
-    T, heads = slots.numel(), cfg.kv_heads
-    shape = (T, heads, _DIM)
-    if (k.get_device() == dev and v.get_device() == dev and k.shape == shape and v.shape == shape
-            and k.is_contiguous() and v.is_contiguous()):
-        ks = vs = heads * _DIM
-    else:
-        ks, vs = _strided_rows("k", k, T, heads, dev), _strided_rows("v", v, T, heads, dev)
+    T = _count("slots", slots.numel())
+    ks = _strided_rows("k", k, T, cfg.kv_heads, dev)
+    vs = _strided_rows("v", v, T, cfg.kv_heads, dev)
     _call("dsa_cache_write", dev, stream, ctypes.byref(cfg), T, code, k.data_ptr(), v.data_ptr(), ks, vs,
           slots.data_ptr(), cache.data_ptr())
 
@@ -216,10 +229,12 @@ def dsa_cache_write(cfg: dsa_cache_cfg, k, v, slots, cache, stream=None):
 def dsa_cache_read(cfg: dsa_cache_cfg, cache, slots, k, v, stream=None):
     """Read the records slots [T] int32 names into k and v [T, kv_heads, 128]
     (bf16, f16 or f32); zeros for a slot outside the cache."""
+    if stream is None and _calls and _made(_calls.read(cfg, cache, slots, k, v), "dsa_cache_read"):
+        return
     code = _row_type("k", k, 3)
     dev = _device_of("slots", slots, _I32)
     _cache(cfg, cache, dev)
-    T = slots.numel()
+    T = _count("slots", slots.numel())
     n = T * cfg.kv_heads * _DIM
     _need("k", k, k.dtype, n, dev)
     _need("v", v, k.dtype, n, dev)
@@ -229,26 +244,8 @@ def dsa_cache_read(cfg: dsa_cache_cfg, cache, slots, k, v, stream=None):
 
 def _attention_args(cfg, cache, q, idx, o, lse):
     """(type code, tokens, heads, select, device) of an attention call's tensors."""
-    if type(cfg) is not dsa_cache_cfg:
-        raise TypeError(f"cfg: expected a dsa_cache_cfg, got {type(cfg).__name__}")
-    dtype = q.dtype if isinstance(q, _Tensor) else None
-    code, dev = _ROW_TYPES.get(dtype, 99), -1
-    try:
-        T, H, D = q.shape
-        rows, Kc = idx.shape
-        dev = q.get_device()
-        if (code < 2 and dev >= 0 and D == _DIM and rows == T and q.is_contiguous()
-                and cache.dtype is _U8 and cache.get_device() == dev and cache.is_contiguous()
-                and cache.numel() >= cfg.pages * cfg.page_size * cfg.kv_heads * RECORD_BYTES
-                and idx.dtype is _I32 and idx.get_device() == dev and idx.is_contiguous()
-                and o.dtype is dtype and o.get_device() == dev and o.is_contiguous() and o.numel() >= T * H * _DIM
-                and lse.dtype is _F32 and lse.get_device() == dev and lse.is_contiguous() and lse.numel() >= T * H):
-            return code, T, H, Kc, dev
-    except (AttributeError, ValueError):
-        pass
-    # one by one, for the reason
-    _row_type("q", q, 2)
-    dev = _device_of("q", q, dtype)
+    code = _row_type("q", q, 2)
+    dev = _device_of("q", q, q.dtype)
     if q.dim() != 3 or q.shape[2] != _DIM:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [tokens, heads, {_DIM}]")
     T, H, _ = q.shape
@@ -256,9 +253,9 @@ def _attention_args(cfg, cache, q, idx, o, lse):
     _need("idx", idx, _I32, 0, dev)
     if idx.dim() != 2 or idx.shape[0] != T:
         raise ValueError(f"idx: shape {tuple(idx.shape)}, expected [{T}, select]")
-    _need("o", o, dtype, T * H * _DIM, dev)
-    _need("lse", lse, _F32, T * H, dev)
-    raise ValueError("a tensor changed while it was checked")
+    _need("o", o, q.dtype, T * H * _DIM, dev)
+    _need("lse", lse, torch.float32, T * H, dev)
+    return code, _count("q", T), _count("q", H), _count("idx", idx.shape[1]), dev
 
 
 def dsa_cache_attention(cfg: dsa_cache_cfg, cache, q, idx, token_req, tables, scale: float, o, lse, stream=None):
@@ -266,13 +263,15 @@ def dsa_cache_attention(cfg: dsa_cache_cfg, cache, q, idx, token_req, tables, sc
     [T, Kc] int32 positions (below 0: unused) of request token_req[t], whose
     pages are tables[request]; writes o [T, H, 128] (q's type) and lse [T, H]
     f32."""
+    if stream is None and _calls and _made(
+            _calls.attention(cfg, cache, q, idx, token_req, tables, scale, o, lse), "dsa_cache_attention"):
+        return
     code, T, H, Kc, dev = _attention_args(cfg, cache, q, idx, o, lse)
     _need("token_req", token_req, _I32, T, dev)
     _need("tables", tables, _I32, 0, dev)
-    shape = tables.shape
-    if len(shape) != 2:
-        raise ValueError(f"tables: shape {tuple(shape)}, expected [requests, pages per request]")
-    R, P = shape
+    if tables.dim() != 2:
+        raise ValueError(f"tables: shape {tuple(tables.shape)}, expected [requests, pages per request]")
+    R, P = (_count("tables", n) for n in tables.shape)
     _call("dsa_cache_attention", dev, stream, ctypes.byref(cfg), T, H, Kc, R, P, code, cache.data_ptr(),
           q.data_ptr(), idx.data_ptr(), token_req.data_ptr(), tables.data_ptr(), scale, o.data_ptr(), lse.data_ptr())
 
@@ -291,10 +290,13 @@ def dsa_cache_attention_prompt(cfg: dsa_cache_cfg, cache, q, idx, table, scale: 
     """dsa_cache_attention for the tokens of one request's prompt chunk, 128 /
     (H / kv_heads) neighbours at a time over the union of their selections:
     idx rows strictly ascending, then -1; table [P] int32 the request's pages."""
+    if stream is None and _calls and _made(
+            _calls.prompt(cfg, cache, q, idx, table, scale, workspace, o, lse), "dsa_cache_attention_prompt"):
+        return
     code, T, H, Kc, dev = _attention_args(cfg, cache, q, idx, o, lse)
     _need("table", table, _I32, 0, dev)
-    _need("workspace", workspace, _U8, 0, dev)
-    _call("dsa_cache_attention_prompt", dev, stream, ctypes.byref(cfg), T, H, Kc, table.numel(), code,
+    _need("workspace", workspace, torch.uint8, 0, dev)
+    _call("dsa_cache_attention_prompt", dev, stream, ctypes.byref(cfg), T, H, Kc, _count("table", table.numel()), code,
           cache.data_ptr(), q.data_ptr(), idx.data_ptr(), table.data_ptr(), scale, workspace.data_ptr(),
           workspace.numel(), o.data_ptr(), lse.data_ptr())
 
