@@ -96,8 +96,10 @@ __global__ void __launch_bounds__(kPThreads) plan_kernel(const PlanParams p) {
   const int nthreads = blockDim.x, nwarps = nthreads / 32;
   const int gtid = rank * nthreads + tid, gthreads = nranks * nthreads;
   const int page_mask = (1 << p.shift) - 1;
+  let_next_start();
   if (tid == 0) s_bad = 0;
   __syncthreads();
+  wait_for_previous();
   // thread t takes requests [t * per, (t + 1) * per)
   const int per = (p.R + nthreads - 1) / nthreads;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
@@ -278,7 +280,7 @@ __device__ __forceinline__ At locate(const RowParams& p, int64_t row) {
   At a;
   a.tok = p.kv_shift >= 0 ? row >> p.kv_shift : row / p.kv_heads;
   a.head = (int32_t)(row - a.tok * p.kv_heads);
-  const int32_t s = row < p.rows ? __ldg(p.slots + a.tok) : -1;
+  const int32_t s = row < p.rows ? p.slots[a.tok] : -1;
   a.slot = s < p.nslots ? s : -1;
   return a;
 }
@@ -321,6 +323,8 @@ __global__ void __launch_bounds__(256) write_kernel(const RowParams p) {
   const int64_t row0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * (2 * kWriteUnroll) + (threadIdx.x >> 4 & 1);
   const int g = threadIdx.x & 7;
   const bool is_v = (threadIdx.x & 8) != 0;
+  let_next_start();
+  wait_for_previous();
   At at[kWriteUnroll];
 #pragma unroll
   for (int u = 0; u < kWriteUnroll; ++u) at[u] = locate(p, row0 + 2 * u);
@@ -404,6 +408,8 @@ __global__ void __launch_bounds__(256) read_kernel(const RowParams p, T* k, T* v
   constexpr int kSteps = sizeof(T) / 2;  // a record's steps of a warp
   const int64_t row0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * (kReadUnroll / kSteps);
   const int lane = threadIdx.x & 31;
+  let_next_start();
+  wait_for_previous();
   uint32_t w[kReadUnroll], sb[kReadUnroll];
 #pragma unroll
   for (int u = 0; u < kReadUnroll; ++u) {
@@ -412,9 +418,8 @@ __global__ void __launch_bounds__(256) read_kernel(const RowParams p, T* k, T* v
     w[u] = sb[u] = 0;
     if (at.slot >= 0) {
       const uint8_t* rec = record(p, at);
-      w[u] = kE == 8 ? __ldg(reinterpret_cast<const uint32_t*>(rec + e / 2))
-                     : __ldg(reinterpret_cast<const uint16_t*>(rec + e / 2));
-      sb[u] = __ldg(rec + kRecKs + e / 16);
+      w[u] = kE == 8 ? *reinterpret_cast<const uint32_t*>(rec + e / 2) : *reinterpret_cast<const uint16_t*>(rec + e / 2);
+      sb[u] = rec[kRecKs + e / 16];
     }
   }
 #pragma unroll
@@ -461,19 +466,14 @@ int launch_write(const RowParams& p, cudaStream_t s) {
   const int64_t blocks = (p.rows + 16 * kWriteUnroll - 1) / (16 * kWriteUnroll);
   const uintptr_t bits = (uintptr_t)p.k | (uintptr_t)p.v | (uintptr_t)(p.k_stride * (int64_t)sizeof(T)) |
                          (uintptr_t)(p.v_stride * (int64_t)sizeof(T));
-  if ((bits & 15) == 0)
-    write_kernel<T, true><<<(unsigned)blocks, 256, 0, s>>>(p);
-  else
-    write_kernel<T, false><<<(unsigned)blocks, 256, 0, s>>>(p);
-  return launched();
+  return launch_dependent((bits & 15) == 0 ? write_kernel<T, true> : write_kernel<T, false>, blocks, 256, 0, 0, s, p);
 }
 
 template <typename T>
 int launch_read(const RowParams& p, void* k, void* v, cudaStream_t s) {
   constexpr int kRows = 8 * kReadUnroll / (sizeof(T) / 2);  // of a block
   const int64_t blocks = (p.rows + kRows - 1) / kRows;
-  read_kernel<T><<<(unsigned)blocks, 256, 0, s>>>(p, static_cast<T*>(k), static_cast<T*>(v));
-  return launched();
+  return launch_dependent(read_kernel<T>, blocks, 256, 0, 0, s, p, static_cast<T*>(k), static_cast<T*>(v));
 }
 
 }  // namespace
@@ -537,23 +537,7 @@ int dsa_cache_plan(const dsa_cache_cfg* cfg, int32_t requests, int32_t table_wid
     cudaGetLastError();
     return DSA_ERR_CUDA;
   }
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)nctas);
-  lc.blockDim = dim3((unsigned)threads);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)nctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, kernel, p) != cudaSuccess) {
-    cudaGetLastError();
-    return DSA_ERR_CUDA;
-  }
-  return launched();
+  return launch_dependent(kernel, nctas, threads, smem, nctas, (cudaStream_t)stream, p);
 }
 
 int dsa_cache_write(const dsa_cache_cfg* cfg, int32_t tokens, int32_t dtype, const void* k, const void* v,

@@ -57,6 +57,41 @@ constexpr int kSms = 152;
 
 #ifdef __CUDACC__
 
+// The calls' kernels follow one another closely (a decode step is a plan, a
+// write and an attention, 2 to 15 us each), so each is launched as a
+// programmatic dependent of the one before it: its launch and set-up overlap that
+// one's end.  Every kernel lets its successor start at once and then waits for
+// its predecessor before it touches global memory, so a grid that has ended
+// means that all before it have.  What a predecessor may have written is read by
+// plain loads: the read-only path (__ldg) may be taken ahead of the wait.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch `kernel` on clusters of `cluster` CTAs, as above.
+template <typename... P, typename... A>
+int launch_dependent(void (*kernel)(P...), int64_t ctas, int threads, size_t smem, int cluster, cudaStream_t stream,
+                     const A&... args) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)ctas);
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = cluster > 0 ? 2 : 1;
+  if (cudaLaunchKernelEx(&lc, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return DSA_ERR_CUDA;
+  }
+  return launched();
+}
+
 // 2^e, |e| <= 126
 __host__ __device__ __forceinline__ float pow2f(int e) {
 #ifdef __CUDA_ARCH__

@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
   const int grp = unit / p.kv_heads;   // group of tokens, or token
   const int t0 = grp * tp.G;
 
+  let_next_start();
   if (threadIdx.x == 0) {
     s_abort = 0;
     bar_init(qfull, 256);
@@ -349,12 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
-  // The unions come from the launch before this one (a programmatic dependent
-  // launch: the set-up above overlaps its end).
-  if (kUnion) asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   const uint8_t* rec = kUnion ? tp.records + (int64_t)grp * tp.rec_bytes : nullptr;
   const int32_t* keys = kUnion ? reinterpret_cast<const int32_t*>(rec + tp.keys_off) : p.idx + (int64_t)grp * p.Kc;
-  const int req = kUnion || !p.token_req ? 0 : __ldg(p.token_req + grp);
+  const int req = kUnion || !p.token_req ? 0 : p.token_req[grp];
   const int n = kUnion ? *reinterpret_cast<const int32_t*>(rec) : (req >= 0 && req < p.R ? p.Kc : 0);
   // this CTA's tiles: rank, rank + split, ... of the row's
   const int all_tiles = (int)(((int64_t)n + kTile - 1) / kTile);
@@ -374,10 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
     const int32_t* table = p.tables + (int64_t)req * p.P;
     auto key_of = [&](int i) -> int {
       const int64_t e = ((int64_t)i * split + rank) * kTile + 32 * w4 + lane;
-      return e < n ? keys[e] : -1;  // a plain load: the launch before this one may write them while this one starts
+      return e < n ? keys[e] : -1;
     };
     auto page_of = [&](int key) -> int {
-      return key >= 0 && (key >> p.shift) < p.P ? __ldg(table + (key >> p.shift)) : -1;
+      return key >= 0 && (key >> p.shift) < p.P ? table[key >> p.shift] : -1;
     };
     auto record_of = [&](int key, int page) -> uint32_t {
       if (page < 0 || page >= p.pages) return kNoRecord;
@@ -565,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * kCacheDim + 64 * hf);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const uint4 x = real ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+        const uint4 x = real ? src[u] : make_uint4(0, 0, 0, 0);
         w[4 * u] = x.x;
         w[4 * u + 1] = x.y;
         w[4 * u + 2] = x.z;
@@ -830,25 +829,7 @@ int launch_tile(const TileParams& tp, int64_t units, int split, cudaStream_t s) 
     if (fa.numRegs < kLaunchRegs) return DSA_ERR_UNSUPPORTED;
     if (dev < 64) done[dev] = true;
   }
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)(units * split));
-  lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = kSmem;
-  lc.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = kUnion ? 2 : 1;
-  if (cudaLaunchKernelEx(&lc, kernel, tp) != cudaSuccess) {
-    cudaGetLastError();
-    return DSA_ERR_CUDA;
-  }
-  return launched();
+  return launch_dependent(kernel, units * split, kThreads, kSmem, split, s, tp);
 }
 
 }  // namespace
