@@ -258,18 +258,19 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const uint32_t e = (tile0 + (k + u) * tstep) * kTile + lane;
-      ent[u] = e < (uint32_t)p.Kc ? __ldg(idx + e) : -1;
+      ent[u] = e < (uint32_t)p.Kc ? idx[e] : -1;
     }
   };
+  wait_for_previous();
   entries(0);
-  const int req = p.token_req ? __ldg(p.token_req + tok) : 0;
+  const int req = p.token_req ? p.token_req[tok] : 0;
   uint4 qw[kNT][4];
 #pragma unroll
   for (int nt = 0; nt < kNT; ++nt) {
     const int h = nt * 8 + g;
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (row0 + h) * kCacheDim + 32 * t4);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) qw[nt][u] = h < nh ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < 4; ++u) qw[nt][u] = h < nh ? src[u] : make_uint4(0, 0, 0, 0);
   }
   const uint32_t ntiles = ((uint32_t)p.Kc + kTile - 1) / kTile;
   const uint32_t mine = req >= 0 && req < p.R && ntiles > tile0 ? (ntiles - tile0 + tstep - 1) / tstep : 0;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
   auto pages = [&]() {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
-      page[u] = ent[u] >= 0 && (ent[u] >> p.shift) < p.P ? __ldg(table + (ent[u] >> p.shift)) : -1;
+      page[u] = ent[u] >= 0 && (ent[u] >> p.shift) < p.P ? table[ent[u] >> p.shift] : -1;
   };
   if (mine) pages();
 
@@ -476,6 +477,9 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
       values16<kNT, 16 * kRec>(o, pf[1], v0 + vc + at, v1 + vc + at, v0 + vs + at, v1 + vs + at);
     }
   }
+  // (when CTAs share SMs, successors that are placed early share them unevenly:
+  // 96 rows of 8 heads 16.8 us against 14.6, one row 5.7 against 6.3)
+  if (gridDim.x <= kSms) let_next_start();
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();  // the ring is free
 
@@ -614,30 +618,18 @@ int launch_one(AttendParams p, int split, cudaStream_t s) {
     if (dev < 64) done[dev] = true;
   }
   p.chunks = (p.n + kNT * 8 - 1) / (kNT * 8);
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)((int64_t)p.T * p.kv_heads * p.chunks * split));
-  lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = attend_smem<kNT, kStages>(split > 1);
-  lc.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, kernel, p) != cudaSuccess) {
-    cudaGetLastError();
-    return DSA_ERR_CUDA;
-  }
-  return launched();
+  return launch_dependent(kernel, (int64_t)p.T * p.kv_heads * p.chunks * split, kThreads,
+                          attend_smem<kNT, kStages>(split > 1), split, s, p);
 }
 
-// Two CTAs an SM or fewer: four tiles of a warp in shared memory, so that the
-// loop does not wait for each tile's records; more: two, and twice the CTAs.
+// Up to 1.7 CTAs an SM: four tiles of a warp in shared memory, so that the loop
+// does not wait for each tile's records (2,048 entries of 8 heads: 32 rows over
+// 8 CTAs 8.1 against 8.5 us, 64 over 4 11.0 / 11.1; 16 heads 10.9 / 11.7 and
+// 14.5 / 15.5); more: two tiles, and room for twice the CTAs (38 rows over 8
+// 14.6 / 9.3, 80 over 4 20.9 / 13.1, 256 rows whole 28.8 / 27.5).
 template <int kNT, bool kBf16>
 int launch_staged(const AttendParams& p, int64_t ctas, int split, cudaStream_t s) {
-  return ctas <= 2 * kSms ? launch_one<kNT, kBf16, 4>(p, split, s) : launch_one<kNT, kBf16, 2>(p, split, s);
+  return 10 * ctas <= 17 * kSms ? launch_one<kNT, kBf16, 4>(p, split, s) : launch_one<kNT, kBf16, 2>(p, split, s);
 }
 
 // CTAs of a row of this form: 8 heads a CTA, or 16.
@@ -656,16 +648,18 @@ bool wants_tiles(const AttendParams& p) { return p.n > 16 && warp_units(p) > 64;
 int launch_attend(const AttendParams& p, int32_t dtype, cudaStream_t s) {
   const bool wide = p.n > 8;
   const int64_t units = warp_units(p);
-  // Rows are split while the clusters run at once (3.5 CTAs an SM for 8 heads, 2
-  // for 16; clusters of 16 find room only while each CTA has an SM of its own)
-  // and every warp has a tile.  Measured, 2,048 entries: one row of 8 heads 16.3 /
-  // 13.2 / 8.9 / 7.1 / 6.4 us over 1 / 2 / 4 / 8 / 16 CTAs, 16 rows 8.4 us over 8
-  // and 13.5 over 16, 96 rows (2,176) 20.3 / 18.2 / 15.0 over 1 / 2 / 4, 152 rows
-  // 21.6 over 2 and 29.4 over 4 (a second wave); 256 rows of 16 heads 28.7 us
-  // whole, 44.9 in halves.
+  // Rows are split while the clusters run at once and every warp has two tiles.
+  // Clusters of 16 find room only while each CTA has an SM of its own, the others
+  // up to 2.6 CTAs an SM, 3.3 for 8 heads in fours.  Measured, 2,048 entries of 8
+  // heads, over 1 / 2 / 4 / 8 CTAs: 32 rows 16.4 / 12.5 / 8.5 / 8.1 us, 48 rows
+  // 16.4 / 12.4 / 10.9 / 9.5, 64 16.6 / 12.5 / 11.0 / 11.5, 112 18.5 / 17.2 / 16.2 /
+  // 22.1, 136 21.0 / 18.9 / 19.2 / 25.0, 192 25.0 / 23.7 / 33.1, 256 27.5 / 30.1; of
+  // 16 heads: 48 rows 19.8 / 16.8 / 14.4 / 13.4, 96 23.5 / 21.8 / 18.8 / 26.8, 112
+  // 24.1 / 22.7 / 29.8, 192 29.7 / 29.8, 256 30.8 / 46.5.  Over 8 / 16: one row of 8
+  // heads 7.1 / 6.4, 16 rows 8.4 / 13.5.
+  auto room = [&](int c) { return (c == 16 ? 10 : c == 4 && !wide ? 33 : 26) * kSms / 10; };
   int split = 1;
-  while (split < kMaxSplit && units * split * 2 <= (split * 2 == 16 ? 2 : wide ? 4 : 7) * kSms / 2 &&
-         (int64_t)p.Kc >= (int64_t)split * 2 * kTile * kWarps)
+  while (split < kMaxSplit && units * split * 2 <= room(split * 2) && (int64_t)p.Kc >= (int64_t)split * 2 * kTile * kWarps)
     split *= 2;
   const int64_t ctas = units * split;
   if (ctas >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
