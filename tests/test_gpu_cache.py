@@ -736,3 +736,50 @@ def test_captured_steps_of_several_sizes():
         want = c.attend(q, torch.where(idx < c.ends[:, None], idx, -1), 0.1)
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
         c.step(lens, torch.zeros_like(lens), 400)
+
+
+@pytest.mark.parametrize("H,KV,R", [(8, 1, 5), (16, 2, 40), (64, 1, 70)])
+def test_calls_follow_one_another(H, KV, R):
+    """Steps whose calls depend on one another, enqueued without a pause, give
+    what they give when each call has ended before the next begins."""
+    torch, dsa = _mods()
+    page, P, K, steps = 16, 8, 48, 12
+    gen = torch.Generator(DEV).manual_seed(51)
+    kv = torch.randn(steps, 2, 2 * R, KV, 128, device=DEV, generator=gen).bfloat16()
+    q = torch.randn(steps, 2 * R, H, 128, device=DEV, generator=gen).bfloat16()
+    grow = torch.randint(0, 3, (steps, R), device=DEV, generator=gen, dtype=torch.int32)
+    pick = torch.randint(0, 1 << 20, (steps, 2 * R, K), device=DEV, generator=gen, dtype=torch.int32)
+
+    def run(pause):
+        wait = torch.cuda.synchronize if pause else lambda: None
+        c = dsa.PagedCache(requests=R, pages=R * P, pages_per_request=P, page_size=page, kv_heads=KV)
+        lens = torch.zeros(R, dtype=torch.int32, device=DEV)
+        got = []
+        for i in range(steps):
+            lens.add_(grow[i])
+            wait()
+            c.step(lens, grow[i], 2 * R)
+            wait()
+            c.store(kv[i, 0], kv[i, 1])
+            wait()
+            idx = torch.where(c.ends[:, None] > 0, pick[i] % c.ends.clamp(min=1)[:, None], -1)
+            wait()
+            got += c.attend(q[i], idx, 0.1)
+            wait()
+            got += c.fetch(c.slots)
+            wait()
+            got += c.attend(q[i], idx, 0.1)  # straight after another call
+            wait()
+            got += [c.slots.clone(), c.status.clone(), c.free_pages.clone()]
+            if H // KV in (8, 16):
+                n = 2 * R
+                rows = torch.arange(K, device=DEV, dtype=torch.int32).repeat(n, 1)
+                got += c.attend(q[i], torch.where(rows < lens[0], rows, -1), 0.1, request=0)
+                wait()
+        torch.cuda.synchronize()
+        return got
+
+    want = run(True)
+    for _ in range(3):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
