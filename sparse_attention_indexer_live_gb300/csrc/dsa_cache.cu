@@ -2,10 +2,10 @@
 // lengths, rows stored and rows read back (declared in include/dsa_select.h).
 //
 // Plans are latency: one launch, a prefix sum over the requests and a look-up a
-// token; 2.8 us for 96 tokens of 48 requests, 7 us for 66,016 tokens of 512.
-// Rows are bandwidth: 65,536 tokens x 2 heads of f16 stored and read back in 28.7
-// us (6.0 TB/s, 0.88 of the measured copy), 262,144 rows read as bf16 in 30.5 us
-// (5.7 TB/s, 0.84).
+// token; 2.6 us for 96 tokens of 48 requests, 5.7 us for 66,016 tokens of 512.
+// Rows are bandwidth: 65,536 tokens x 2 heads of f16 stored in 27.1 us (6.4 TB/s,
+// 0.94 of the measured copy), 262,144 rows read as bf16 in 28.0 us (6.2 TB/s,
+// 0.91).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kPThreads = 1024;  // at most
 constexpr int kMaxRequests = 8192;
-constexpr int kMaxPlanCluster = 8;
+constexpr int kMaxPlanCluster = 16;
 
 struct PlanParams {
   int32_t R, P, T, cap, pages, shift;
@@ -521,8 +521,9 @@ int dsa_cache_plan(const dsa_cache_cfg* cfg, int32_t requests, int32_t table_wid
   p.slots = slots;
   p.status = status;
   // Four tokens of a thread; a CTA of up to 1,024 threads, then more of them in
-  // one cluster.  Small steps take small CTAs: 96 tokens of 48 requests 3.0 us
-  // with 128 threads, 5.4 with 1,024.
+  // one cluster, as many as there are tokens for (66,016 tokens 6.7 us over 8 CTAs,
+  // 5.7 over 16).  Small steps take small CTAs: 96 tokens of 48 requests 3.0 us with
+  // 128 threads, 5.4 with 1,024.
   const int64_t want = std::max<int64_t>(requests, ((int64_t)tokens + 3) / 4);
   const int threads = (int)std::min<int64_t>(kPThreads, std::max<int64_t>(128, (want + 31) / 32 * 32));
   int nctas = 1;
@@ -534,6 +535,10 @@ int dsa_cache_plan(const dsa_cache_cfg* cfg, int32_t requests, int32_t table_wid
   if (smem > 47 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            5 * (int)sizeof(int32_t) * kMaxRequests) != cudaSuccess) {
+    cudaGetLastError();
+    return DSA_ERR_CUDA;
+  }
+  if (nctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
     cudaGetLastError();
     return DSA_ERR_CUDA;
   }
