@@ -3,9 +3,9 @@
 //
 // Plans are latency: one launch, a prefix sum over the requests and a look-up a
 // token; 2.6 us for 96 tokens of 48 requests, 5.7 us for 66,016 tokens of 512.
-// Rows are bandwidth: 65,536 tokens x 2 heads of f16 stored in 27.1 us (6.4 TB/s,
-// 0.94 of the measured copy), 262,144 rows read as bf16 in 28.0 us (6.2 TB/s,
-// 0.91).
+// Rows are bandwidth: 65,536 tokens x 2 heads of f16 stored and read back in 27.1
+// us (6.4 TB/s, 0.94 of the measured copy), 262,144 rows read as bf16 in 28.0 us
+// (6.2 TB/s, 0.91).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
