@@ -33,7 +33,7 @@
 
 #include <algorithm>
 
-#include "dsa_select.h"
+#include "dsa_internal.h"
 
 namespace {
 
@@ -157,6 +157,9 @@ __global__ void __launch_bounds__(kUThreads)
   // the attention launch that reads these records may start its own setup now
   // (it waits for this grid to finish before reading them)
   asm volatile("griddepcontrol.launch_dependents;");
+  // and this one may itself have started before the launch that wrote the lists
+  // had ended (their loads are plain ones: the read-only path may be taken ahead)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grp = blockIdx.x;
   const int t0 = grp * G;
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(kUThreads)
 #pragma unroll
         for (int u = 0; u < kUBatch; ++u) {
           const int i = i0 + 4 * kUThreads * u;
-          v[u] = i < total_in ? __ldg(reinterpret_cast<const int4*>(rows + i)) : make_int4(-1, -1, -1, -1);
+          v[u] = i < total_in ? *reinterpret_cast<const int4*>(rows + i) : make_int4(-1, -1, -1, -1);
         }
 #pragma unroll
         for (int u = 0; u < kUBatch; ++u) {
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(kUThreads)
         }
       }
     } else {
-      for (int i = tid; i < total_in; i += kUThreads) f(__ldg(rows + i), row_of(i));
+      for (int i = tid; i < total_in; i += kUThreads) f(rows[i], row_of(i));
     }
   };
   // the keys to scan: [0, S), or the chunks between the extreme valid entries
@@ -1218,21 +1221,8 @@ int launch_attention(const dsa_attention_cfg* cfg, const uint16_t* q, const uint
 
 }  // namespace
 
-extern "C" {
-
-int dsa_sparse_attention_workspace(const dsa_attention_cfg* cfg, size_t* bytes) {
-  if (!bytes) return DSA_ERR_INVALID_ARG;
-  *bytes = 0;
-  const int st = check_attention_cfg(cfg);
-  if (st != DSA_OK) return st;
-  const int G = kRows / cfg->heads;
-  const int64_t groups = ((int64_t)cfg->tokens + G - 1) / G;
-  *bytes = (size_t)(groups * union_layout(G, cfg->select).bytes);
-  return DSA_OK;
-}
-
-int dsa_group_union(const dsa_attention_cfg* cfg, const int32_t* idx, void* workspace, size_t workspace_bytes,
-                    struct CUstream_st* stream) {
+int dsa_group_union_launch(const dsa_attention_cfg* cfg, const int32_t* idx, void* workspace, size_t workspace_bytes,
+                           bool dependent, cudaStream_t stream) {
   size_t need = 0;
   int st = dsa_sparse_attention_workspace(cfg, &need);
   if (st != DSA_OK) return st;
@@ -1252,9 +1242,40 @@ int dsa_group_union(const dsa_attention_cfg* cfg, const int32_t* idx, void* work
     }
     if (dev < 64) configured[dev] = true;
   }
-  union_kernel<<<groups, kUThreads, U.smem, (cudaStream_t)stream>>>(
-      idx, cfg->tokens, cfg->select, cfg->keys, G, static_cast<uint8_t*>(workspace), union_layout(G, cfg->select), U);
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)groups);
+  lc.blockDim = dim3(kUThreads);
+  lc.dynamicSmemBytes = (size_t)U.smem;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = dependent ? 1 : 0;
+  if (cudaLaunchKernelEx(&lc, union_kernel, idx, cfg->tokens, cfg->select, cfg->keys, (int32_t)G,
+                         static_cast<uint8_t*>(workspace), union_layout(G, cfg->select), U) != cudaSuccess) {
+    cudaGetLastError();
+    return DSA_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+extern "C" {
+
+int dsa_sparse_attention_workspace(const dsa_attention_cfg* cfg, size_t* bytes) {
+  if (!bytes) return DSA_ERR_INVALID_ARG;
+  *bytes = 0;
+  const int st = check_attention_cfg(cfg);
+  if (st != DSA_OK) return st;
+  const int G = kRows / cfg->heads;
+  const int64_t groups = ((int64_t)cfg->tokens + G - 1) / G;
+  *bytes = (size_t)(groups * union_layout(G, cfg->select).bytes);
+  return DSA_OK;
+}
+
+int dsa_group_union(const dsa_attention_cfg* cfg, const int32_t* idx, void* workspace, size_t workspace_bytes,
+                    struct CUstream_st* stream) {
+  return dsa_group_union_launch(cfg, idx, workspace, workspace_bytes, false, (cudaStream_t)stream);
 }
 
 int dsa_sparse_attention(const dsa_attention_cfg* cfg, const uint16_t* q, const uint16_t* k, const uint16_t* v,

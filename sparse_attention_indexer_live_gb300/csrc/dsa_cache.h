@@ -60,7 +60,7 @@ constexpr int kSms = 152;
 // The calls' kernels follow one another closely (a decode step is a plan, a
 // write and an attention, 2 to 15 us each), so each is launched as a
 // programmatic dependent of the one before it: its launch and set-up overlap that
-// one's end.  Every kernel lets its successor start at once and then waits for
+// one's end (launches that wait for it start 2 us and more after it).  Every kernel lets its successor start at once and then waits for
 // its predecessor before it touches global memory, so a grid that has ended
 // means that all before it have.  What a predecessor may have written is read by
 // plain loads: the read-only path (__ldg) may be taken ahead of the wait.

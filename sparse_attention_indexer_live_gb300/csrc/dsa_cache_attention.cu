@@ -719,7 +719,7 @@ int dsa_cache_attention_prompt(const dsa_cache_cfg* cfg, int32_t tokens, int32_t
   if (!workspace || ((uintptr_t)workspace & 15u) || workspace_bytes < need) return DSA_ERR_INVALID_ARG;
   dsa_attention_cfg u = {tokens, heads / cfg->kv_heads, (int32_t)std::min<int64_t>((int64_t)table_width * cfg->page_size, INT32_MAX),
                          kCacheDim, kCacheDim, select};
-  st = dsa_group_union(&u, idx, workspace, workspace_bytes, stream);
+  st = dsa_group_union_launch(&u, idx, workspace, workspace_bytes, true, (cudaStream_t)stream);
   if (st != DSA_OK) return st;
   return dsa_cache_tile(make_params(cfg, tokens, heads, select, 1, table_width, cache, q, idx, nullptr, table, scale, o,
                                     lse),

@@ -61,4 +61,10 @@ DSA_HIDDEN int dsa_fused_blocks(const dsa_select_plan* plan, uint8_t* records, c
 DSA_HIDDEN int dsa_fused_topk(const dsa_select_plan* plan, const uint8_t* records, const int32_t* ends,
                               const int32_t* cand, int32_t* topk, cudaStream_t stream);
 
+// dsa_group_union; dependent: the launch may start before the one before it has
+// ended (it waits for it), which is safe only if what follows on the stream
+// reads nothing before its own wait.
+DSA_HIDDEN int dsa_group_union_launch(const dsa_attention_cfg* cfg, const int32_t* idx, void* workspace,
+                                      size_t workspace_bytes, bool dependent, cudaStream_t stream);
+
 #endif  // DSA_INTERNAL_H

@@ -293,6 +293,9 @@ SHAPES = [  # T, H, kv_heads, select, page, context, type
     (70, 17, 1, 1, 16, 40, "bf16"), (34, 24, 1, 129, 16, 300, "f16"), (40, 64, 1, 130, 8, 500, "bf16"),
     (160, 32, 1, 65, 64, 300, "f16"), (20, 128, 1, 2050, 64, 3000, "bf16"), (34, 96, 2, 1100, 16, 1500, "f16"),
     (9, 128, 1, 1030, 32, 1200, "bf16"),
+    # rows split over 2, 4 and 8 CTAs that share SMs
+    (150, 8, 1, 600, 64, 800, "bf16"), (80, 8, 1, 1100, 64, 1300, "f16"), (45, 16, 1, 2050, 64, 2300, "bf16"),
+    (22, 8, 2, 2049, 16, 2300, "bf16"),
 ]
 
 
