@@ -739,31 +739,36 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
       if (real && hf == 0) p.lse[row] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.6931471805599453f;
     }
     if (split > 1) {
-      // Join: every CTA finishes 128 / split of the rows and receives the others'
-      // shares of them over its stages, which all are done with.
-      const int per = 128 / split;
+      // Join: every CTA finishes an equal run of the rows (of a token's own heads:
+      // rows past them are neither sent nor finished, 64 heads of 17 tokens 14.6 /
+      // 12.9 us) and receives the others' shares of them over its stages, which all
+      // are done with.  Fetching the shares instead, row by row, was slower for 128
+      // heads (16.8 against 15.8) and no faster for 64.
+      const int per = ((kUnion ? 128 : p.n) + split - 1) / split;
       float* ro = reinterpret_cast<float*>(base);
       float* rm = reinterpret_cast<float*>(base + kOffRecvM);
       float* rl = reinterpret_cast<float*>(base + kOffRecvL);
       cluster.sync();
       {
-        const int to = r / per, at = rank * per + r % per;
+        const int to = real ? r / per : rank, at = real ? rank * per + r % per : 0;
         float* dst = cluster.map_shared_rank(ro, to) + at * kORow + 64 * hf;
-  #pragma unroll
+#pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t ov[32];
           if (ntiles > 0 && done) {
             tld32(lane_base + kTmemO + 64 * hf + 32 * c, ov);
             tld_wait();
           } else {
-  #pragma unroll
+#pragma unroll
             for (int j = 0; j < 32; ++j) ov[j] = 0u;
           }
-  #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<uint4*>(dst + 32 * c + j) = make_uint4(ov[j], ov[j + 1], ov[j + 2], ov[j + 3]);
+          if (real) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<uint4*>(dst + 32 * c + j) = make_uint4(ov[j], ov[j + 1], ov[j + 2], ov[j + 3]);
+          }
         }
-        if (hf == 0) {
+        if (real && hf == 0) {
           cluster.map_shared_rank(rm, to)[at] = m_used;
           cluster.map_shared_rank(rl, to)[at] = l;
         }
@@ -851,7 +856,8 @@ int dsa_cache_tile(const AttendParams& p, const uint8_t* records, bool bf16, cud
   // Few units: their tiles go over a cluster while every CTA has an SM of its
   // own and four tiles or more (of a list as long as one token's).  Clusters of
   // eight such CTAs, an SM each, find room for about half of the SMs: 64 heads,
-  // 2,048 entries, 4 tokens 15.4 / 13.0 us over 4 / 8 CTAs, 16 tokens 15.4 / 23.8.
+  // 2,048 entries, 8 tokens 10.5 us over 8 CTAs, 10 tokens 12.7 over 4; 16 tokens over
+  // 4 / 8, with a slower join than today's, 15.4 / 23.8.
   int split = 1;
   while (split < kMaxSplit && units * split * 2 <= (split * 2 == 8 ? kSms / 2 : kSms) &&
          (int64_t)p.Kc >= (int64_t)split * 4 * kTile)
