@@ -371,20 +371,19 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
       if (i < n && lane < 27) {
         const uint32_t src = list_from + i * (kTile * 4);
         const uint32_t dst = copy_to + st * kStageBytes;
-        if (full >> i & 1) {
-          uint32_t rec[11];
+        uint32_t rec[11];
 #pragma unroll
-          for (int j = 0; j < 11; ++j) rec[j] = lds32(src + 12 * j);
+        for (int j = 0; j < 11; ++j) rec[j] = lds32(src + 12 * j);
+        if (full >> i & 1) {
 #pragma unroll
           for (int j = 0; j < 11; ++j)
             if (j < 10 || lane < 18) cp16(dst + 3 * kRec * j, base + (uint64_t)rec[j] * kRec);
         } else {
-#pragma unroll 1
+#pragma unroll
           for (int j = 0; j < 11; ++j)
-            if (j < 10 || lane < 18) {
-              const uint32_t rec = list[i * kTile + first + 3 * j];
-              cp16_or_zero(dst + 3 * kRec * j, base + (rec == kNoRecord ? 0 : (uint64_t)rec * kRec), rec != kNoRecord);
-            }
+            if (j < 10 || lane < 18)
+              cp16_or_zero(dst + 3 * kRec * j, base + (rec[j] == kNoRecord ? 0 : (uint64_t)rec[j] * kRec),
+                           rec[j] != kNoRecord);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -543,19 +542,45 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
   if (split == 1) return;
   // join the CTAs' shares: CTA `rank` finishes every split-th head
   cluster.sync();
-  for (int j = 0; rank + j * split < nh; ++j) {
-    float mx = -INFINITY;
-    for (int c = 0; c < split; ++c) mx = fmaxf(mx, recv->m[c * hp + j]);
-    const float b = mx == -INFINITY ? 0.f : mx;
-    float ls = 0.f, os = 0.f;
-    for (int c = 0; c < split; ++c) {
-      const float a = ex2(recv->m[c * hp + j] - b);
-      ls += a * recv->l[c * hp + j];
-      os += a * recv->o[c * hp + j][tid];
+  if (hp <= 2) {
+    for (int j = 0; rank + j * split < nh; ++j) {
+      float mx = -INFINITY;
+      for (int c = 0; c < split; ++c) mx = fmaxf(mx, recv->m[c * hp + j]);
+      const float b = mx == -INFINITY ? 0.f : mx;
+      float ls = 0.f, os = 0.f;
+      for (int c = 0; c < split; ++c) {
+        const float a = ex2(recv->m[c * hp + j] - b);
+        ls += a * recv->l[c * hp + j];
+        os += a * recv->o[c * hp + j][tid];
+      }
+      const int64_t row = row0 + rank + j * split;
+      store<kBf16>(p.o, row * kCacheDim + tid, ls == 0.f ? 0.f : os / ls * p.v_mul);
+      if (tid == 0) p.lse[row] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * 0.6931471805599453f;
     }
-    const int64_t row = row0 + rank + j * split;
-    store<kBf16>(p.o, row * kCacheDim + tid, ls == 0.f ? 0.f : os / ls * p.v_mul);
-    if (tid == 0) p.lse[row] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * 0.6931471805599453f;
+    return;
+  }
+  // More heads a CTA: a thread per share (16 at most) takes its weight, then every
+  // thread a dim (16 heads over 2 CTAs: 1.5 us less than head after head).
+  float* w2 = &wgt[0][0];
+  if (tid < split * hp) {
+    const int c = tid / hp, j = tid - c * hp, h = rank + j * split;
+    if (h < nh) {
+      float mx = -INFINITY;
+      for (int u = 0; u < split; ++u) mx = fmaxf(mx, recv->m[u * hp + j]);
+      const float b = mx == -INFINITY ? 0.f : mx;
+      float ls = 0.f;
+      for (int u = 0; u < split; ++u) ls += ex2(recv->m[u * hp + j] - b) * recv->l[u * hp + j];
+      w2[tid] = ls == 0.f ? 0.f : ex2(recv->m[tid] - b) * (p.v_mul / ls);
+      if (c == 0) p.lse[row0 + h] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * 0.6931471805599453f;
+    }
+  }
+  __syncthreads();
+#pragma unroll 2
+  for (int j = 0; rank + j * split < nh; ++j) {
+    float os = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < split; ++c) os = fmaf(w2[c * hp + j], recv->o[c * hp + j][tid], os);
+    store<kBf16>(p.o, (row0 + rank + j * split) * kCacheDim + tid, os);
   }
 }
 
@@ -641,26 +666,33 @@ int64_t warp_units(const AttendParams& p) {
 // Whether tiles of 128 rows serve a call better.  They expand a record once for
 // all of a key/value head's query heads, this form once for every 16; but with
 // few CTAs this form splits further.  Lists of 2,048, this form against tiles:
-// 64 heads 8.8 against 12.7 us (1 token), 15.2 / 15.4 (16), 28.8 / 20.4 (64),
-// 92 / 54 (256); 24 heads 11.3 / 15.1 (16), 22.3 / 19.2 (64).
-bool wants_tiles(const AttendParams& p) { return p.n > 16 && warp_units(p) > 64; }
+// 64 heads 7.8 / 10.1 us (1 token), 11.0 / 10.5 (8), 13.3 / 12.7 (10), 14.7 / 12.9
+// (16), 21.9 / 13.2 (32); 24 heads 10.8 / 11.6 (16), 13.3 / 11.7 (20); 128 heads
+// 10.9 / 13.1 (4), 18.3 / 15.5 (10).
+bool wants_tiles(const AttendParams& p) { return p.n > 16 && warp_units(p) > 36; }
 
 int launch_attend(const AttendParams& p, int32_t dtype, cudaStream_t s) {
   const bool wide = p.n > 8;
   const int64_t units = warp_units(p);
-  // Rows are split while the clusters run at once and every warp has two tiles.
+  // Rows are split as far as the clusters run at once and the list is worth it.
   // Clusters of 16 find room only while each CTA has an SM of its own, the others
-  // up to 2.6 CTAs an SM, 3.3 for 8 heads in fours.  Measured, 2,048 entries of 8
-  // heads, over 1 / 2 / 4 / 8 CTAs: 32 rows 16.4 / 12.5 / 8.5 / 8.1 us, 48 rows
-  // 16.4 / 12.4 / 10.9 / 9.5, 64 16.6 / 12.5 / 11.0 / 11.5, 112 18.5 / 17.2 / 16.2 /
-  // 22.1, 136 21.0 / 18.9 / 19.2 / 25.0, 192 25.0 / 23.7 / 33.1, 256 27.5 / 30.1; of
-  // 16 heads: 48 rows 19.8 / 16.8 / 14.4 / 13.4, 96 23.5 / 21.8 / 18.8 / 26.8, 112
-  // 24.1 / 22.7 / 29.8, 192 29.7 / 29.8, 256 30.8 / 46.5.  Over 8 / 16: one row of 8
-  // heads 7.1 / 6.4, 16 rows 8.4 / 13.5.
+  // up to 2.6 CTAs an SM, 3.3 for 8 heads in fours.  2,048 entries of 8 heads, over
+  // 1 / 2 / 4 / 8 CTAs: 32 rows 16.4 / 12.5 / 8.5 / 8.1 us, 48 rows 16.4 / 12.4 /
+  // 10.9 / 9.5, 64 16.6 / 12.5 / 11.0 / 11.5, 112 18.5 / 17.2 / 16.2 / 22.1, 136 21.0 /
+  // 18.9 / 19.2 / 25.0, 192 25.0 / 23.7 / 33.1, 256 27.5 / 30.1; of 16 heads: 48 rows
+  // 19.8 / 16.8 / 14.4 / 13.4, 96 23.5 / 21.8 / 18.8 / 26.8, 112 24.1 / 22.7 / 29.8,
+  // 192 29.7 / 29.8, 256 30.8 / 46.5.  Over 8 / 16: one row of 8 heads 7.1 / 6.4, 16
+  // rows 8.4 / 13.5.
+  // The join costs 2 us and more, fewest shares most (each CTA then finishes more
+  // heads), so short lists stay whole: 2 rows of 8 heads 4.9 / 6.2 / 6.0 / 5.7 us at
+  // 256 entries, 5.8 / 6.7 / 6.1 / 5.8 at 384, 6.7 / 6.8 / 6.0 / 5.8 at 512; 60 rows
+  // 6.8 / 7.4 / 7.4 at 512, 8.4 / 8.2 / 8.0 at 768; 100 rows 11.6 / 11.3 / 9.9 at 1,024;
+  // of 16 heads 10.5 / 12.8 / 12.9 at 768, 14.0 / 14.3 / 13.8 at 1,024, 16.7 / 17.4 /
+  // 16.2 at 1,500.
   auto room = [&](int c) { return (c == 16 ? 10 : c == 4 && !wide ? 33 : 26) * kSms / 10; };
-  int split = 1;
-  while (split < kMaxSplit && units * split * 2 <= room(split * 2) && (int64_t)p.Kc >= (int64_t)split * 2 * kTile * kWarps)
-    split *= 2;
+  auto least = [&](int c) { return c == 16 ? 1024 : c == 8 ? (wide ? 640 : 512) : c == 4 ? 768 : wide ? 2048 : 1024; };
+  int split = kMaxSplit;
+  while (split > 1 && (units * split > room(split) || p.Kc < least(split))) split /= 2;
   const int64_t ctas = units * split;
   if (ctas >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
   if (!wide)

@@ -294,8 +294,9 @@ SHAPES = [  # T, H, kv_heads, select, page, context, type
     (160, 32, 1, 65, 64, 300, "f16"), (20, 128, 1, 2050, 64, 3000, "bf16"), (34, 96, 2, 1100, 16, 1500, "f16"),
     (9, 128, 1, 1030, 32, 1200, "bf16"),
     # rows split over 2, 4 and 8 CTAs that share SMs
-    (150, 8, 1, 600, 64, 800, "bf16"), (80, 8, 1, 1100, 64, 1300, "f16"), (45, 16, 1, 2050, 64, 2300, "bf16"),
-    (22, 8, 2, 2049, 16, 2300, "bf16"),
+    (150, 7, 1, 1100, 64, 1300, "bf16"), (80, 8, 1, 1100, 64, 1300, "f16"), (45, 16, 1, 2050, 64, 2300, "bf16"),
+    (22, 8, 2, 2049, 16, 2300, "bf16"), (100, 16, 1, 2050, 64, 2300, "f16"), (50, 12, 1, 900, 32, 1000, "bf16"),
+    (30, 10, 2, 800, 16, 900, "f16"), (7, 13, 1, 650, 16, 700, "bf16"),
 ]
 
 
