@@ -51,6 +51,8 @@ struct AttendParams {
 // union records of groups of 128 / n tokens (dsa_group_union), whose keys are
 // positions of request 0; NULL: a token a tile, its own list.  n <= 128 rows.
 DSA_HIDDEN int dsa_cache_tile(const AttendParams& p, const uint8_t* records, bool bf16, cudaStream_t stream);
+// CTAs that each of `units` rows of tiles, `select` entries a token, is split over.
+DSA_HIDDEN int dsa_cache_tile_split(int64_t units, int32_t select);
 
 // SMs of the device.
 constexpr int kSms = 152;

@@ -663,37 +663,60 @@ int64_t warp_units(const AttendParams& p) {
   return (int64_t)p.T * p.kv_heads * ((p.n + wide - 1) / wide);
 }
 
-// Whether tiles of 128 rows serve a call better.  They expand a record once for
-// all of a key/value head's query heads, this form once for every 16; but with
-// few CTAs this form splits further.  Lists of 2,048, this form against tiles:
-// 64 heads 7.8 / 10.1 us (1 token), 11.0 / 10.5 (8), 13.3 / 12.7 (10), 14.7 / 12.9
-// (16), 21.9 / 13.2 (32); 24 heads 10.8 / 11.6 (16), 13.3 / 11.7 (20); 128 heads
-// 10.9 / 13.1 (4), 18.3 / 15.5 (10).
-bool wants_tiles(const AttendParams& p) { return p.n > 16 && warp_units(p) > 36; }
-
-int launch_attend(const AttendParams& p, int32_t dtype, cudaStream_t s) {
+// Rows are split as far as the clusters run at once and the list is worth it.
+// Clusters of 16 find room only while each CTA has an SM of its own, the others
+// up to 2.6 CTAs an SM, 3.3 for 8 heads in fours.  2,048 entries of 8 heads, over
+// 1 / 2 / 4 / 8 CTAs: 32 rows 16.4 / 12.5 / 8.5 / 8.1 us, 48 rows 16.4 / 12.4 /
+// 10.9 / 9.5, 64 16.6 / 12.5 / 11.0 / 11.5, 112 18.5 / 17.2 / 16.2 / 22.1, 136 21.0 /
+// 18.9 / 19.2 / 25.0, 192 25.0 / 23.7 / 33.1, 256 27.5 / 30.1; of 16 heads: 48 rows
+// 19.8 / 16.8 / 14.4 / 13.4, 96 23.5 / 21.8 / 18.8 / 26.8, 112 24.1 / 22.7 / 29.8,
+// 192 29.7 / 29.8, 256 30.8 / 46.5.  Over 8 / 16: one row of 8 heads 7.1 / 6.4, 16
+// rows 8.4 / 13.5.
+// The join costs 2 us and more, fewest shares most (each CTA then finishes more
+// heads), so short lists stay whole: 2 rows of 8 heads 4.9 / 6.2 / 6.0 / 5.7 us at
+// 256 entries, 5.8 / 6.7 / 6.1 / 5.8 at 384, 6.7 / 6.8 / 6.0 / 5.8 at 512; 60 rows
+// 6.8 / 7.4 / 7.4 at 512, 8.4 / 8.2 / 8.0 at 768; 100 rows 11.6 / 11.3 / 9.9 at 1,024;
+// of 16 heads 10.5 / 12.8 / 12.9 at 768, 14.0 / 14.3 / 13.8 at 1,024, 16.7 / 17.4 /
+// 16.2 at 1,500.
+int attend_split(const AttendParams& p) {
   const bool wide = p.n > 8;
   const int64_t units = warp_units(p);
-  // Rows are split as far as the clusters run at once and the list is worth it.
-  // Clusters of 16 find room only while each CTA has an SM of its own, the others
-  // up to 2.6 CTAs an SM, 3.3 for 8 heads in fours.  2,048 entries of 8 heads, over
-  // 1 / 2 / 4 / 8 CTAs: 32 rows 16.4 / 12.5 / 8.5 / 8.1 us, 48 rows 16.4 / 12.4 /
-  // 10.9 / 9.5, 64 16.6 / 12.5 / 11.0 / 11.5, 112 18.5 / 17.2 / 16.2 / 22.1, 136 21.0 /
-  // 18.9 / 19.2 / 25.0, 192 25.0 / 23.7 / 33.1, 256 27.5 / 30.1; of 16 heads: 48 rows
-  // 19.8 / 16.8 / 14.4 / 13.4, 96 23.5 / 21.8 / 18.8 / 26.8, 112 24.1 / 22.7 / 29.8,
-  // 192 29.7 / 29.8, 256 30.8 / 46.5.  Over 8 / 16: one row of 8 heads 7.1 / 6.4, 16
-  // rows 8.4 / 13.5.
-  // The join costs 2 us and more, fewest shares most (each CTA then finishes more
-  // heads), so short lists stay whole: 2 rows of 8 heads 4.9 / 6.2 / 6.0 / 5.7 us at
-  // 256 entries, 5.8 / 6.7 / 6.1 / 5.8 at 384, 6.7 / 6.8 / 6.0 / 5.8 at 512; 60 rows
-  // 6.8 / 7.4 / 7.4 at 512, 8.4 / 8.2 / 8.0 at 768; 100 rows 11.6 / 11.3 / 9.9 at 1,024;
-  // of 16 heads 10.5 / 12.8 / 12.9 at 768, 14.0 / 14.3 / 13.8 at 1,024, 16.7 / 17.4 /
-  // 16.2 at 1,500.
   auto room = [&](int c) { return (c == 16 ? 10 : c == 4 && !wide ? 33 : 26) * kSms / 10; };
   auto least = [&](int c) { return c == 16 ? 1024 : c == 8 ? (wide ? 640 : 512) : c == 4 ? 768 : wide ? 2048 : 1024; };
   int split = kMaxSplit;
   while (split > 1 && (units * split > room(split) || p.Kc < least(split))) split /= 2;
-  const int64_t ctas = units * split;
+  return split;
+}
+
+// Whether tiles of 128 rows serve a call better.  They expand a record once for
+// all of a key/value head's query heads, this form once for every 16; but a CTA
+// of theirs takes an SM and 5 to 8 us beside its tiles, and this form splits
+// further.  The smaller of two estimates in us, each a fit to what was measured
+// (30 to 2,048 entries, 24 to 128 heads, 1 to 400 tokens) that is off by up to a
+// fifth where the two are far apart.  This form against tiles, 2,048 entries: 64
+// heads 7.8 / 10.1 us (1 token), 11.0 / 10.5 (8), 14.7 / 12.9 (16), 21.9 / 13.2 (32);
+// 24 heads 10.8 / 11.6 (16), 13.3 / 11.7 (20); 128 heads 10.9 / 13.1 (4), 18.3 / 15.5
+// (10).  256 entries: 24 heads 6.6 / 7.6 (50), 10.7 / 15.1 (200, tiles in a second
+// wave); 64 heads 8.0 / 8.3 (50), 10.7 / 8.3 (100).
+bool wants_tiles(const AttendParams& p) {
+  if (p.n <= 16) return false;
+  const int64_t tile_units = (int64_t)p.T * p.kv_heads;
+  const int ts = dsa_cache_tile_split(tile_units, p.Kc);
+  const int64_t tiles = (p.Kc + 128 * (int64_t)ts - 1) / (128 * (int64_t)ts);
+  const int64_t waves = (tile_units * ts + kSms - 1) / kSms;
+  const double tile_us = waves * (4.7 + p.n / 40.0 + 1.2 * tiles) + (ts > 1 ? 1.5 : 0.0);
+  const int s = attend_split(p);
+  const double ctas = (double)warp_units(p) * s, most = 3.0 * kSms;
+  const int64_t steps = (p.Kc + 128 * (int64_t)s - 1) / (128 * (int64_t)s);  // tiles of a warp
+  double us = ctas <= most ? 4.3 + 0.006 * ctas + steps * (0.85 + 0.003 * ctas) : ctas / most * (7.0 + 2.2 * steps);
+  if (s > 1) us += 10 * ctas <= 17 * kSms ? 2.5 : 3.5;
+  return tile_us < us;
+}
+
+int launch_attend(const AttendParams& p, int32_t dtype, cudaStream_t s) {
+  const bool wide = p.n > 8;
+  const int split = attend_split(p);
+  const int64_t ctas = warp_units(p) * split;
   if (ctas >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
   if (!wide)
     return dtype == DSA_BF16 ? launch_staged<1, true>(p, ctas, split, s) : launch_staged<1, false>(p, ctas, split, s);

@@ -839,6 +839,19 @@ int launch_tile(const TileParams& tp, int64_t units, int split, cudaStream_t s) 
 
 }  // namespace
 
+// Few units: their tiles go over a cluster while every CTA has an SM of its
+// own and four tiles or more (of a list as long as one token's).  Clusters of
+// eight such CTAs, an SM each, find room for about half of the SMs: 64 heads,
+// 2,048 entries, 8 tokens 10.5 us over 8 CTAs, 10 tokens 12.7 over 4; 16 tokens over
+// 4 / 8, with a slower join than today's, 15.4 / 23.8.
+int dsa_cache_tile_split(int64_t units, int32_t select) {
+  int split = 1;
+  while (split < kMaxSplit && units * split * 2 <= (split * 2 == 8 ? kSms / 2 : kSms) &&
+         (int64_t)select >= (int64_t)split * 4 * kTile)
+    split *= 2;
+  return split;
+}
+
 int dsa_cache_tile(const AttendParams& p, const uint8_t* records, bool bf16, cudaStream_t stream) {
   TileParams tp;
   tp.a = p;
@@ -853,15 +866,7 @@ int dsa_cache_tile(const AttendParams& p, const uint8_t* records, bool bf16, cud
   tp.negate = p.scale_log2 < 0.f;
   if (tp.negate) tp.a.scale_log2 = -p.scale_log2;
   const int64_t units = (int64_t)((p.T + tp.G - 1) / tp.G) * p.kv_heads;
-  // Few units: their tiles go over a cluster while every CTA has an SM of its
-  // own and four tiles or more (of a list as long as one token's).  Clusters of
-  // eight such CTAs, an SM each, find room for about half of the SMs: 64 heads,
-  // 2,048 entries, 8 tokens 10.5 us over 8 CTAs, 10 tokens 12.7 over 4; 16 tokens over
-  // 4 / 8, with a slower join than today's, 15.4 / 23.8.
-  int split = 1;
-  while (split < kMaxSplit && units * split * 2 <= (split * 2 == 8 ? kSms / 2 : kSms) &&
-         (int64_t)p.Kc >= (int64_t)split * 4 * kTile)
-    split *= 2;
+  const int split = dsa_cache_tile_split(units, p.Kc);
   if (units * split >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
   if (records)
     return bf16 ? launch_tile<true, true>(tp, units, split, stream) : launch_tile<false, true>(tp, units, split, stream);

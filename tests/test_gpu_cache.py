@@ -297,6 +297,9 @@ SHAPES = [  # T, H, kv_heads, select, page, context, type
     (150, 7, 1, 1100, 64, 1300, "bf16"), (80, 8, 1, 1100, 64, 1300, "f16"), (45, 16, 1, 2050, 64, 2300, "bf16"),
     (22, 8, 2, 2049, 16, 2300, "bf16"), (100, 16, 1, 2050, 64, 2300, "f16"), (50, 12, 1, 900, 32, 1000, "bf16"),
     (30, 10, 2, 800, 16, 900, "f16"), (7, 13, 1, 650, 16, 700, "bf16"),
+    # tiles, whole: short lists of many tokens
+    (100, 64, 1, 300, 16, 400, "bf16"), (90, 17, 1, 200, 64, 300, "f16"), (130, 100, 1, 5, 16, 60, "bf16"),
+    (70, 128, 1, 33, 8, 90, "f16"), (75, 120, 2, 129, 16, 200, "bf16"),
 ]
 
 
@@ -305,7 +308,7 @@ def test_attention(T, H, KV, Kc, page, ctx, dtype):
     _Case(T, H, KV, Kc, page=page, ctx=ctx, dtype=dtype, seed=T + H + Kc).device().launch().check()
 
 
-@pytest.mark.parametrize("H,KV,T", [(8, 1, 14), (16, 2, 14), (64, 1, 14), (64, 1, 40), (128, 1, 14)])
+@pytest.mark.parametrize("H,KV,T", [(8, 1, 14), (16, 2, 14), (64, 1, 14), (64, 1, 40), (128, 1, 14), (128, 1, 70)])
 def test_attention_edge_rows(H, KV, T):
     c = _Case(T, H, KV, 150, page=16, ctx=200, R=5, sort=False, seed=H)
     c.idx[0] = -1                                   # nothing
@@ -324,7 +327,7 @@ def test_attention_edge_rows(H, KV, T):
     c.device().launch().check()
 
 
-@pytest.mark.parametrize("H,T", [(8, 6), (64, 6), (128, 12)])
+@pytest.mark.parametrize("H,T", [(8, 6), (64, 6), (128, 12), (128, 70)])
 def test_attention_ignores_what_is_not_selected(H, T):
     # NaN scales in places no row lists
     c = _Case(T, H, 1, 60, page=8, ctx=80, R=2, seed=3)
@@ -345,7 +348,7 @@ def test_attention_ignores_what_is_not_selected(H, T):
     assert np.isnan(o[2]).all() and np.isfinite(o).any()
 
 
-@pytest.mark.parametrize("H,T", [(8, 7), (24, 7), (128, 12)])
+@pytest.mark.parametrize("H,T", [(8, 7), (24, 7), (128, 12), (128, 70)])
 def test_attention_query_magnitudes(H, T):
     rng = np.random.default_rng(8)
     q = rng.standard_normal((T, H, 128))
