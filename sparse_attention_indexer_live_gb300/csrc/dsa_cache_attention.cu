@@ -8,10 +8,10 @@
 // position, of which every scale and code is expanded once for 8 (or 16) heads.
 //
 // What bounds it: a batch (512 tokens x 4 key/value heads x 8 heads, 1,001
-// entries) takes 75 us against 45 us for its bytes at the measured copy rate:
+// entries) takes 73 us against 45 us for its bytes at the measured copy rate:
 // 290 instructions a 16 positions (134 of them conversions and scalings) keep
 // the schedulers 77 % busy in the loop, and a third of a CTA's life is the
-// look-ups before and the join after it.  One token (6.4 us) is launch, three
+// look-ups before and the join after it.  One token (5.5 us) is launch, three
 // dependent reads (entry, page, record), two tiles a warp and the cluster's join.
 // Measured: records by cp.async.bulk, one 144-byte copy a lane, 122 us against
 // 100 for 16-byte cp.async pieces; look-ups one tile at a time 95 us against 79

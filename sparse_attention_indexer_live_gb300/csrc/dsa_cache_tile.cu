@@ -21,7 +21,7 @@
 //
 // What bounds it: neither HBM (2,048 tokens of 8 heads over a million positions:
 // 90 MB read in 52 us) nor the tensor cores (16 products of 128 x 128 x 16 a
-// tile, 68 cycles each at the peak rate: 1,090 of a tile's 3,500 cycles), but
+// tile, 68 cycles each at the peak rate: 1,090 of a tile's 2,700 cycles), but
 // the softmax's chain within a tile -- TMEM load, masks, maximum, exponentials,
 // TMEM store, each 150 to 900 cycles -- at five warps a scheduler.  Measured for
 // the same chunk, with the union's 18 us: 71.2 us; codes through registers in

@@ -137,7 +137,7 @@ def test_what_is_left_to_the_binding(calls, name):
             s.seen = None
             assert call(*{**a, n: torch.cat([flat, flat])}.values()) == 0  # more is fine
     bad = dsa.cache_cfg(pages=PAGES, page_size=24, kv_heads=KV)
-    if name != "plan":  # a plan's cfg is the library's to judge
+    if name != "plan":  # a plan's cfg is left to the library
         left({**a, "cfg": bad})
         left({**a, "cfg": dsa.cache_cfg(pages=2 ** 30, page_size=1, kv_heads=64)})
     if "scale" in a:
