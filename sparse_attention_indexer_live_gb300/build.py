@@ -40,10 +40,12 @@ def nvcc_path() -> str:
 
 def calls_path() -> str | None:
     """The module built from cache_calls.cpp (None without torch)."""
+    if importlib.util.find_spec("torch") is None:
+        return None
     try:
         version = importlib.metadata.version("torch")
     except importlib.metadata.PackageNotFoundError:
-        return None
+        version = ""
     return os.path.join(BUILD_DIR, f"cache_calls.torch{version}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 

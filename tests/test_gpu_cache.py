@@ -790,3 +790,68 @@ def test_calls_follow_one_another(H, KV, R):
     for _ in range(3):
         for a, b in zip(run(False), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("form", ["decode", "prompt"])
+def test_captured_between_copies_and_streams(form):
+    """A graph in which copies and clears come right before the calls and one
+    call runs on a second stream: the same results as without a graph."""
+    torch, dsa = _mods()
+    R, page, T, H = 2, 16, 8, 16
+    gen = torch.Generator(DEV).manual_seed(61)
+    c = dsa.PagedCache(requests=R, pages=32, pages_per_request=16, page_size=page)
+    lens0 = torch.tensor([90, 33], dtype=torch.int32, device=DEV)
+    c.step(lens0, lens0, 123)
+    c.ok()
+    c.store(*torch.randn(2, 123, 1, 128, device=DEV, generator=gen).bfloat16().unbind(0))
+    src = [torch.randn(2, T, 1, 128, device=DEV, generator=gen).bfloat16() for _ in range(3)]
+    qs = [torch.randn(T, H, 128, device=DEV, generator=gen).half() for _ in range(3)]
+    lists = torch.arange(80, device=DEV, dtype=torch.int32).repeat(T, 1)
+    lens_in, fresh_in = lens0 + torch.tensor([6, 2], dtype=torch.int32, device=DEV), torch.tensor(
+        [6, 2], dtype=torch.int32, device=DEV)
+    lens, fresh, idx = torch.empty_like(lens_in), torch.empty_like(fresh_in), torch.empty_like(lists)
+    kv_in, kv = src[0].clone(), torch.empty_like(src[0])
+    q_in, q = qs[0].clone(), torch.empty_like(qs[0])
+    rows = torch.empty(2, T, 1, 128, dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+    c.step(lens_in, fresh_in, T)  # makes the maps
+
+    def step():
+        main = torch.cuda.current_stream()
+        lens.copy_(lens_in)
+        fresh.copy_(fresh_in)
+        c.step(lens, fresh, T)
+        kv.copy_(kv_in)
+        c.store(kv[0], kv[1])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            rows.zero_()
+            dsa.dsa_cache_read(c.cfg, c.data, c.slots, rows[0], rows[1])
+        q.copy_(q_in)
+        idx.copy_(lists)
+        o, lse = c.attend(q, idx, 0.1, request=0 if form == "prompt" else None)
+        main.wait_stream(side)
+        again = c.attend(q, idx, 0.1, request=0 if form == "prompt" else None)
+        return o, lse, rows.clone(), *again
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for x, y in zip(src, qs):
+        kv_in.copy_(x)
+        q_in.copy_(y)
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        have = [t.clone() for t in got]
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(have, want))
+        assert torch.equal(have[0], have[3]) and torch.equal(have[1], have[4])
+    assert dsa.dsa_cache_attention_status() == dsa.DSA_OK
