@@ -1086,6 +1086,7 @@ __global__ void __launch_bounds__(kAThreads, 1) attention_kernel(const AttnParam
           if (m_used > -INFINITY) alpha = ex2(m_used - m_new);
           m_used = m_new;
         }
+        tst_wait();  // two stores to the same columns keep no order of their own
         // rows without a change recompute the same weights
         weights(m_used == -INFINITY ? 0.f : m_used, false);
         if (__any_sync(0xFFFFFFFFu, alpha != 1.f) && i >= 1) {

@@ -682,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
           if (m_used > -INFINITY) alpha = ex2(m_used - m_new);
           m_used = m_new;
         }
+        tst_wait();  // two stores to the same columns keep no order of their own
         weights(m_used == -INFINITY ? 0.f : m_used, false);
         if (__any_sync(0xFFFFFFFFu, alpha != 1.f) && i >= 1) {
           // rescale this half of the row of O once the previous P V is done
