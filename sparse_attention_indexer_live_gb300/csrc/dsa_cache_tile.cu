@@ -60,7 +60,8 @@ constexpr int kOffRaw = kOffV + kVStages * 2 * kBlk;
 constexpr int kOffMask = kOffRaw + kRaw * kRawBytes;            // [stage][token][4 words]
 constexpr int kOffValid = kOffMask + kMaskStages * 16 * 4 * 4;   // [stage][4 words]
 constexpr int kOffXch = kOffValid + kMaskStages * 4 * 4;         // [parity][half][row]
-constexpr int kOffBars = kOffXch + 2 * 2 * 128 * 4;
+constexpr int kOffBad = kOffXch + 2 * 2 * 128 * 4;               // [half][row]
+constexpr int kOffBars = kOffBad + 2 * 128 * 4;
 constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 2 * kMaskStages + 6;
 constexpr int kOffTmem = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffTmem + 16 + 1024;  // + slack for the 1024-byte alignment
@@ -80,6 +81,7 @@ constexpr long long kWaitCycles = 4000000000ll;  // ~2 s
 
 __device__ int g_cache_attn_error;
 __shared__ int s_abort;
+__shared__ int s_nan;  // a value scale of the CTA's tiles is a NaN
 
 struct TileParams {
   AttendParams a;
@@ -280,8 +282,7 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
 __device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
-// Whether one of two e4m3 bytes is a NaN, and the pair with zeros for those.
-__device__ __forceinline__ bool has_nan(uint32_t s) { return (s & 0x7F) == 0x7F || (s & 0x7F00) == 0x7F00; }
+// Two e4m3 bytes with zeros in place of NaN.
 __device__ __forceinline__ uint32_t without_nan(uint32_t s) {
   if ((s & 0x7F) == 0x7F) s &= 0xFF00u;
   if ((s & 0x7F00) == 0x7F00) s &= 0xFFu;
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
   uint32_t* maskrow = reinterpret_cast<uint32_t*>(base + kOffMask);
   uint32_t* valid = reinterpret_cast<uint32_t*>(base + kOffValid);
   float* xch = reinterpret_cast<float*>(base + kOffXch);
+  uint32_t* xbad = reinterpret_cast<uint32_t*>(base + kOffBad);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + kOffBars);
   uint64_t* qfull = bars;                   // Q in TMEM (softmax)
   uint64_t* kfull = qfull + 1;              // [2] key tile expanded (its 4 warps)
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
 
   let_next_start();
   if (threadIdx.x == 0) {
-    s_abort = 0;
+    s_abort = s_nan = 0;
     bar_init(qfull, 256);
     for (int i = 0; i < kKStages; ++i) {
       bar_init(&kfull[i], 4);
@@ -358,6 +360,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
   // this CTA's tiles: rank, rank + split, ... of the row's
   const int all_tiles = (int)(((int64_t)n + kTile - 1) / kTile);
   const int ntiles = (all_tiles - rank + split - 1) / split;
+  auto page_of = [&](int key) -> int {
+    return key >= 0 && (key >> p.shift) < p.P ? p.tables[(int64_t)req * p.P + (key >> p.shift)] : -1;
+  };
+  auto record_of = [&](int key, int page) -> uint32_t {
+    if (page < 0 || page >= p.pages) return kNoRecord;
+    const uint32_t slot = ((uint32_t)page << p.shift) + (key & ((1u << p.shift) - 1));
+    return slot * p.kv_heads + kvh;
+  };
 
   if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
@@ -370,18 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
     const bool is_k = warp < 4;
     const int w4 = warp & 3;
     const int r8 = lane & 7, quarter = lane >> 3;
-    const int32_t* table = p.tables + (int64_t)req * p.P;
     auto key_of = [&](int i) -> int {
       const int64_t e = ((int64_t)i * split + rank) * kTile + 32 * w4 + lane;
       return e < n ? keys[e] : -1;
-    };
-    auto page_of = [&](int key) -> int {
-      return key >= 0 && (key >> p.shift) < p.P ? table[key >> p.shift] : -1;
-    };
-    auto record_of = [&](int key, int page) -> uint32_t {
-      if (page < 0 || page >= p.pages) return kNoRecord;
-      const uint32_t slot = ((uint32_t)page << p.shift) + (key & ((1u << p.shift) - 1));
-      return slot * p.kv_heads + kvh;
     };
     // raw stages: 64 bytes of codes a row, 16-byte pieces swizzled by the row's
     // pair so that eight rows' pieces lie on different banks; 16 of scales
@@ -437,11 +438,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                      : "r"(raw_code + slot * kRawBytes + 8 * q * 64));
         const uint32_t sa = raw_scale + slot * kRawBytes + (8 * q + r8) * 16 + 2 * quarter;
-        // A NaN among a record's scales goes to the scores of the rows that
-        // attend to it, through its keys: 0 times a NaN value would reach the
-        // others of the tile.
+        // A NaN value would reach rows that do not attend to it (0 times it is a
+        // NaN): values are expanded without, and those that do find it at the end.
+        // (Both pairs are read by both kinds of warps: 72.0 us for the 2,048-token
+        // chunk, 72.7 with one of them.)
         const uint32_t sv = lds16(sa + 8);
-        uint32_t s = is_k ? (has_nan(sv) ? 0x7F7Fu : lds16(sa)) : without_nan(sv);
+        uint32_t s = is_k ? lds16(sa) : sv;
+        if (!is_k) {
+          const uint32_t clean = without_nan(s);
+          if (clean != s) *(volatile int*)&s_nan = 1;
+          s = clean;
+        }
         s = e4m3x2(s);
         const uint32_t lo = __byte_perm(s, 0, 0x1010), hi = __byte_perm(s, 0, 0x3232);
 #pragma unroll
@@ -708,9 +715,46 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
       done = wait_all(&pvdone[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1);
       fence_after();
     }
+    // The dims that the row loses to NaN values (bit g: dims 16 g .. 16 g + 15),
+    // its positions' scales read once more: each lane a position, then those that
+    // have a NaN one after another.
+    uint32_t bad = 0;
+    if (ntiles > 0 && done && wait_all(&vfull[(ntiles - 1) % kVStages], ((ntiles - 1) / kVStages) & 1) &&
+        *(volatile int*)&s_nan) {
+      const uint32_t* masks = reinterpret_cast<const uint32_t*>(rec + tp.masks_off);
+#pragma unroll 1
+      for (int i = 0; i < 2 * ntiles; ++i) {
+        const int64_t e = ((int64_t)(i >> 1) * split + rank) * kTile + 64 * hf + 32 * (i & 1) + lane;
+        const int key = e < n ? keys[e] : -1;
+        const uint32_t x = record_of(key, page_of(key));
+        uint32_t lost = 0;
+        if (x != kNoRecord) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p.cache + (uint64_t)x * kRec + kRecVs);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) lost |= (uint32_t)(((j < 4 ? v.x : v.y) >> (8 * (j & 3)) & 0x7F) == 0x7F) << j;
+        }
+        const uint32_t seen = kUnion && lost ? masks[e] : 0u;
+        for (uint32_t some = __ballot_sync(0xFFFFFFFFu, lost != 0); some; some &= some - 1) {
+          const int from = __ffs(some) - 1;
+          const uint32_t a = __shfl_sync(0xFFFFFFFFu, lost, from), b = __shfl_sync(0xFFFFFFFFu, seen, from);
+          if (!kUnion || (b >> g & 1u)) bad |= a;
+        }
+      }
+    }
+    __syncwarp();
     // the row's sum: its halves' (added in the same order by both)
     xch[((ntiles & 1) * 2 + hf) * 128 + r] = l;
+    xbad[hf * 128 + r] = bad;
     named_sync(pair_bar, 64);
+    bad |= xbad[(hf ^ 1) * 128 + r];
+    // 32 dims of the row's half with those it loses
+    auto lose = [&](int c, uint32_t (&ov)[32]) {
+      const uint32_t two = bad >> (4 * hf + 2 * c);
+      if (!(two & 3u)) return;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (two >> (j >> 4) & 1u) ov[j] = 0x7FFFFFFFu;
+    };
     const float l_other = xch[((ntiles & 1) * 2 + (hf ^ 1)) * 128 + r];
     l = hf == 0 ? l + l_other : l_other + l;
     if (split == 1) {
@@ -726,6 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
 #pragma unroll
           for (int j = 0; j < 32; ++j) ov[j] = 0u;
         }
+        lose(c, ov);
         if (real) {
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
@@ -763,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
 #pragma unroll
             for (int j = 0; j < 32; ++j) ov[j] = 0u;
           }
+          lose(c, ov);
           if (real) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)

@@ -1,0 +1,43 @@
+"""The paged 4-bit cache where its forms, types and plans could differ from their
+definition, against the plain forms of tests/cache_ref.py."""
+import numpy as np
+import pytest
+
+from tests import cache_ref as ref
+from tests.test_gpu_cache import DEV, HALF, _Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("form,T,H,KV,Kc,ctx", [
+    ("decode", 6, 8, 1, 60, 200), ("decode", 5, 16, 2, 300, 700), ("decode", 2, 8, 1, 2100, 2500),
+    # tiles of a token's heads: whole, and split over CTAs
+    ("decode", 70, 128, 1, 60, 200), ("decode", 100, 64, 1, 300, 900), ("decode", 10, 128, 1, 1100, 1500),
+    # tiles of neighbours: whole, and split
+    ("prompt", 40, 8, 1, 60, 400), ("prompt", 20, 16, 2, 1100, 3000)])
+def test_nan_value_scales_reach_their_dims(form, T, H, KV, Kc, ctx):
+    """A NaN among a record's value scales makes that scale's 16 dims of the rows
+    that attend to it NaN: no other dim, no other row and no lse."""
+    c = _Case(T, H, KV, Kc, page=16, ctx=ctx, R=1, seed=T + H)
+    c.idx[1, 5:] = -1
+    clean = c.cache.copy()
+    p, q, r = int(c.idx[0][Kc // 2]), int(c.idx[T - 1 if T > 2 else 0][Kc - 1]), int(c.idx[T // 2][0])
+    c.cache[c.tables[0, p // 16], p % 16, 0, 139] = 0x7F
+    for g in (0, 4, 7):
+        c.cache[c.tables[0, q // 16], q % 16, KV - 1, 136 + g] = 0xFF
+    for step in range(2):
+        if step == 1:  # beside a NaN key, whose rows are NaN as a whole
+            c.cache[c.tables[0, r // 16], r % 16, 0, 130] = 0x7F
+        c.device().launch(form)
+        c.torch.cuda.synchronize()
+        o, lse = c.o[:T].double().cpu().numpy(), c.lse[:T].double().cpu().numpy()
+        args = (c.page, c.q.double().numpy(), c.idx, c.req, c.tables, c.scale)
+        with np.errstate(invalid="ignore"):
+            nan_o, nan_l = (np.isnan(x) for x in ref.attention(c.cache, *args)[:2])
+        assert nan_o.any() and nan_l.any() == (step == 1) and (step == 1 or not nan_o.all())
+        assert np.array_equal(np.isnan(o), nan_o) and np.array_equal(np.isnan(lse), nan_l)
+        wo, wl, vmax, amax = ref.attention(clean, *args)
+        delta = 2.0 ** -16 * amax
+        assert (np.abs(lse - wl) <= delta + 2.0 ** -22 * (8 + np.abs(wl)))[~nan_l].all()
+        bound = HALF["bf16"] * np.abs(wo) + (vmax * (2 * delta + 2.0 ** -11 + Kc * 2.0 ** -25 + 2.0 ** -19))[..., None]
+        assert (np.abs(o - wo) <= bound)[~nan_o].all()
