@@ -12,8 +12,9 @@ A decode step's kernels take a few microseconds, and so do a dozen tensors looke
 at from Python.  Once the library is loaded an ordinary call -- nothing wrong with
 it, the tensors on the current device, no stream given -- is checked and made by
 the module built from csrc/cache_calls.cpp (two plans 17 -> 5.7 us, an attention
-call 7.9 -> 2.8, a read 5.8 -> 2.6); what that returns None for is checked and made, or refused with
-the reason, here.
+call 7.9 -> 2.8, a read 5.8 -> 2.6); what that returns None for is checked and
+made, or refused with the reason, here.  Where the module was not built, every
+call is.
 """
 from __future__ import annotations
 
@@ -21,6 +22,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -110,7 +112,7 @@ def _row_type(name, t, types):
     return code
 
 
-_calls = None  # the module of ordinary calls, once the library is loaded
+_calls = None  # the module of ordinary calls, once the library is loaded; False where there is none
 
 
 def _load_calls(functions=None, host=False):
@@ -154,7 +156,12 @@ def _call(name, dev, stream, *args):
         s = stream.cuda_stream
     fn = getattr(binding.load(), name)
     if _calls is None:
-        _calls = _load_calls()
+        try:
+            _calls = _load_calls()
+        except (OSError, ImportError) as e:
+            _calls = False
+            warnings.warn(f"cache_calls is not used, the cache's calls take a few us more each: {e}", RuntimeWarning,
+                          stacklevel=3)
     with torch.cuda.device(dev):
         binding._check(fn(*args, s), name)
 
