@@ -1239,7 +1239,8 @@ int dsa_group_union_launch(const dsa_attention_cfg* cfg, const int32_t* idx, voi
   int st = dsa_sparse_attention_workspace(cfg, &need);
   if (st != DSA_OK) return st;
   if (cfg->tokens == 0) return DSA_OK;
-  if (!idx || !workspace || (((uintptr_t)workspace) & 15u) || workspace_bytes < need) return DSA_ERR_INVALID_ARG;
+  if (!idx && cfg->select > 0) return DSA_ERR_INVALID_ARG;  // lists of no entry may have no memory
+  if (!workspace || !workspace || (((uintptr_t)workspace) & 15u) || workspace_bytes < need) return DSA_ERR_INVALID_ARG;
   const int G = kRows / cfg->heads;
   const int groups = (cfg->tokens + G - 1) / G;
   const UnionShape U = union_shape(G, cfg->select, cfg->keys);

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from tests import cache_ref as ref
-from tests.test_gpu_cache import DEV, HALF, _Case
+from tests.test_gpu_cache import DEV, HALF, _Case, _mods
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +41,31 @@ def test_nan_value_scales_reach_their_dims(form, T, H, KV, Kc, ctx):
         assert (np.abs(lse - wl) <= delta + 2.0 ** -22 * (8 + np.abs(wl)))[~nan_l].all()
         bound = HALF["bf16"] * np.abs(wo) + (vmax * (2 * delta + 2.0 ** -11 + Kc * 2.0 ** -25 + 2.0 ** -19))[..., None]
         assert (np.abs(o - wo) <= bound)[~nan_o].all()
+
+
+@pytest.mark.parametrize("H,KV,P", [(8, 1, 4), (32, 2, 4), (8, 1, 9000), (16, 1, 0)])
+def test_prompt_lists_of_no_entry(H, KV, P):
+    torch, dsa = _mods()
+    cfg = dsa.cache_cfg(pages=4, page_size=16, kv_heads=KV)
+    cache = torch.full((dsa.dsa_cache_bytes(cfg),), 0xFF, dtype=torch.uint8, device=DEV)
+    q = torch.ones(21, H, 128, dtype=torch.bfloat16, device=DEV)
+    idx = torch.empty((21, 0), dtype=torch.int32, device=DEV)
+    o, lse = torch.full_like(q, 7.0), torch.full((21, H), 7.0, device=DEV)
+    ws = torch.empty(dsa.dsa_cache_attention_prompt_workspace(cfg, q, idx), dtype=torch.uint8, device=DEV)
+    dsa.dsa_cache_attention_prompt(cfg, cache, q, idx, torch.zeros(P, dtype=torch.int32, device=DEV), 0.1, ws, o, lse)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    assert dsa.dsa_cache_attention_status() == dsa.DSA_OK
+
+
+def test_union_of_lists_of_no_entry():
+    """The bf16 attention's lists of no entry, which share the union launch."""
+    torch, dsa = _mods()
+    q = torch.ones(21, 8, 128, dtype=torch.bfloat16, device=DEV)
+    k = torch.ones(70, 128, dtype=torch.bfloat16, device=DEV)
+    idx = torch.empty((21, 0), dtype=torch.int32, device=DEV)
+    cfg = dsa.attention_cfg(q, k, idx)
+    ws = torch.empty(dsa.dsa_sparse_attention_workspace(cfg), dtype=torch.uint8, device=DEV)
+    o, lse = torch.full((21, 8, 128), 7.0, device=DEV), torch.full((21, 8), 7.0, device=DEV)
+    dsa.dsa_sparse_attention(cfg, q, k, k, idx, 0.1, ws, o, lse)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    assert dsa.dsa_sparse_attention_status() == dsa.DSA_OK
