@@ -536,8 +536,8 @@ int dsa_cache_attention_prompt(const dsa_cache_cfg* cfg, int32_t tokens, int32_t
                                struct CUstream_st* stream);
 
 /* DSA_ERR_TIMEOUT once after a launch of dsa_cache_attention or
- * dsa_cache_attention_prompt gave up a wait (then cleared), else DSA_OK;
- * synchronises the device. */
+ * dsa_cache_attention_prompt on the current device gave up a wait (then
+ * cleared), else DSA_OK; synchronises the device, every stream of it. */
 int dsa_cache_attention_status(void);
 
 /* Static description of a status code. */

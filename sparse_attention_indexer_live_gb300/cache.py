@@ -18,6 +18,7 @@ call is.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -308,10 +309,11 @@ def dsa_cache_attention_prompt(cfg: dsa_cache_cfg, cache, q, idx, table, scale: 
           workspace.numel(), o.data_ptr(), lse.data_ptr())
 
 
-def dsa_cache_attention_status() -> int:
+def dsa_cache_attention_status(device=None) -> int:
     """DSA_OK, or DSA_ERR_TIMEOUT once after an attention kernel over the cache
-    gave up a wait (synchronises the device)."""
-    return int(binding.load().dsa_cache_attention_status())
+    gave up a wait on `device` (the current one, if None), which is synchronised."""
+    with torch.cuda.device(device) if device is not None else contextlib.nullcontext():
+        return int(binding.load().dsa_cache_attention_status())
 
 
 # ---------------------------------------------------------------------------

@@ -922,6 +922,8 @@ int dsa_cache_tile(const AttendParams& p, const uint8_t* records, bool bf16, cud
 
 extern "C" int dsa_cache_attention_status(void) {
   int v = 0, zero = 0;
+  // the copies alone wait for no stream but the default one and those that block it
+  if (cudaDeviceSynchronize() != cudaSuccess) return DSA_ERR_CUDA;
   if (cudaMemcpyFromSymbol(&v, g_cache_attn_error, sizeof(int)) != cudaSuccess) return DSA_ERR_CUDA;
   if (v && cudaMemcpyToSymbol(g_cache_attn_error, &zero, sizeof(int)) != cudaSuccess) return DSA_ERR_CUDA;
   return v ? DSA_ERR_TIMEOUT : DSA_OK;

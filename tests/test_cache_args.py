@@ -227,3 +227,22 @@ def test_struct_layout(tmp_path):
     out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
     assert [int(x) for x in out] == [ctypes.sizeof(C.dsa_cache_cfg), C.RECORD_BYTES] + [
         getattr(C.dsa_cache_cfg, f).offset for f in fields]
+
+
+def test_status_is_of_a_device(monkeypatch):
+    entered = []
+
+    class device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            entered.append(self.d)
+
+        def __exit__(self, *a):
+            entered.append("left")
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(C.binding, "load", lambda: type("L", (), dict(
+        dsa_cache_attention_status=staticmethod(lambda: entered.append("asked") or 4))))
+    assert C.dsa_cache_attention_status(1) == 4 and C.dsa_cache_attention_status() == 4
+    assert entered == [1, "asked", "left", "asked"]

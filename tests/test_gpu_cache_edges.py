@@ -69,3 +69,17 @@ def test_union_of_lists_of_no_entry():
     dsa.dsa_sparse_attention(cfg, q, k, k, idx, 0.1, ws, o, lse)
     assert (o == 0).all() and torch.isneginf(lse).all()
     assert dsa.dsa_sparse_attention_status() == dsa.DSA_OK
+
+
+def test_status_waits_for_every_stream():
+    c = _Case(20, 128, 1, 130, ctx=200, seed=3).device()
+    torch, dsa = c.torch, c.dsa
+    s = torch.cuda.Stream()
+    c.launch()
+    assert dsa.dsa_cache_attention_status() == dsa.DSA_OK
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200000000)  # 0.1 s
+        c.launch()
+    assert dsa.dsa_cache_attention_status() == dsa.DSA_OK
+    assert s.query(), "the status came before the launch it is asked about had ended"
+    c.check()
