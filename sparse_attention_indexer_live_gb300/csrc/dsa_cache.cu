@@ -532,15 +532,26 @@ int dsa_cache_plan(const dsa_cache_cfg* cfg, int32_t requests, int32_t table_wid
                       (int64_t)requests * table_width < ((int64_t)1 << 31);
   const auto kernel = narrow ? plan_kernel<int> : plan_kernel<long long>;
   const size_t smem = 5 * sizeof(int32_t) * (size_t)requests;
-  if (smem > 47 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           5 * (int)sizeof(int32_t) * kMaxRequests) != cudaSuccess) {
+  const bool large = smem > 47 * 1024;
+  const int most_smem = 5 * (int)sizeof(int32_t) * kMaxRequests;
+  if (large && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem) != cudaSuccess) {
     cudaGetLastError();
     return DSA_ERR_CUDA;
   }
-  if (nctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-    cudaGetLastError();
-    return DSA_ERR_CUDA;
+  if (nctas > 1) {
+    static int fits[64][2][2];  // by device, kernel and memory: the largest cluster, 0 before the first call
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+    int most = dev < 64 ? fits[dev][narrow][large] : 0;
+    if (!most) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        cudaGetLastError();
+        return DSA_ERR_CUDA;
+      }
+      most = cluster_that_fits(kernel, kPThreads, large ? most_smem : 47 * 1024, kMaxPlanCluster);
+      if (dev < 64) fits[dev][narrow][large] = most;
+    }
+    nctas = std::min(nctas, most);
   }
   return launch_dependent(kernel, nctas, threads, smem, nctas, (cudaStream_t)stream, p);
 }

@@ -42,6 +42,7 @@ struct AttendParams {
   void* o;
   float* lse;
   int32_t T, H, n, kv_heads, Kc, R, P, pages, shift;
+  int32_t sms;       // of the device
   int32_t chunks;    // groups of query heads a key/value head's are taken in
   float scale_log2;  // softmax scale * 2^k_shift * log2(e)
   float v_mul;       // 2^v_shift
@@ -51,11 +52,9 @@ struct AttendParams {
 // union records of groups of 128 / n tokens (dsa_group_union), whose keys are
 // positions of request 0; NULL: a token a tile, its own list.  n <= 128 rows.
 DSA_HIDDEN int dsa_cache_tile(const AttendParams& p, const uint8_t* records, bool bf16, cudaStream_t stream);
-// CTAs that each of `units` rows of tiles, `select` entries a token, is split over.
-DSA_HIDDEN int dsa_cache_tile_split(int64_t units, int32_t select);
-
-// SMs of the device.
-constexpr int kSms = 152;
+// CTAs that each of `units` rows of tiles, `select` entries a token, is split
+// over on `sms` SMs.
+DSA_HIDDEN int dsa_cache_tile_split(int64_t units, int32_t select, int32_t sms);
 
 #ifdef __CUDACC__
 
@@ -68,6 +67,30 @@ constexpr int kSms = 152;
 // plain loads: the read-only path (__ldg) may be taken ahead of the wait.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The most CTAs, of `most`, `most` / 2, ... 1, of a cluster of `kernel` for which
+// the current device has room: the rules below were measured on 152 SMs, and
+// another part, or a part of one, may have fewer SMs that can form a cluster.
+template <typename... P>
+int cluster_that_fits(void (*kernel)(P...), int threads, size_t smem, int most) {
+  for (; most > 1; most /= 2) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)most);
+    lc.blockDim = dim3((unsigned)threads);
+    lc.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)most;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &lc) == cudaSuccess && clusters > 0) break;
+    cudaGetLastError();
+  }
+  return most;
+}
 
 // Launch `kernel` on clusters of `cluster` CTAs, as above.
 template <typename... P, typename... A>

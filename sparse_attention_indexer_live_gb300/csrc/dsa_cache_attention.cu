@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
   }
   // (when CTAs share SMs, successors that are placed early share them unevenly:
   // 96 rows of 8 heads 16.8 us against 14.6, one row 5.7 against 6.3)
-  if (gridDim.x <= kSms) let_next_start();
+  if (gridDim.x <= p.sms) let_next_start();
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();  // the ring is free
 
@@ -602,6 +602,21 @@ int check_attention(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads, int
   return DSA_OK;
 }
 
+// SMs of the current device; 0 when it cannot be asked.
+int device_sms() {
+  static int known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) {
+    if (dev < 64 && known[dev]) return known[dev];
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) {
+      if (dev < 64) known[dev] = n;
+      return n;
+    }
+  }
+  cudaGetLastError();
+  return 0;
+}
+
 AttendParams make_params(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads, int32_t select, int32_t requests,
                          int32_t table_width, const uint8_t* cache, const void* q, const int32_t* idx,
                          const int32_t* token_req, const int32_t* tables, float scale, void* o, float* lse) {
@@ -622,6 +637,7 @@ AttendParams make_params(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads
   p.P = table_width;
   p.pages = cfg->pages;
   p.shift = log2_of(cfg->page_size);
+  p.sms = device_sms();
   p.scale_log2 = scale_log2_of(cfg, scale);
   p.v_mul = pow2f(cfg->v_shift);
   return p;
@@ -629,19 +645,22 @@ AttendParams make_params(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads
 
 template <int kNT, bool kBf16, int kStages>
 int launch_one(AttendParams p, int split, cudaStream_t s) {
-  static bool done[64];
+  static int fits[64];  // by device: the largest cluster, 0 before the first call
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
   const auto kernel = attend_kernel<kNT, kBf16, kStages>;
-  if (dev >= 64 || !done[dev]) {
+  int most = dev < 64 ? fits[dev] : 0;
+  if (!most) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem<kNT, kStages>(true)) !=
             cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
       cudaGetLastError();
       return DSA_ERR_CUDA;
     }
-    if (dev < 64) done[dev] = true;
+    most = cluster_that_fits(kernel, kThreads, attend_smem<kNT, kStages>(true), kMaxSplit);
+    if (dev < 64) fits[dev] = most;
   }
+  split = std::min(split, most);
   p.chunks = (p.n + kNT * 8 - 1) / (kNT * 8);
   return launch_dependent(kernel, (int64_t)p.T * p.kv_heads * p.chunks * split, kThreads,
                           attend_smem<kNT, kStages>(split > 1), split, s, p);
@@ -654,7 +673,7 @@ int launch_one(AttendParams p, int split, cudaStream_t s) {
 // 14.6 / 9.3, 80 over 4 20.9 / 13.1, 256 rows whole 28.8 / 27.5).
 template <int kNT, bool kBf16>
 int launch_staged(const AttendParams& p, int64_t ctas, int split, cudaStream_t s) {
-  return 10 * ctas <= 17 * kSms ? launch_one<kNT, kBf16, 4>(p, split, s) : launch_one<kNT, kBf16, 2>(p, split, s);
+  return 10 * ctas <= 17 * p.sms ? launch_one<kNT, kBf16, 4>(p, split, s) : launch_one<kNT, kBf16, 2>(p, split, s);
 }
 
 // CTAs of a row of this form: 8 heads a CTA, or 16.
@@ -663,7 +682,8 @@ int64_t warp_units(const AttendParams& p) {
   return (int64_t)p.T * p.kv_heads * ((p.n + wide - 1) / wide);
 }
 
-// Rows are split as far as the clusters run at once and the list is worth it.
+// Rows are split as far as the clusters run at once and the list is worth it (a
+// cluster for which the device has no room is halved at the launch).
 // Clusters of 16 find room only while each CTA has an SM of its own, the others
 // up to 2.6 CTAs an SM, 3.3 for 8 heads in fours.  2,048 entries of 8 heads, over
 // 1 / 2 / 4 / 8 CTAs: 32 rows 16.4 / 12.5 / 8.5 / 8.1 us, 48 rows 16.4 / 12.4 /
@@ -681,7 +701,7 @@ int64_t warp_units(const AttendParams& p) {
 int attend_split(const AttendParams& p) {
   const bool wide = p.n > 8;
   const int64_t units = warp_units(p);
-  auto room = [&](int c) { return (c == 16 ? 10 : c == 4 && !wide ? 33 : 26) * kSms / 10; };
+  auto room = [&](int c) { return (c == 16 ? 10 : c == 4 && !wide ? 33 : 26) * p.sms / 10; };
   auto least = [&](int c) { return c == 16 ? 1024 : c == 8 ? (wide ? 640 : 512) : c == 4 ? 768 : wide ? 2048 : 1024; };
   int split = kMaxSplit;
   while (split > 1 && (units * split > room(split) || p.Kc < least(split))) split /= 2;
@@ -701,15 +721,15 @@ int attend_split(const AttendParams& p) {
 bool wants_tiles(const AttendParams& p) {
   if (p.n <= 16) return false;
   const int64_t tile_units = (int64_t)p.T * p.kv_heads;
-  const int ts = dsa_cache_tile_split(tile_units, p.Kc);
+  const int ts = dsa_cache_tile_split(tile_units, p.Kc, p.sms);
   const int64_t tiles = (p.Kc + 128 * (int64_t)ts - 1) / (128 * (int64_t)ts);
-  const int64_t waves = (tile_units * ts + kSms - 1) / kSms;
+  const int64_t waves = (tile_units * ts + p.sms - 1) / p.sms;
   const double tile_us = waves * (4.7 + p.n / 40.0 + 1.2 * tiles) + (ts > 1 ? 1.5 : 0.0);
   const int s = attend_split(p);
-  const double ctas = (double)warp_units(p) * s, most = 3.0 * kSms;
+  const double ctas = (double)warp_units(p) * s, most = 3.0 * p.sms;
   const int64_t steps = (p.Kc + 128 * (int64_t)s - 1) / (128 * (int64_t)s);  // tiles of a warp
   double us = ctas <= most ? 4.3 + 0.006 * ctas + steps * (0.85 + 0.003 * ctas) : ctas / most * (7.0 + 2.2 * steps);
-  if (s > 1) us += 10 * ctas <= 17 * kSms ? 2.5 : 3.5;
+  if (s > 1) us += 10 * ctas <= 17 * p.sms ? 2.5 : 3.5;
   return tile_us < us;
 }
 
@@ -744,6 +764,7 @@ int dsa_cache_attention(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads,
     return DSA_ERR_INVALID_ARG;
   const AttendParams p = make_params(cfg, tokens, heads, select, requests, table_width, cache, q, idx, token_req, tables,
                                      scale, o, lse);
+  if (!p.sms) return DSA_ERR_CUDA;
   if (wants_tiles(p)) return dsa_cache_tile(p, nullptr, dtype == DSA_BF16, (cudaStream_t)stream);
   return launch_attend(p, dtype, (cudaStream_t)stream);
 }
@@ -774,11 +795,12 @@ int dsa_cache_attention_prompt(const dsa_cache_cfg* cfg, int32_t tokens, int32_t
   if (!workspace || ((uintptr_t)workspace & 15u) || workspace_bytes < need) return DSA_ERR_INVALID_ARG;
   dsa_attention_cfg u = {tokens, heads / cfg->kv_heads, (int32_t)std::min<int64_t>((int64_t)table_width * cfg->page_size, INT32_MAX),
                          kCacheDim, kCacheDim, select};
+  const AttendParams p = make_params(cfg, tokens, heads, select, 1, table_width, cache, q, idx, nullptr, table, scale, o,
+                                     lse);
+  if (!p.sms) return DSA_ERR_CUDA;
   st = dsa_group_union_launch(&u, idx, workspace, workspace_bytes, true, (cudaStream_t)stream);
   if (st != DSA_OK) return st;
-  return dsa_cache_tile(make_params(cfg, tokens, heads, select, 1, table_width, cache, q, idx, nullptr, table, scale, o,
-                                    lse),
-                        static_cast<const uint8_t*>(workspace), dtype == DSA_BF16, (cudaStream_t)stream);
+  return dsa_cache_tile(p, static_cast<const uint8_t*>(workspace), dtype == DSA_BF16, (cudaStream_t)stream);
 }
 
 }  // extern "C"

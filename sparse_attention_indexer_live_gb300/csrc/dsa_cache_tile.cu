@@ -866,11 +866,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
 
 template <bool kBf16, bool kUnion>
 int launch_tile(const TileParams& tp, int64_t units, int split, cudaStream_t s) {
-  static bool done[64];
+  static int fits[64];  // by device: the largest cluster, 0 before the first call
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
   const auto kernel = tile_kernel<kBf16, kUnion>;
-  if (dev >= 64 || !done[dev]) {
+  int most = dev < 64 ? fits[dev] : 0;
+  if (!most) {
     cudaFuncAttributes fa;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
         cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) {
@@ -879,8 +880,10 @@ int launch_tile(const TileParams& tp, int64_t units, int split, cudaStream_t s) 
     }
     // the register split needs the whole launch allocation it was sized for
     if (fa.numRegs < kLaunchRegs) return DSA_ERR_UNSUPPORTED;
-    if (dev < 64) done[dev] = true;
+    most = cluster_that_fits(kernel, kThreads, kSmem, kMaxSplit);
+    if (dev < 64) fits[dev] = most;
   }
+  split = std::min(split, most);
   return launch_dependent(kernel, units * split, kThreads, kSmem, split, s, tp);
 }
 
@@ -891,9 +894,9 @@ int launch_tile(const TileParams& tp, int64_t units, int split, cudaStream_t s) 
 // eight such CTAs, an SM each, find room for about half of the SMs: 64 heads,
 // 2,048 entries, 8 tokens 10.5 us over 8 CTAs, 10 tokens 12.7 over 4; 16 tokens over
 // 4 / 8, with a slower join than today's, 15.4 / 23.8.
-int dsa_cache_tile_split(int64_t units, int32_t select) {
+int dsa_cache_tile_split(int64_t units, int32_t select, int32_t sms) {
   int split = 1;
-  while (split < kMaxSplit && units * split * 2 <= (split * 2 == 8 ? kSms / 2 : kSms) &&
+  while (split < kMaxSplit && units * split * 2 <= (split * 2 == 8 ? sms / 2 : sms) &&
          (int64_t)select >= (int64_t)split * 4 * kTile)
     split *= 2;
   return split;
@@ -913,7 +916,7 @@ int dsa_cache_tile(const AttendParams& p, const uint8_t* records, bool bf16, cud
   tp.negate = p.scale_log2 < 0.f;
   if (tp.negate) tp.a.scale_log2 = -p.scale_log2;
   const int64_t units = (int64_t)((p.T + tp.G - 1) / tp.G) * p.kv_heads;
-  const int split = dsa_cache_tile_split(units, p.Kc);
+  const int split = dsa_cache_tile_split(units, p.Kc, p.sms);
   if (units * split >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
   if (records)
     return bf16 ? launch_tile<true, true>(tp, units, split, stream) : launch_tile<false, true>(tp, units, split, stream);
