@@ -32,6 +32,14 @@ inline int log2_of(int x) {
 
 inline int launched() { return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
 
+// Softmax weights are taken against 2^-kLift of the running maximum, which moves
+// only when a score's weight would pass 2^kMost.  They enter the second product
+// in f16: the largest is between 2^7 and 2^15, so that what f16 does not hold of the
+// small ones is 2^-32 of it each (against the maximum itself 2^-25: a first entry
+// 2^25.5 above the 2^20 after it left their 2 % out of o).
+constexpr float kLift = 7.f;
+constexpr float kMost = 15.f;
+
 // What both forms of the attention take.
 struct AttendParams {
   const uint8_t* cache;

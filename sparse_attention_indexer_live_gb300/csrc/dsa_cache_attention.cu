@@ -4,7 +4,7 @@
 //
 // For token t and head h of key/value head h / n, over the positions j of t's
 // list: s_j = scale q . k_j, o = sum_j 2^(c s_j - m) v_j / sum_j 2^(c s_j - m)
-// with c = log2 e and m a running maximum.  A list is one pass: 144 bytes a
+// with c = log2 e and m from a running maximum (dsa_cache.h).  A list is one pass: 144 bytes a
 // position, of which every scale and code is expanded once for 8 (or 16) heads.
 //
 // What bounds it: a batch (512 tokens x 4 key/value heads x 8 heads, 1,001
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
   const uint32_t v0 = ring + stage_row(2 * t4) * kRec, v1 = ring + stage_row(2 * t4 + 1) * kRec;
   const uint32_t vc = kRecV + 8 * g, vs = kRecVs + g;
 
-  // nm: minus the maximum that weights are taken against
+  // nm: minus what weights are taken against
   float nm[kNT][2], l[kNT][2], o[kNT][8][4];
 #pragma unroll
   for (int nt = 0; nt < kNT; ++nt) {
@@ -429,9 +429,8 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
             y[f][nt][c] = s[f][nt][c] + nm[nt][c & 1];
             top = fmaxf(top, y[f][nt][c]);
           }
-      // The maximum moves only when a score is above it by more than 8 (weights
-      // stay below 2^8, within f16), and at a head's first score.
-      if (__any_sync(0xFFFFFFFFu, !(top <= 8.f))) {
+      // nm moves at a head's first score, and when a weight would pass 2^kMost
+      if (__any_sync(0xFFFFFFFFu, !(top <= kMost))) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -440,9 +439,10 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-            if (x + nm[nt][c] > 8.f) {
-              const float alpha = nm[nt][c] == kNone ? 0.f : ex2(-nm[nt][c] - x);
-              nm[nt][c] = -x;
+            if (x + nm[nt][c] > kMost) {
+              const float next = kLift - x;
+              const float alpha = nm[nt][c] == kNone ? 0.f : ex2(next - nm[nt][c]);
+              nm[nt][c] = next;
               l[nt][c] *= alpha;
 #pragma unroll
               for (int i8 = 0; i8 < 8; ++i8) {

@@ -629,9 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
         for (int j = 0; j < 32; ++j)
           if (!(mw & (1u << j))) sc[c][j] = __float_as_uint(-INFINITY);
       }
-      // One pass: weights 2^(s c - m) against the running maximum m, which
-      // moves only when the row's maximum rises by more than 8 (the weights
-      // stay below 2^8, within f16); then the pass is redone and O rescaled.
+      // One pass: weights 2^(s c - m), m from a running maximum (dsa_cache.h): it
+      // moves only when a weight would pass 2^kMost; then the pass is redone and O
+      // rescaled.
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       float lsum;
       const uint32_t p_addr = lane_base + ss * 128 + 64 * hf;
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
             if (track) {
               upk2(ffma2(pk2(s0, s1), cc, mm), x0, x1);
               upk2(ffma2(pk2(s2, s3), cc, mm), x2, x3);
-            } else {  // the products rounded as in the maximum: its weight is 1 at any magnitude
+            } else {  // the products rounded as in the maximum: its weight is right at any magnitude
               x0 = __fadd_rn(__fmul_rn(s0, c2), -m_eff);
               x1 = __fadd_rn(__fmul_rn(s1, c2), -m_eff);
               x2 = __fadd_rn(__fmul_rn(s2, c2), -m_eff);
@@ -679,15 +679,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
       xch[((i & 1) * 2 + hf) * 128 + r] = mine;
       named_sync(pair_bar, 64);
       const float other = xch[((i & 1) * 2 + (hf ^ 1)) * 128 + r];
-      const float m_new = fmaxf(m_used, fmaxf(mine, other));
-      const bool redo = m_used == -INFINITY ? m_new > -INFINITY : m_new > m_used + 8.f;
+      const float m_new = fmaxf(mine, other);
+      const bool redo = m_used == -INFINITY ? m_new > -INFINITY : m_new - m_used > kMost;
       float alpha = 1.f;
       // (and always for scores so large that the fused exponent is off: the
       // product's rounding, 2^-24 of it, is not the maximum's)
       if (__any_sync(0xFFFFFFFFu, redo || fabsf(m_used) > 65536.f)) {
         if (redo) {
-          if (m_used > -INFINITY) alpha = ex2(m_used - m_new);
-          m_used = m_new;
+          const float next = m_new - kLift;
+          if (m_used > -INFINITY) alpha = ex2(m_used - next);
+          m_used = next;
         }
         tst_wait();  // two stores to the same columns keep no order of their own
         weights(m_used == -INFINITY ? 0.f : m_used, false);

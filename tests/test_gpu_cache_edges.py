@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from tests import cache_ref as ref
-from tests.test_gpu_cache import DEV, HALF, _Case, _mods
+from tests.test_gpu_cache import DEV, HALF, _Case, _mods, _type
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,34 @@ def test_status_waits_for_every_stream():
     assert dsa.dsa_cache_attention_status() == dsa.DSA_OK
     assert s.query(), "the status came before the launch it is asked about had ended"
     c.check()
+
+
+@pytest.mark.parametrize("H,KV,T,dtype", [(512, 64, 4, "f16"), (1024, 64, 4, "bf16"), (2560, 20, 4, "f16")])
+def test_long_lists_of_small_weights(H, KV, T, dtype):
+    """2^20 entries, of which the first outweighs each of the others by 2^25.5 and
+    all of them together by 45: what they bring is in o as it is in lse.  The
+    bound is the other tests', its term for weights below f16's normal range
+    against a largest weight of 2^7 at least, n 2^-32, and what so long a list
+    adds: a thread sums n / 64 weights at most one after another (2^-24 of the sum
+    each), a product n / 16 times 16 of them (2^-23 of what o has by then)."""
+    torch, dsa = _mods()
+    n, page = 1 << 20, 64
+    k, v = np.zeros((64, 128)), np.full((64, 128), 6.0)
+    k[0], v[0] = 6.0, 0.0  # exact in 4 bits
+    cfg = dsa.cache_cfg(pages=1, page_size=page, kv_heads=KV)
+    cache = torch.from_numpy(np.repeat(ref.pack(k, v)[:, None], KV, 1).reshape(-1)).to(DEV)
+    q = torch.ones(T, H, 128, dtype=_type(torch, dtype), device=DEV)
+    idx = (torch.arange(n, device=DEV) % 63 + 1).int()
+    idx[0] = 0
+    o, lse = torch.empty_like(q), torch.empty(T, H, device=DEV)
+    score = 25.5 * np.log(2.0)
+    dsa.dsa_cache_attention(cfg, cache, q, idx.repeat(T, 1), torch.zeros(T, dtype=torch.int32, device=DEV),
+                            torch.zeros((1, 1), dtype=torch.int32, device=DEV), score / 768, o, lse)
+    rest = (n - 1) * np.exp(-score)
+    wo, wl = 6.0 * rest / (1 + rest), score + np.log1p(rest)
+    delta = 2.0 ** -16 * score
+    total = n / 64 * 2.0 ** -24
+    assert np.abs(lse.double().cpu().numpy() - wl).max() <= delta + total + 2.0 ** -22 * (8 + wl)
+    err = np.abs(o.double().cpu().numpy() - wo).max()
+    assert err <= (HALF[dtype] + total + n / 16 * 2.0 ** -23) * wo + 6.0 * (
+        2 * delta + 2.0 ** -11 + n * 2.0 ** -32 + 2.0 ** -19), err
