@@ -4,6 +4,8 @@ The work runs in hand-written sm_103a CUDA kernels behind a C ABI
 (include/dsa_select.h, built by ``build.build()``); this package is the thin
 Python binding over it.
 """
+import importlib.util
+
 from .binding import (attention_cfg, dsa_attention_cfg, dsa_group_union, dsa_sparse_attention,
                       dsa_group_union_ranges, dsa_sparse_attention_ranges,
                       dsa_sparse_attention_ranges_workspace, ranges_attention_cfg,
@@ -28,13 +30,13 @@ __all__ = ["DSA_OK", "DSA_ERR_INVALID_ARG", "DSA_ERR_UNSUPPORTED", "DSA_ERR_CUDA
            "Shard", "ShardedSelector", "shard_rows", "attention_cfg", "dsa_attention_cfg",
            "dsa_group_union", "dsa_sparse_attention_workspace", "dsa_sparse_attention",
            "dsa_sparse_attention_status", "ranges_attention_cfg", "dsa_sparse_attention_ranges_workspace",
-           "dsa_group_union_ranges", "dsa_sparse_attention_ranges", "PagedCache", "cache_cfg", "dsa_cache_cfg",
-           "dsa_cache_bytes", "dsa_cache_plan", "dsa_cache_write", "dsa_cache_read", "dsa_cache_attention",
-           "dsa_cache_attention_prompt", "dsa_cache_attention_prompt_workspace", "dsa_cache_attention_status"]
+           "dsa_group_union_ranges", "dsa_sparse_attention_ranges"]
 
 _CACHE = ("PagedCache", "cache_cfg", "dsa_cache_cfg", "dsa_cache_bytes", "dsa_cache_plan", "dsa_cache_write",
           "dsa_cache_read", "dsa_cache_attention", "dsa_cache_attention_prompt",
           "dsa_cache_attention_prompt_workspace", "dsa_cache_attention_status")
+if importlib.util.find_spec("torch") is not None:  # import * takes the names below, and with them torch
+    __all__ += _CACHE
 
 
 def __getattr__(name):

@@ -2,6 +2,8 @@
 load, the library is built all the same and the calls go through ctypes."""
 import contextlib
 import os
+import subprocess
+import sys
 import types
 
 import pytest
@@ -53,3 +55,16 @@ def test_calls_without_the_module(tmp_path, monkeypatch, file):
         C.dsa_cache_read(cfg, cache, i32(3), rows, rows)
     C.dsa_cache_read(cfg, cache, i32(3), rows, rows)  # and is not looked for again
     assert len(seen) == 2 and seen[0][1:3] == (3, 2) and seen[0][-1] == 77
+
+
+def test_import_star_without_torch():
+    """A Python without torch (-S: without its site packages) gets every name but the cache's."""
+    root = os.path.dirname(B.PKG)
+    code = (f"import sys; sys.path.insert(0, {root!r})\nfrom importlib.util import find_spec\n"
+            "print(find_spec('torch') is None)\nfrom sparse_attention_indexer_live_gb300 import *\n"
+            "print(DSA_OK, dsa_select_topk.__name__, 'PagedCache' in globals())")
+    out = subprocess.run([sys.executable, "-S", "-c", code], capture_output=True, text=True, check=True).stdout.split()
+    if out[0] != "True":
+        pytest.skip("torch is part of this Python")
+    assert out[1:] == ["0", "dsa_select_topk", "False"]
+    assert set(C.__dict__) >= {n for n in dsa.__all__ if "cache" in n.lower()} and "PagedCache" in dsa.__all__
