@@ -349,6 +349,8 @@ class PagedCache:
         [tokens], first and status.  A graph that captured steps of one size
         stays good when other sizes follow: steps share one memory, and what
         they have outgrown is kept."""
+        if tokens < 0:
+            raise ValueError(f"tokens: {tokens}")
         if tokens != self.slots.numel():
             if tokens > self._maps[-1].shape[1]:
                 room = max(tokens, 2 * self._maps[-1].shape[1])

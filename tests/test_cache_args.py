@@ -246,3 +246,14 @@ def test_status_is_of_a_device(monkeypatch):
         dsa_cache_attention_status=staticmethod(lambda: entered.append("asked") or 4))))
     assert C.dsa_cache_attention_status(1) == 4 and C.dsa_cache_attention_status() == 4
     assert entered == [1, "asked", "left", "asked"]
+
+
+def test_a_step_of_negative_size(monkeypatch):
+    planned = []
+    monkeypatch.setattr(C, "dsa_cache_plan", lambda *a: planned.append(a))
+    c = C.PagedCache.__new__(C.PagedCache)
+    c._maps = [torch.empty((3, 64), dtype=torch.int32)]
+    c.slots = c._maps[0][2, :5]
+    with pytest.raises(ValueError, match="tokens"):
+        c.step(None, None, -1)
+    assert not planned and c.slots.numel() == 5
