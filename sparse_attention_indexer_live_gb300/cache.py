@@ -52,6 +52,7 @@ def cache_cfg(*, pages, page_size=64, kv_heads=1, k_shift=0, v_shift=0) -> dsa_c
 
 def dsa_cache_bytes(cfg: dsa_cache_cfg) -> int:
     """Bytes of the cache `cfg` describes."""
+    _cfg(cfg)
     n = ctypes.c_size_t(0)
     binding._check(binding.load().dsa_cache_bytes(ctypes.byref(cfg), ctypes.byref(n)), "dsa_cache_bytes")
     return int(n.value)
@@ -286,10 +287,16 @@ def dsa_cache_attention(cfg: dsa_cache_cfg, cache, q, idx, token_req, tables, sc
 
 def dsa_cache_attention_prompt_workspace(cfg: dsa_cache_cfg, q, idx) -> int:
     """Workspace bytes of dsa_cache_attention_prompt for q [T, H, 128] and idx [T, Kc]."""
+    _cfg(cfg)
+    for name, t, dims in (("q", q, 3), ("idx", idx, 2)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+        if t.dim() != dims:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {dims} dims")
     n = ctypes.c_size_t(0)
     binding._check(binding.load().dsa_cache_attention_prompt_workspace(
-        ctypes.byref(cfg), q.shape[0], q.shape[1], idx.shape[1], ctypes.byref(n)),
-        "dsa_cache_attention_prompt_workspace")
+        ctypes.byref(cfg), _count("q", q.shape[0]), _count("q", q.shape[1]), _count("idx", idx.shape[1]),
+        ctypes.byref(n)), "dsa_cache_attention_prompt_workspace")
     return int(n.value)
 
 

@@ -257,3 +257,19 @@ def test_a_step_of_negative_size(monkeypatch):
     with pytest.raises(ValueError, match="tokens"):
         c.step(None, None, -1)
     assert not planned and c.slots.numel() == 5
+
+
+def test_sizes_are_asked_with_a_cache_cfg(lib):
+    q, idx = torch.zeros(5, 16, 128), torch.zeros(5, 64, dtype=torch.int32)
+    assert C.dsa_cache_attention_prompt_workspace(cfg(), q, idx) == 16 + 2 * 16 * 64 * 4
+    for other in (None, dsa.dsa_attention_cfg(1, 8, 10, 128, 128, 4), (ctypes.c_int32 * 5)(1, 16, 1, 0, 0)):
+        with pytest.raises(TypeError):
+            C.dsa_cache_bytes(other)
+        with pytest.raises(TypeError):
+            C.dsa_cache_attention_prompt_workspace(other, q, idx)
+    with pytest.raises(TypeError):
+        C.dsa_cache_attention_prompt_workspace(cfg(), q, None)
+    wide = torch.zeros(1, dtype=torch.int32).expand(5, 2 ** 32 + 4)  # not 4 entries a list
+    for a in ((q[0], idx), (q, idx[0]), (q, wide)):
+        with pytest.raises(ValueError):
+            C.dsa_cache_attention_prompt_workspace(cfg(), *a)
