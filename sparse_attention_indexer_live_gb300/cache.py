@@ -47,7 +47,11 @@ def cache_cfg(*, pages, page_size=64, kv_heads=1, k_shift=0, v_shift=0) -> dsa_c
     """A cache's shape: `pages` pages of `page_size` (a power of two) positions
     of `kv_heads` key/value heads; keys are stored divided by 2^k_shift, values
     by 2^v_shift."""
-    return dsa_cache_cfg(pages=pages, page_size=page_size, kv_heads=kv_heads, k_shift=k_shift, v_shift=v_shift)
+    values = dict(pages=pages, page_size=page_size, kv_heads=kv_heads, k_shift=k_shift, v_shift=v_shift)
+    for name, n in values.items():
+        if not -1 << 31 <= n < 1 << 31:  # the structure would keep its low 32 bits
+            raise ValueError(f"{name}: {n} is more than 32 bits hold")
+    return dsa_cache_cfg(**values)
 
 
 def dsa_cache_bytes(cfg: dsa_cache_cfg) -> int:

@@ -273,3 +273,11 @@ def test_sizes_are_asked_with_a_cache_cfg(lib):
     for a in ((q[0], idx), (q, idx[0]), (q, wide)):
         with pytest.raises(ValueError):
             C.dsa_cache_attention_prompt_workspace(cfg(), *a)
+
+
+@pytest.mark.parametrize("name", ["pages", "page_size", "kv_heads", "k_shift", "v_shift"])
+def test_cfg_numbers_past_32_bits(name):
+    for n in (2 ** 32 + 1, 2 ** 31, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match=name):
+            cfg(**{name: n})
+    assert getattr(cfg(**{name: 2 ** 31 - 1}), name) == 2 ** 31 - 1  # the library's to refuse
