@@ -1,12 +1,18 @@
 """The paged 4-bit cache where its forms, types and plans could differ from their
 definition, against the plain forms of tests/cache_ref.py."""
+import subprocess
+import sys
+import textwrap
+
 import numpy as np
 import pytest
 
 from tests import cache_ref as ref
-from tests.test_gpu_cache import DEV, HALF, _Case, _mods, _type
+from tests.test_gpu_cache import DEV, HALF, _Case, _mods, _run_plan, _same_plan, _type
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("form,T,H,KV,Kc,ctx", [
@@ -114,3 +120,77 @@ def test_long_lists_of_small_weights(H, KV, T, dtype):
     err = np.abs(o.double().cpu().numpy() - wo).max()
     assert err <= (HALF[dtype] + total + n / 16 * 2.0 ** -23) * wo + 6.0 * (
         2 * delta + 2.0 ** -11 + n * 2.0 ** -32 + 2.0 ** -19), err
+
+
+@pytest.mark.parametrize("fresh", [32, 33, 300000])
+def test_plans_whose_sums_pass_32_bits(fresh):
+    """8,192 requests and 262,144 tokens: filled exactly, passed by 8,192, and with
+    counts whose sum is past 2^31."""
+    torch, dsa = _mods()
+    R, T, page, P = 8192, 1 << 18, 4096, 80
+    rng = np.random.default_rng(fresh)
+    lens = np.minimum(fresh + rng.integers(0, 20000, R), P * page)
+    held = np.minimum(rng.integers(0, 4, R), P)
+    tables = np.where(np.arange(P)[None, :] < held[:, None], np.arange(R * P).reshape(R, P) % 70000, -1)
+    free = rng.permutation(70000)
+    args = (page, 70000, lens, np.full(R, fresh), tables, held, free, 60000, T)
+    want = ref.plan(*args)
+    assert want["status"][0] == (0 if fresh == 32 else 3)
+    _same_plan(_run_plan(torch, dsa, *args), want)
+
+
+@pytest.mark.parametrize("dtype,k_shift,v_shift", [("bf16", 3, -9), ("bf16", -32, 32), ("f16", 2, -3), ("f16", -5, 4)])
+def test_shifts_of_16_bit_rows(dtype, k_shift, v_shift):
+    torch, dsa = _mods()
+    dt = _type(torch, dtype)
+    shift = torch.tensor([2.0 ** k_shift, 2.0 ** v_shift], dtype=torch.float64).view(2, 1, 1, 1)
+    g = torch.Generator().manual_seed(7)
+    rows = (torch.randn(2, 40, 2, 128, generator=g).to(dt).double() * shift).to(dt)
+    x = (rows.double() / shift).numpy()
+    cfg = dsa.cache_cfg(pages=10, page_size=4, kv_heads=2, k_shift=k_shift, v_shift=v_shift)
+    cache = torch.zeros(dsa.dsa_cache_bytes(cfg), dtype=torch.uint8, device=DEV)
+    slots = torch.arange(40, dtype=torch.int32, device=DEV)
+    dsa.dsa_cache_write(cfg, *rows.to(DEV).unbind(0), slots, cache)
+    rec = ref.pack(x[0], x[1])
+    assert np.array_equal(cache.cpu().numpy().reshape(rec.shape), rec)
+    out = torch.empty(2, 40, 2, 128, dtype=dt, device=DEV)
+    dsa.dsa_cache_read(cfg, cache, slots, *out.unbind(0))
+    want = torch.from_numpy(np.stack(ref.expand(rec))) * shift
+    assert torch.equal(out.cpu(), want.to(dt))
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first use of every kernel is in a capture: the graph gives
+    what the calls give without one."""
+    _mods()
+    script = textwrap.dedent(f"""
+        import sys
+        sys.path.insert(0, {ROOT!r})
+        import torch
+        import sparse_attention_indexer_live_gb300 as dsa
+        d = dict(dtype=torch.int32, device="cuda:0")
+        gen = torch.Generator("cuda:0").manual_seed(1)
+        R, T = 4, 9000  # a plan of several CTAs
+        lens = torch.tensor([4000, 3000, 1500, 500], **d)
+        rows = torch.randn(2, T, 1, 128, device="cuda:0", generator=gen).half()
+        lists = torch.arange(2048, **d).repeat(32, 1).contiguous()
+        qs = [torch.randn(n, h, 128, device="cuda:0", generator=gen).half() for n, h in ((1, 8), (16, 16), (20, 128), (32, 8))]
+        def run():
+            c = dsa.PagedCache(requests=R, pages=200, pages_per_request=100)
+            c.step(lens, lens, T)
+            c.store(rows[0], rows[1])
+            out = [c.attend(q, lists[:len(q)], 0.1) for q in qs] + [c.attend(qs[3], lists, 0.1, request=0)]
+            return [x for pair in out for x in pair] + list(c.fetch(c.slots)) + [c.status, c.data]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = run()
+        g.replay()
+        torch.cuda.synchronize()
+        want = run()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert want[-2].tolist() == [0, 0, T, 200 - 63 - 47 - 24 - 8], want[-2].tolist()
+        print("same")
+    """)
+    res = subprocess.run([sys.executable, "-c", script], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and res.stdout.split()[-1] == "same", res.stderr[-2000:]
