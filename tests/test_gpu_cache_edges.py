@@ -1,5 +1,6 @@
 """The paged 4-bit cache where its forms, types and plans could differ from their
 definition, against the plain forms of tests/cache_ref.py."""
+import os
 import subprocess
 import sys
 import textwrap
