@@ -77,7 +77,14 @@ constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_
 constexpr uint32_t kIdescPV = kIdesc | (1u << 16);
 constexpr int kMaxSplit = 8;
 constexpr uint32_t kNoRecord = 0xFFFFFFFFu;
+// Test builds shorten the waits and starve one barrier, so that they run out.
+#ifdef DSA_CACHE_TEST_WAIT_CYCLES
+constexpr long long kWaitCycles = DSA_CACHE_TEST_WAIT_CYCLES;
+constexpr uint32_t kQArrivals = 257;  // one more than there are
+#else
 constexpr long long kWaitCycles = 4000000000ll;  // ~2 s
+constexpr uint32_t kQArrivals = 256;
+#endif
 
 __device__ int g_cache_attn_error;
 __shared__ int s_abort;
@@ -323,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
   let_next_start();
   if (threadIdx.x == 0) {
     s_abort = s_nan = 0;
-    bar_init(qfull, 256);
+    bar_init(qfull, kQArrivals);
     for (int i = 0; i < kKStages; ++i) {
       bar_init(&kfull[i], 4);
       bar_init(&kempty[i], 1);
