@@ -500,9 +500,10 @@ int dsa_cache_read(const dsa_cache_cfg* cfg, int32_t tokens, int32_t dtype, cons
  *   q, o    [tokens, heads, 128] of one type, DSA_BF16 or DSA_F16, 16-byte
  *           aligned;  lse  f32 [tokens, heads]
  *   scale   of any sign; scale * 2^k_shift * log2(e) is finite in f32
- * Scores and sums are held in fp32; the softmax weights and the expanded rows
- * enter the products in f16 (the rows exactly; a weight is off by 2^-11 of it,
- * or by 2^-32 of the row's largest), o is rounded once.  A NaN key
+ * Scores and sums are held in fp32; q, the softmax weights and the expanded rows
+ * enter the products in f16 (the rows exactly, and q but for elements below
+ * 2^-26 of a row's largest; a weight is off by 2^-11 of it, or by 2^-32 of the
+ * row's largest), o is rounded once.  A NaN key
  * scale makes the rows that attend to its record NaN, o and lse; a NaN value
  * scale its 16 dims of their o, and nothing else.  Few rows
  * split their lists over a cluster of CTAs; the order of every sum is fixed,

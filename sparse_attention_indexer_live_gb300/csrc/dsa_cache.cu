@@ -1,11 +1,13 @@
 // dsa_cache.cu -- the paged 4-bit key/value cache: page plans from request
 // lengths, rows stored and rows read back (declared in include/dsa_select.h).
 //
-// Plans are latency: one launch, a prefix sum over the requests and a look-up a
-// token; 2.6 us for 96 tokens of 48 requests, 5.7 us for 66,016 tokens of 512.
+// A small plan is latency: one launch, a prefix sum over the requests and a
+// look-up a token, 2.9 us for 96 tokens of 48 requests; a large one is half that
+// and half the tokens' maps on one cluster's 16 SMs, 6.2 us for 66,016 tokens of 512.
 // Rows are bandwidth: 65,536 tokens x 2 heads of f16 stored and read back in 27.1
 // us (6.4 TB/s, 0.94 of the measured copy), 262,144 rows read as bf16 in 28.0 us
-// (6.2 TB/s, 0.91).
+// (6.2 TB/s, 0.91); of f32 read in 24.8 us (0.91) and stored in 27.9 (0.81: 17
+// divisions a thread that 16-bit rows do not have).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -521,9 +523,9 @@ int dsa_cache_plan(const dsa_cache_cfg* cfg, int32_t requests, int32_t table_wid
   p.slots = slots;
   p.status = status;
   // Four tokens of a thread; a CTA of up to 1,024 threads, then more of them in
-  // one cluster, as many as there are tokens for (66,016 tokens 6.7 us over 8 CTAs,
-  // 5.7 over 16).  Small steps take small CTAs: 96 tokens of 48 requests 3.0 us with
-  // 128 threads, 5.4 with 1,024.
+  // one cluster, as many as there are tokens for (66,016 tokens 8.2 us over 8 CTAs,
+  // 6.2 over 16).  Small steps take small CTAs: 96 tokens of 48 requests 2.9 us with
+  // 128 threads, 3.3 with 1,024.
   const int64_t want = std::max<int64_t>(requests, ((int64_t)tokens + 3) / 4);
   const int threads = (int)std::min<int64_t>(kPThreads, std::max<int64_t>(128, (want + 31) / 32 * 32));
   int nctas = 1;

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 2 : kNT == 1 ? 4 : 3)
 
   // q as the B operand: thread (g, t4) holds head g's dims 32 t4 .. 32 t4 + 31,
   // scaled by a power of two that puts the row's largest element at 2^12, so
-  // that bf16 rows of any magnitude are exact in f16
+  // that rows of any magnitude are exact in f16, elements down to 2^-26 of it
   uint32_t qf[kNT][16];
   float sc[kNT][2];  // exponent factor of heads 2 t4 and 2 t4 + 1
 #pragma unroll

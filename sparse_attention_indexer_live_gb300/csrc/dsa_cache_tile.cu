@@ -14,19 +14,20 @@
 //     with Q in TMEM as the A operand, into one of two buffers, and O += P V with
 //     P in TMEM over the scores it came from and V as an N-major operand;
 //   * two softmax warpgroups, each half of the columns of every row: one pass
-//     against a running maximum that moves rarely; weights are rounded to f16,
-//     the sum takes them unrounded.
+//     against a base that follows the running maximum and moves rarely; weights
+//     are rounded to f16, the sum takes them unrounded.
 // Splits of a row's tiles over a cluster are joined through distributed shared
 // memory.  Every mbarrier wait is bounded by a clock limit.
 //
 // What bounds it: neither HBM (2,048 tokens of 8 heads over a million positions:
-// 90 MB read in 52 us) nor the tensor cores (16 products of 128 x 128 x 16 a
+// 90 MB read in 54 us) nor the tensor cores (16 products of 128 x 128 x 16 a
 // tile, 68 cycles each at the peak rate: 1,090 of a tile's 2,700 cycles), but
 // the softmax's chain within a tile -- TMEM load, masks, maximum, exponentials,
 // TMEM store, each 150 to 900 cycles -- at five warps a scheduler.  Measured for
-// the same chunk, with the union's 18 us: 71.2 us; codes through registers in
-// place of the ring 79.9; sixteen softmax warps of 32 columns 77.6; a warpgroup a
-// tile with an O each 74.2, with tiles of 64 and four S buffers 73.0.
+// the same chunk, with the union's 18 us: 72.0 us.  Against 72.5 at the time:
+// codes through registers in place of the ring 79.9; sixteen softmax warps of 32
+// columns 77.6; a warpgroup a tile with an O each 74.2, with tiles of 64 and four S
+// buffers 77.8, and two MMA warps besides 73.0.
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const TileParams tp) 
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int pair_bar = 1 + (sw & 3);  // named barrier of the two warps sharing these rows
     // Q: this row's half as f16, scaled by a power of two that puts the row's
-    // largest element at 2^12 (bf16 rows of any magnitude are then exact)
+    // largest element at 2^12 (elements down to 2^-26 of it are then exact)
     float c2;
     {
       uint32_t w[32];
