@@ -503,11 +503,10 @@ int dsa_cache_read(const dsa_cache_cfg* cfg, int32_t tokens, int32_t dtype, cons
  * Scores and sums are held in fp32; q, the softmax weights and the expanded rows
  * enter the products in f16 (the rows exactly, and q but for elements below
  * 2^-26 of a row's largest; a weight is off by 2^-11 of it, or by 2^-32 of the
- * row's largest), o is rounded once.  A NaN key
- * scale makes the rows that attend to its record NaN, o and lse; a NaN value
- * scale its 16 dims of their o, and nothing else.  Few rows
- * split their lists over a cluster of CTAs; the order of every sum is fixed,
- * so results repeat bit for bit.
+ * row's largest), o is rounded once.  A NaN key scale makes the rows that attend
+ * to its record NaN, o and lse; a NaN value scale its 16 dims of their o, and
+ * nothing else.  Few rows split their lists over a cluster of CTAs; the order of
+ * every sum is fixed, so results repeat bit for bit.
  */
 int dsa_cache_attention(const dsa_cache_cfg* cfg, int32_t tokens, int32_t heads, int32_t select,
                         int32_t requests, int32_t table_width, int32_t dtype, const uint8_t* cache,
