@@ -541,6 +541,139 @@ int dsa_cache_attention_prompt(const dsa_cache_cfg* cfg, int32_t tokens, int32_t
  * cleared), else DSA_OK; synchronises the device, every stream of it. */
 int dsa_cache_attention_status(void);
 
+/*
+ * Paged key/value cache held in 16 bits: a step's rotated rows stored, causal
+ * attention of its tokens to everything before them, and attention to the pages
+ * that each token's queries score highest.  dsa_cache_plan above serves this
+ * cache too (its slots, ends, first and tables number positions and pages, not
+ * records).  This library's own design.
+ *
+ * Layout.  k_cache and v_cache [pages, page_size, kv_heads, 128], means [pages,
+ * kv_heads, 128], all of cfg's type, each 16-byte aligned.  Request r's position
+ * p is row p % page_size of page tables[r, p / page_size].  The means hold each
+ * full page's mean key; what they hold of other pages is not read.
+ *   pages      >= 0; pages * page_size < 2^31
+ *   page_size  16, 32, 64 or 128
+ *   kv_heads   1 .. 64
+ *   dtype      DSA_BF16 or DSA_F16
+ * A cfg outside these limits gives DSA_ERR_INVALID_ARG (DSA_ERR_UNSUPPORTED for
+ * other powers of two of page_size and more kv_heads).
+ *
+ * A step (dsa_kv_attention, dsa_kv_select, dsa_kv_block_attention).  Tokens
+ * first[r] .. first[r + 1] - 1 are request r's newest, lens[r] its length with
+ * them: token i has position p = lens[r] - first[r + 1] + i.  Rows of tokens at
+ * or past first[requests] are left as they were.  heads = kv_heads * n, n = 1 ..
+ * 128; query head h belongs to key/value head h / n.
+ *   requests   1 .. 8192 (tokens 0: nothing is read);  table_width >= 0
+ *   q          [tokens, heads, 128] with q_stride elements (a multiple of 8)
+ *              from one token to the next, 16-byte aligned
+ *   first int32 [requests + 1], ascending from 0 up to tokens;  lens int32
+ *   [requests];  tables int32 [requests, table_width]
+ * A position at or past table_width * page_size, or in a page whose id is not in
+ * [0, pages), is not attended to.
+ */
+typedef struct dsa_kv_cfg {
+  int32_t pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t dtype;
+} dsa_kv_cfg;
+
+/*
+ * Store a step's rows and rotate its queries.  Token i has position ends[i] - 1
+ * and goes to slots[i] (page * page_size + row); its q, k and v rows lie q_stride,
+ * k_stride and v_stride elements (multiples of 8) after the token's before it,
+ * heads and dims packed, 16-byte aligned.
+ *   rotation  pairs (a, b) of the first `rotary` dims (a multiple of 16, 0 .. 128)
+ *             become gain * (a cos x - b sin x, b cos x + a sin x) with x =
+ *             position * 2 pi * turns[j] / 2^64: dims j and j + rotary / 2 are
+ *             pair j, or with neighbours != 0 dims 2 j and 2 j + 1.  turns int64
+ *             [rotary / 2]: a frequency as a fraction of 2^64 of a turn a
+ *             position, so that the angle of a far position is reduced exactly.
+ *             Keys and queries are rotated in f32 and rounded once; other dims
+ *             and values are copied.
+ *   q_out     [tokens, heads, 128] contiguous; may be q.  heads 0: no queries.
+ *   means     NULL: not kept.  A page whose last row is stored by this call gets
+ *             the mean of its rows as stored, summed in f32 in a fixed order and
+ *             rounded once.
+ *   ends      1 <= ends[i]; a token with less is not looked at (its q_out row is
+ *             left as it was)
+ *   slots     one outside [0, pages * page_size): k and v are not stored.  No slot
+ *             twice; where means are kept, tokens that store into one page stand
+ *             next to one another in the order of their slots, as in a plan.
+ */
+int dsa_kv_append(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t rotary, int32_t neighbours,
+                  float gain, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                  int64_t v_stride, const int32_t* ends, const int32_t* slots, const int64_t* turns, void* q_out,
+                  void* k_cache, void* v_cache, void* means, struct CUstream_st* stream);
+
+/*
+ * Causal attention of a step's tokens: with A(t) the positions 0 .. p of t's
+ * request,
+ *     o[t, h] = sum_{j in A(t)} softmax_j(scale * q[t, h] . k[j]) v[j]
+ *     lse[t, h] = ln sum_{j in A(t)} exp(scale * q[t, h] . k[j])
+ * and an empty A(t) gives o = 0, lse = -inf.  Single tokens, drafts and prompt
+ * chunks may stand side by side.
+ *   o    [tokens, heads, 128] of cfg's type, 16-byte aligned;  lse f32 [tokens, heads]
+ *   scale  of any sign; scale * log2(e) is finite in f32
+ *   workspace  device memory, 16-byte aligned, of at least
+ *              dsa_kv_attention_workspace() bytes; nothing in it has to start at
+ *              zero.  Calls that may run at the same time need one each.
+ * Scores, sums and outputs are held in f32; the softmax weights are rounded to
+ * cfg's type for the second product.  What a row does not attend to -- later
+ * positions, stale rows of a page -- has no effect on it, whatever it holds.
+ * Results repeat bit for bit.
+ */
+int dsa_kv_attention_workspace(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests,
+                               int32_t table_width, size_t* bytes);
+
+int dsa_kv_attention(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests, int32_t table_width,
+                     const void* k_cache, const void* v_cache, const void* q, int64_t q_stride,
+                     const int32_t* first, const int32_t* lens, const int32_t* tables, float scale,
+                     void* workspace, size_t workspace_bytes, void* o, float* lse, struct CUstream_st* stream);
+
+/*
+ * The pages each token's queries score highest: for token t at position p and
+ * key/value head g, page j's score is the sum over the group's heads of
+ * q[t, h] . means[page j, g].  The first `lead` pages and the last `trail` up to
+ * the token's own (p / page_size) are taken always, and of the others before them
+ * the best, select pages in all (all there are, if fewer).
+ *   idx     int32 [tokens, kv_heads, select]: page numbers within the request,
+ *           ascending, then -1
+ *   select  1 .. 256;  lead >= 0, trail >= 1, lead + trail <= select
+ *   workspace  as above, dsa_kv_select_workspace() bytes
+ * Ranks are those of the scores in exact arithmetic (f64 where f32 cannot tell
+ * two apart); among equal scores the lower page wins; a NaN score ranks below
+ * every other.  A page without a valid id has no score and ranks as a NaN does.
+ */
+int dsa_kv_select_workspace(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests,
+                            int32_t table_width, size_t* bytes);
+
+int dsa_kv_select(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests, int32_t table_width,
+                  int32_t select, int32_t lead, int32_t trail, const void* means, const void* q, int64_t q_stride,
+                  const int32_t* first, const int32_t* lens, const int32_t* tables, void* workspace,
+                  size_t workspace_bytes, int32_t* idx, struct CUstream_st* stream);
+
+/*
+ * dsa_kv_attention with A(t), for a query head of key/value head g, cut down to
+ * the positions up to t's own in the pages idx[t, g] lists.
+ *   idx  int32 [tokens, kv_heads, select] (the rows of dsa_kv_select qualify):
+ *        strictly ascending, then -1;  select 1 .. 4096
+ */
+int dsa_kv_block_attention_workspace(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests,
+                                     int32_t table_width, int32_t select, size_t* bytes);
+
+int dsa_kv_block_attention(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests,
+                           int32_t table_width, int32_t select, const void* k_cache, const void* v_cache,
+                           const void* q, int64_t q_stride, const int32_t* idx, const int32_t* first,
+                           const int32_t* lens, const int32_t* tables, float scale, void* workspace,
+                           size_t workspace_bytes, void* o, float* lse, struct CUstream_st* stream);
+
+/* DSA_ERR_TIMEOUT once after a launch of dsa_kv_attention or
+ * dsa_kv_block_attention on the current device gave up a wait (then cleared),
+ * else DSA_OK; synchronises the device, every stream of it. */
+int dsa_kv_status(void);
+
 /* Static description of a status code. */
 const char* dsa_status_string(int status);
 

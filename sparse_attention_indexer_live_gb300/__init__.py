@@ -35,14 +35,21 @@ __all__ = ["DSA_OK", "DSA_ERR_INVALID_ARG", "DSA_ERR_UNSUPPORTED", "DSA_ERR_CUDA
 _CACHE = ("PagedCache", "cache_cfg", "dsa_cache_cfg", "dsa_cache_bytes", "dsa_cache_plan", "dsa_cache_write",
           "dsa_cache_read", "dsa_cache_attention", "dsa_cache_attention_prompt",
           "dsa_cache_attention_prompt_workspace", "dsa_cache_attention_status")
+_KV = ("PagedKV", "kv_cfg", "dsa_kv_cfg", "rotary_turns", "dsa_kv_append", "dsa_kv_attention",
+       "dsa_kv_attention_workspace", "dsa_kv_select", "dsa_kv_select_workspace", "dsa_kv_block_attention",
+       "dsa_kv_block_attention_workspace", "dsa_kv_status")
 if importlib.util.find_spec("torch") is not None:  # import * takes the names below, and with them torch
-    __all__ += _CACHE
+    __all__ += _CACHE + _KV
 
 
 def __getattr__(name):
-    """cache.py imports torch, which the rest of the package does not need to load."""
+    """cache.py and kv.py import torch, which the rest of the package does not need to load."""
     if name in _CACHE:
         from . import cache
         globals().update({n: getattr(cache, n) for n in _CACHE})
+        return globals()[name]
+    if name in _KV:
+        from . import kv
+        globals().update({n: getattr(kv, n) for n in _KV})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

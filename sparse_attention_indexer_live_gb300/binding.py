@@ -43,7 +43,9 @@ EXPORTS = ("dsa_select_init", "dsa_select_destroy", "dsa_plan_describe", "dsa_ca
            "dsa_sparse_attention_ranges", "dsa_sparse_attention_status", "dsa_cache_bytes",
            "dsa_cache_plan", "dsa_cache_write", "dsa_cache_read", "dsa_cache_attention",
            "dsa_cache_attention_prompt_workspace", "dsa_cache_attention_prompt",
-           "dsa_cache_attention_status", "dsa_status_string")
+           "dsa_cache_attention_status", "dsa_kv_append", "dsa_kv_attention_workspace", "dsa_kv_attention",
+           "dsa_kv_select_workspace", "dsa_kv_select", "dsa_kv_block_attention_workspace",
+           "dsa_kv_block_attention", "dsa_kv_status", "dsa_status_string")
 
 # Size of the library's fixed scratch array used by dsa_indexer_select_noalloc
 # (DSA_NOALLOC_SCRATCH_BYTES in include/dsa_select.h).
@@ -139,7 +141,17 @@ def load(path: str | None = None):
                     ("dsa_cache_read", [vp, c32, c32, vp, vp, vp, vp, vp]),
                     ("dsa_cache_attention", [vp] + [c32] * 6 + [vp] * 5 + [f32, vp, vp, vp]),
                     ("dsa_cache_attention_prompt_workspace", [vp, c32, c32, c32, vp]),
-                    ("dsa_cache_attention_prompt", [vp] + [c32] * 5 + [vp] * 4 + [f32, vp, size, vp, vp, vp])):
+                    ("dsa_cache_attention_prompt", [vp] + [c32] * 5 + [vp] * 4 + [f32, vp, size, vp, vp, vp]),
+                    # the dsa_kv_* calls (kv.py), the same
+                    ("dsa_kv_append", [vp] + [c32] * 4 + [f32] + [vp, c64] * 3 + [vp] * 8),
+                    ("dsa_kv_attention_workspace", [vp] + [c32] * 4 + [vp]),
+                    ("dsa_kv_attention", [vp] + [c32] * 4 + [vp] * 3 + [c64] + [vp] * 3 + [f32, vp, size, vp, vp, vp]),
+                    ("dsa_kv_select_workspace", [vp] + [c32] * 4 + [vp]),
+                    ("dsa_kv_select", [vp] + [c32] * 7 + [vp] * 2 + [c64] + [vp] * 4 + [size, vp, vp]),
+                    ("dsa_kv_block_attention_workspace", [vp] + [c32] * 5 + [vp]),
+                    ("dsa_kv_block_attention",
+                     [vp] + [c32] * 5 + [vp] * 3 + [c64] + [vp] * 4 + [f32, vp, size, vp, vp, vp]),
+                    ("dsa_kv_status", [])):
                 fn = getattr(L, name)
                 fn.restype, fn.argtypes = i32, args
             L.dsa_status_string.restype = ctypes.c_char_p

@@ -330,6 +330,15 @@ def dsa_cache_attention_status(device=None) -> int:
 # ---------------------------------------------------------------------------
 # a cache with its tables
 
+def refusal(status):
+    """Wait for a plan's status [4]; RuntimeError with the reason when the step could not be taken."""
+    code, short, _, _ = status.tolist()
+    if code != PLAN_OK:
+        why = {PLAN_NO_PAGES: f"{short} pages short", PLAN_TABLE_WIDTH: "a request needs more pages than its table has",
+               PLAN_TOKENS: "more tokens than the step has room for"}.get(code, "lengths or counts out of range")
+        raise RuntimeError(f"cache step not taken: {why}")
+
+
 class PagedCache:
     """A cache of one layer with the pages of up to `requests` requests.
 
@@ -372,11 +381,7 @@ class PagedCache:
 
     def ok(self):
         """Wait for the last step's status; RuntimeError when it could not be taken."""
-        code, short, _, _ = self.status.tolist()
-        if code != PLAN_OK:
-            why = {PLAN_NO_PAGES: f"{short} pages short", PLAN_TABLE_WIDTH: "a request needs more pages than its table has",
-                   PLAN_TOKENS: "more tokens than the step has room for"}.get(code, "lengths or counts out of range")
-            raise RuntimeError(f"cache step not taken: {why}")
+        refusal(self.status)
 
     def store(self, k, v):
         """Write the step's rows, k and v [tokens, kv_heads, 128]."""
