@@ -174,7 +174,7 @@ def test_rotary_turns():
     f = 1e4 ** (-torch.arange(0, 128, 2, dtype=torch.float64) / 128)
     turns = dsa.rotary_turns(f)
     for x, y in zip(f.tolist(), turns.tolist()):
-        assert abs(y / 2 ** 64 - x / (2 * math.pi)) <= 2.0 ** -53 * x
+        assert abs(y / 2 ** 64 - x / (2 * math.pi)) <= 2.0 ** -53 * x + 2.0 ** -64
     assert dsa.rotary_turns([]).numel() == 0
 
 
