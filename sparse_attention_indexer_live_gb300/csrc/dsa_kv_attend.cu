@@ -1,6 +1,30 @@
 // dsa_kv_attend.cu -- causal attention of a step's tokens over the paged 16-bit
 // cache, to every position or to a selection of pages.  Semantics:
 // include/dsa_select.h.
+//
+// Rows of a tile are the query heads of 128 / n neighbouring tokens of a request
+// that share a key/value head (row = token * n + head), columns 128 positions.
+// One CTA an SM takes units of work -- a tile of rows, or two -- one after
+// another:
+//   * a scheduler warp finds the units.  The step's lengths are in device memory,
+//     so every CTA sums the work of all requests, takes an equal share of it and
+//     cuts the first and last unit of the share where it has to; the shares of a
+//     cut unit go to the workspace and a second kernel joins them;
+//   * a TMA warp brings Q tiles once a unit and key and value tiles through a ring
+//     of five, a box a page and half of the dims, 128B-swizzled;
+//   * one warp issues tcgen05.mma: S = Q K^T (both in shared memory) and O += P V,
+//     P in tensor memory over the scores it came from;
+//   * two softmax warpgroups, a thread a row.
+// The two warpgroups have a stream of tiles each, so that the tensor cores have one's
+// product while the other's scores are weighed: with two row tiles in the unit, a
+// row tile each against the same keys (PAIR); with one, every other tile of its
+// positions, joined at the end.  A selection of pages is walked as the union of
+// the tile's tokens' lists, each row masked to its own.
+// Every mbarrier wait is bounded by a clock limit.
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -8,94 +32,1308 @@
 
 namespace {
 
+constexpr int kThreads = 384;  // warps 0-7 softmax, 8 TMA, 9 MMA, 10 scheduler, 11 tensor memory
+// Registers (setmaxnreg): 168 a thread at launch; 256 x 200 + 128 x 104 = 384 x 168.
+constexpr int kLaunchRegs = 168, kSoftRegs = 200, kSideRegs = 104;
+static_assert(256 * kSoftRegs + 128 * kSideRegs <= kThreads * kLaunchRegs, "register split exceeds the launch's");
+constexpr int kTile = 128;
+constexpr int kHalf = 128 * 128;     // bytes of one half of the dims of a tile: 128 rows of 128
+constexpr int kTileBytes = 2 * kHalf;
+constexpr int kStages = 5, kInfos = 8, kDescs = 2;
+constexpr int kOffKV = 2 * kTileBytes;  // after two Q tiles
+constexpr int kOffInfo = kOffKV + kStages * kTileBytes;
+struct Info {            // of one tile of positions
+  int32_t page[8];       // sparse: its pages, by number in the request (-1: none)
+  uint32_t good[4];      // positions whose page is there
+  int32_t j;             // dense: the tile's number
+  int32_t last;          // of the unit
+  int32_t spare[2];
+};
+struct Desc {            // of one unit, or of a CTA's share of one
+  int32_t stop, r, kvh, t0, ntok, pos0, pair, slot;  // slot: of the workspace, -1: a whole unit
+  int32_t j0, j1;        // dense: tiles
+  int32_t from, to;      // sparse: page numbers
+  int32_t spare[4];
+};
+constexpr int kOffDesc = kOffInfo + kInfos * (int)sizeof(Info);
+constexpr int kOffXch = kOffDesc + kDescs * (int)sizeof(Desc);  // [stream][row] maximum and sum
+constexpr int kOffScan = kOffXch;                               // (before the first unit) warps' sums
+constexpr int kOffBars = kOffXch + 2 * 128 * 8;
+constexpr int kNumBars = 2 + 2 * kStages + kInfos + 2 * kDescs + 6 + 3;
+constexpr int kOffWord = kOffBars + kNumBars * 8;  // tensor memory's address, abort flag
+constexpr int kSmem = kOffWord + 16;
+static_assert(kSmem <= 232448, "shared memory");
+constexpr uint32_t kTmemCols = 512, kTmemO = 256;  // S (and P) at 0 and 128, O at 256 and 384
+constexpr int kNever = 0x7FFFFFFF;                 // past every page number
+// A unit costs this many positions besides its own; a CTA takes no share below
+// kLeast; a cut less than kSnap tiles from a unit's end moves there.
+constexpr int kUnitCost = 256;
+constexpr int kLeast = 512;
+constexpr int kSnap = 2;
+constexpr int kMaxCtas = 1024;
+#ifdef DSA_KV_TEST_WAIT_CYCLES  // test builds shorten the waits and starve one barrier
+constexpr long long kWaitCycles = DSA_KV_TEST_WAIT_CYCLES;
+constexpr uint32_t kPArrivals = 129;
+#else
+constexpr long long kWaitCycles = 8000000000ll;  // ~4 s
+constexpr uint32_t kPArrivals = 128;
+#endif
+
+__device__ int g_kv_error;
+
+// Where the shares of cut units meet: for CTA c > 0 the unit its share begins in.
+struct Cut {
+  int32_t r, kvh, t0, ntok, at, tiles, pair, spare;
+};
+struct Sizes {
+  int64_t ml_off, o_off, bytes;
+  int32_t ctas, rows;
+};
+
+struct Launch {
+  CUtensorMap q, k, v;
+  KvParams p;
+  int32_t tpt;      // tokens a row tile
+  int32_t log_cpt;  // log2 of pages a tile of positions
+  int32_t rows;     // of a slot of the workspace
+  uint8_t* ws;      // [kMaxCtas] Cut, int32 CTAs with a share | sums | outputs
+  int64_t ml_off, o_off;
+};
+
+__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(n));
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(su32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait; false when the phase has not completed in time (the error word and
+// the CTA's flag are then set, and the CTA's other waits fail at once).
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
+  if (bar_try(b, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (bar_try(b, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort = 1;
+      atomicExch(&g_kv_error, 1);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_all(uint64_t* b, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(b, parity, abort));
+}
+// For what is still in flight when a CTA gives up: bounded, whatever the flag says.
+__device__ __forceinline__ void drain(uint64_t* b, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!bar_try(b, parity) && clock64() - t0 < kWaitCycles) {
+  }
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
+  return x != 0;
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(su32(bar))
+      : "memory");
+}
+// Descriptors of 128B-swizzled tiles of 128-byte rows: K-major (rows are M or N,
+// dims K), and N-major (rows are K; leading offset: the next 64 dims).
+__device__ __forceinline__ uint64_t sdesc(uint32_t a, uint32_t leading) {
+  uint64_t d = (uint64_t)((a & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(leading >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;  // stride byte offset: 8-row groups
+  d |= (uint64_t)1 << 46;            // descriptor version
+  d |= (uint64_t)2 << 61;            // 128-byte swizzle
+  return d;
+}
+// f32 accumulator, A and B bf16 or f16, M = N = 128
+template <bool kBf16>
+constexpr uint32_t kIdesc = (1u << 4) | (kBf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(128 >> 3) << 17) |
+                            ((uint32_t)(128 >> 4) << 24);
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+               " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+               "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+               " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+               "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// S = Q K^T over the 128 dims.
+template <bool kBf16>
+__device__ __forceinline__ void mma_qk(uint32_t s, uint64_t q, uint64_t k) {
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    const uint32_t off = (uint32_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+    mma_ss(s, q + off, k + off, kIdesc<kBf16>, kk > 0);
+  }
+}
+// O (+)= P V over 128 positions, P's positions 2 c and 2 c + 1 in column c.
+template <bool kBf16>
+__device__ __forceinline__ void mma_pv(uint32_t o, uint32_t p, uint64_t v, bool add) {
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts(o, p + 8 * kk, v + (uint32_t)((kk * 16 * 128) >> 4), kIdesc<kBf16> | (1u << 16), add || kk > 0);
+}
+__device__ __forceinline__ void mma_commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(b))
+               : "memory");
+}
+__device__ __forceinline__ void tld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tst32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tst16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void upk2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
-// One row of one query head by a warp, on the CUDA cores: 32 positions at a time,
-// a lane each for the score, four dims a lane for the values.
+// ---------------------------------------------------------------------------
+// units
+
+// The units of one request: tpu tokens each (the last one fewer), for every
+// key/value head.  Unit u costs its positions and kUnitCost (a selection: as many
+// positions as a list has).
+template <bool kSparse>
+struct Units {
+  Request q;
+  int32_t tpu, n;
+  int64_t each;    // sparse: a unit's cost
+  int64_t base;    // dense: pos0 + kUnitCost
+  __device__ Units(const Launch& L, int r) {
+    q = request_of(L.p.first, L.p.lens, r, L.p.T);
+    tpu = kSparse ? L.tpt : 2 * L.tpt;
+    n = (q.b - q.a + tpu - 1) / tpu;
+    each = (int64_t)L.p.select * L.p.page + kUnitCost;
+    base = (int64_t)max(q.pos0, 0) + kUnitCost;
+  }
+  // of the units before u, u < n
+  __device__ int64_t before(int64_t u) const {
+    return kSparse ? u * each : u * base + (int64_t)tpu * (u * (u + 1) / 2);
+  }
+  __device__ int64_t cost(int u) const {
+    return kSparse ? each : base + min((int64_t)(q.b - q.a), ((int64_t)u + 1) * tpu);
+  }
+  __device__ int64_t head() const { return n ? before(n - 1) + cost(n - 1) : 0; }
+  // the unit at x, 0 <= x < head()
+  __device__ int find(int64_t x) const {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (before(mid) <= x)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  }
+  // tiles of a unit (at least one: a tile of nothing gives zeros)
+  __device__ int tiles(const Launch& L, int u) const {
+    if (kSparse) return max(1, (L.p.select + (1 << L.log_cpt) - 1) >> L.log_cpt);
+    const int64_t keys = q.pos0 < 0 ? 0 : (int64_t)q.pos0 + min((int64_t)(q.b - q.a), ((int64_t)u + 1) * tpu);
+    return max(1, (int)((min(keys, (int64_t)L.p.P << L.p.shift) + kTile - 1) / kTile));
+  }
+};
+// The tile before which a unit of n tiles is cut x after its beginning.
+__device__ __forceinline__ int cut_at(int64_t x, int n) {
+  const int64_t j = max((int64_t)0, x - kUnitCost + kTile / 2) / kTile;
+  return j < kSnap ? 0 : n - j < kSnap ? n : (int)j;
+}
+__device__ __forceinline__ int64_t share_at(int64_t all, int c, int ctas) {
+  return all / ctas * c + all % ctas * c / ctas;
+}
+
+// ---------------------------------------------------------------------------
+// one row on the CUDA cores
+
+// The output of one row (before the normaliser) by a warp: sum_j 2^(s_j - m) v_j
+// over its positions, four dims a lane.  0 times a NaN or an infinity of the values
+// is a NaN in the tensor cores' product, so a row whose output is not finite
+// although its sum is may owe that to a position that it does not attend to: such a
+// row is computed again from those that it does.  (Without a selection: if one of
+// the positions after its own, up to the end of the unit's tiles, is to blame.)
 template <bool kBf16>
-struct Row {
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  // positions [from, to) of the page `id` of key/value head g
-  __device__ void page(const KvParams& p, const char* q, int g, int id, int from, int to) {
+struct RowAgain {
+  float o[4];
+  __device__ void page(const KvParams& p, const char* q, int g, int id, int from, int to, float m) {
     const int lane = threadIdx.x & 31;
     if (id < 0 || id >= p.pages) return;
+#pragma unroll 1
     for (int j0 = from; j0 < to; j0 += 32) {
-      const int64_t base = ((int64_t)id * p.page + j0) * p.kv_heads + g;
-      float s = -INFINITY;
+      const int64_t at = ((int64_t)id * p.page + j0) * p.kv_heads + g;
+      float w = 0.f;
       if (j0 + lane < to) {
-        const char* k = static_cast<const char*>(p.k) + 2 * kKvDim * (base + (int64_t)lane * p.kv_heads);
+        const char* k = static_cast<const char*>(p.k) + 2 * kKvDim * (at + (int64_t)lane * p.kv_heads);
         float d = 0.f;
+        Eight row[kKvDim / 8];
+#pragma unroll
+        for (int c = 0; c < kKvDim / 8; ++c) row[c] = load8(k + 16 * c);
+#pragma unroll
         for (int c = 0; c < kKvDim / 8; ++c) {
           float x[8], y[8];
           unpack8<kBf16>(load8(q + 16 * c), x);
-          unpack8<kBf16>(load8(k + 16 * c), y);
+          unpack8<kBf16>(row[c], y);
 #pragma unroll
           for (int e = 0; e < 8; ++e) d = fmaf(x[e], y[e], d);
         }
-        s = (p.flip ? -d : d) * p.c2;
+        w = ex2((p.flip ? -d : d) * p.c2 - m);
       }
-      float top = s;
-#pragma unroll
-      for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-      const float next = fmaxf(m, top);
-      const float base_m = next == -INFINITY ? 0.f : next;
-      const float w = ex2(s - base_m), alpha = m == -INFINITY ? 0.f : ex2(m - base_m);
-      m = next;
-      float sum = w;
-#pragma unroll
-      for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-      l = l * alpha + sum;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] *= alpha;
       const int n = min(32, to - j0);
-      for (int j = 0; j < n; ++j) {
-        const float pj = __shfl_sync(0xFFFFFFFFu, w, j);
-        const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const char*>(p.v) +
-                                                        2 * (kKvDim * (base + (int64_t)j * p.kv_heads) + 4 * lane));
-        const float2 a = pair_f32<kBf16>(x.x), b = pair_f32<kBf16>(x.y);
-        o[0] = fmaf(pj, a.x, o[0]);
-        o[1] = fmaf(pj, a.y, o[1]);
-        o[2] = fmaf(pj, b.x, o[2]);
-        o[3] = fmaf(pj, b.y, o[3]);
+#pragma unroll 1
+      for (int j = 0; j < n; j += 8) {
+        uint2 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[i] = j + i < n ? *reinterpret_cast<const uint2*>(static_cast<const char*>(p.v) +
+                                                             2 * (kKvDim * (at + (int64_t)(j + i) * p.kv_heads) + 4 * lane))
+                           : make_uint2(0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float pj = __shfl_sync(0xFFFFFFFFu, w, j + i);  // (0 past the last position)
+          const float2 a = pair_f32<kBf16>(x[i].x), b = pair_f32<kBf16>(x[i].y);
+          o[0] = fmaf(pj, a.x, o[0]);
+          o[1] = fmaf(pj, a.y, o[1]);
+          o[2] = fmaf(pj, b.x, o[2]);
+          o[3] = fmaf(pj, b.y, o[3]);
+        }
       }
     }
   }
 };
-
 template <bool kBf16>
-__global__ void __launch_bounds__(256) row_kernel(const KvParams p) {
+__device__ __noinline__ bool odd_after(const Launch& L, const Desc& d, int pos) {
+  const KvParams& p = L.p;
+  const int32_t* table = p.tables + (int64_t)d.r * p.P;
+  const int64_t end = min((int64_t)d.j1 * kTile, (int64_t)p.P << p.shift);
+  const uint32_t top = kBf16 ? 0x7F80u : 0x7C00u;  // an exponent of ones
+  for (int64_t x = (int64_t)pos + 1 + (threadIdx.x & 31); __any_sync(0xFFFFFFFFu, x < end); x += 32) {
+    bool odd = false;
+    const int id = x < end ? table[x >> p.shift] : -1;
+    if (id >= 0 && id < p.pages) {
+      const char* v = static_cast<const char*>(p.v) +
+                      2 * kKvDim * ((((int64_t)id << p.shift) + (x & (p.page - 1))) * p.kv_heads + d.kvh);
+      for (int c = 0; c < kKvDim / 8; ++c) {
+        const Eight e = load8(v + 16 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) odd |= (e.w[i] & top) == top || (e.w[i] >> 16 & top) == top;
+      }
+    }
+    if (__any_sync(0xFFFFFFFFu, odd)) return true;
+  }
+  return false;
+}
+template <bool kBf16, bool kSparse>
+__device__ __noinline__ float4 row_again(const Launch& L, const Desc& d, int t, int h, int pos, float m) {
+  const KvParams& p = L.p;
+  const char* q = static_cast<const char*>(p.q) + 2 * (t * p.q_stride + h * kKvDim);
+  const int32_t* table = p.tables + (int64_t)d.r * p.P;
+  RowAgain<kBf16> row;
+  row.o[0] = row.o[1] = row.o[2] = row.o[3] = 0.f;
+  if (kSparse) {
+    const int32_t* idx = p.idx + ((int64_t)t * p.kv_heads + d.kvh) * p.select;
+    for (int i = 0; i < p.select && idx[i] >= 0; ++i) {
+      const int j = idx[i];
+      if (j >= d.from && j < d.to && j < p.P && j <= pos >> p.shift)
+        row.page(p, q, d.kvh, table[j], 0, min(p.page, pos - (j << p.shift) + 1), m);
+    }
+  } else {
+    const int64_t end = min((int64_t)d.j1 * kTile, min((int64_t)pos + 1, (int64_t)p.P << p.shift));
+    for (int64_t x = (int64_t)d.j0 * kTile; x < end; x += p.page)
+      row.page(p, q, d.kvh, table[x >> p.shift], 0, (int)min((int64_t)p.page, end - x), m);
+  }
+  return make_float4(row.o[0], row.o[1], row.o[2], row.o[3]);
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+
+template <bool kBf16, bool kSparse>
+__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Launch L) {
+  extern __shared__ __align__(1024) uint8_t base[];
+  const KvParams& p = L.p;
+  const uint32_t sb = su32(base);
+  Info* info = reinterpret_cast<Info*>(base + kOffInfo);
+  Desc* desc = reinterpret_cast<Desc*>(base + kOffDesc);
+  float2* xch = reinterpret_cast<float2*>(base + kOffXch);
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(base + kOffBars);
+  uint64_t* qempty = qfull + 1;            // every S of the unit done
+  uint64_t* full = qempty + 1;             // [5] a key or value tile has landed
+  uint64_t* empty = full + kStages;        // [5] its products are done
+  uint64_t* tfull = empty + kStages;       // [8] a tile's Info is written
+  uint64_t* dfull = tfull + kInfos;        // [2] a unit's Desc is written
+  uint64_t* dempty = dfull + kDescs;       // [2] read by all warps
+  uint64_t* sfull = dempty + kDescs;       // [2] scores of a stream
+  uint64_t* pfull = sfull + 2;             // [2] weights written over them
+  uint64_t* pvdone = pfull + 2;            // [2] their product done
+  uint64_t* ofree = pvdone + 2;            // both outputs of a unit read
+  uint64_t* xfull = ofree + 1;             // both streams' maxima and sums are there
+  uint64_t* dbar = xfull + 1;              // products in flight when the CTA gives up
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + kOffWord);
+  volatile int* abort = reinterpret_cast<volatile int*>(base + kOffWord + 4);
+  int* start_req = reinterpret_cast<int*>(base + kOffDesc);                  // before the first unit
+  int64_t* start_x = reinterpret_cast<int64_t*>(base + kOffDesc + 8);        // (the scheduler reads them first)
+  int64_t* warp_sum = reinterpret_cast<int64_t*>(base + kOffScan);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  let_next_start();
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    *start_req = -1;
+    bar_init(qfull, 1);
+    bar_init(qempty, 1);
+    for (int i = 0; i < kStages; ++i) {
+      bar_init(&full[i], 1);
+      bar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kInfos; ++i) bar_init(&tfull[i], 1);
+    for (int i = 0; i < kDescs; ++i) {
+      bar_init(&dfull[i], 1);
+      bar_init(&dempty[i], 10);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&sfull[i], 1);
+      bar_init(&pfull[i], kPArrivals);
+      bar_init(&pvdone[i], 1);
+    }
+    bar_init(ofree, 256);
+    bar_init(xfull, 256);
+    bar_init(dbar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 11) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (warp == 8 && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)(lane == 0 ? &L.q : lane == 1 ? &L.k : &L.v)) : "memory");
+  // rows of Q tiles that no token fills stay zeros
+  for (int i = threadIdx.x; i < 2 * kTileBytes / 16; i += kThreads)
+    *reinterpret_cast<uint4*>(base + 16 * i) = make_uint4(0, 0, 0, 0);
+  fence_async_smem();
+  wait_for_previous();
+
+  // this CTA's share of all requests' work
+  const int per = (p.R + kThreads - 1) / kThreads;
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int r = threadIdx.x * per + i;
+    if (r < p.R) mine += Units<kSparse>(L, r).head() * p.kv_heads;
+  }
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  fence_before();
+  __syncthreads();
+  fence_after();
+  int64_t all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) upto += all;
+    all += warp_sum[w];
+  }
+  const int ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, all / kLeast));
+  const bool has = (int)blockIdx.x < ctas && all > 0;
+  const int64_t x0 = has ? share_at(all, blockIdx.x, ctas) : 0, x1 = has ? share_at(all, blockIdx.x + 1, ctas) : 0;
+  if (has && x0 >= upto - mine && x0 < upto) {
+    int64_t at = upto - mine;
+    for (int i = 0; i < per; ++i) {
+      const int r = threadIdx.x * per + i;
+      const int64_t w = r < p.R ? Units<kSparse>(L, r).head() * p.kv_heads : 0;
+      if (x0 < at + w) {
+        *start_req = r;
+        *start_x = at;
+        break;
+      }
+      at += w;
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<int32_t*>(L.ws + kMaxCtas * sizeof(Cut)) = has ? ctas : 0;
+  __syncthreads();
+  const uint32_t tmem = *tmem_slot;
+  const int req0 = *start_req;
+  const int64_t req0_x = *start_x;
+  __syncthreads();  // the scheduler writes over them
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
+    if (warp == 10) {
+      // ---- scheduler
+      int d = 0;
+      bool ok = true;
+      auto publish = [&](const Desc& u) {
+        const int s = d % kDescs;
+        if (d >= kDescs && !wait_all(&dempty[s], ((d / kDescs) & 1) ^ 1, abort)) return false;
+        if (lane == 0) {
+          desc[s] = u;
+          bar_arrive(&dfull[s]);
+        }
+        __syncwarp();
+        ++d;
+        return true;
+      };
+      int64_t x = req0_x;  // where request r begins
+      for (int r = req0; ok && has && r >= 0 && r < p.R && x < x1; ++r) {
+        const Units<kSparse> u(L, r);
+        const int64_t head = u.head();
+        if (head == 0) continue;
+        const int64_t rel = max((int64_t)0, x0 - x);
+        int g = (int)(rel / head);
+        int i = u.find(rel - g * head);
+        for (; ok && g < p.kv_heads && x + g * head < x1; ++g, i = 0) {
+          for (; ok && i < u.n; ++i) {
+            const int64_t at = x + g * head + u.before(i), end = at + u.cost(i);
+            if (at >= x1) break;
+            Desc e;
+            e.stop = 0;
+            e.r = r;
+            e.kvh = g;
+            e.t0 = u.q.a + i * u.tpu;
+            e.ntok = min(u.tpu, u.q.b - e.t0);
+            e.pos0 = u.q.pos0 < 0 ? -1 : u.q.pos0 + i * u.tpu;
+            e.pair = e.ntok > L.tpt;
+            const int n = u.tiles(L, i);
+            e.j0 = x0 > at ? cut_at(x0 - at, n) : 0;
+            e.j1 = x1 < end ? cut_at(x1 - at, n) : n;
+            e.from = 0;
+            e.to = kNever;
+            if (x0 >= at && x0 < end && lane == 0 && blockIdx.x > 0) {
+              Cut c;
+              c.r = r;
+              c.kvh = g;
+              c.t0 = e.t0;
+              c.ntok = e.ntok;
+              c.at = e.j0;
+              c.tiles = n;
+              c.pair = e.pair;
+              c.spare = 0;
+              reinterpret_cast<Cut*>(L.ws)[blockIdx.x] = c;
+            }
+            if (e.j0 >= e.j1) continue;
+            e.slot = e.j0 > 0 ? 2 * (int)blockIdx.x : e.j1 < n ? 2 * (int)blockIdx.x + 1 : -1;
+            if (kSparse) {
+              // shares are cut where the first token's list is
+              const int32_t* list = p.idx + ((int64_t)e.t0 * p.kv_heads + g) * p.select;
+              const int a = e.j0 << L.log_cpt, b = e.j1 << L.log_cpt;
+              if (e.j0 > 0) e.from = list[a] < 0 ? kNever : list[a];
+              if (e.j1 < n) e.to = list[b] < 0 ? kNever : list[b];
+            }
+            ok = publish(e);
+          }
+        }
+        x += head * p.kv_heads;
+      }
+      if (ok) {
+        Desc e;
+        e.stop = 1;
+        publish(e);
+      }
+    } else if (warp == 8) {
+      // ---- TMA: lane b brings box b, half b >> log_cpt of page b & (cpt - 1)
+      const int cpt = 1 << L.log_cpt;
+      const int chunk = lane & (cpt - 1), half = lane >> L.log_cpt;
+      const uint32_t box = sb + kOffKV + (half & 1) * kHalf + chunk * p.page * 128;
+      const uint32_t nowhere = (uint32_t)p.pages << p.shift;  // past the cache: zeros
+      int tile = 0, units = 0;
+      bool ok = true;
+      auto load_pages = [&](int pg, int id, int j, int kvh, bool last) -> bool {
+        // pg: lanes' page numbers (cpt lanes), id: their ids
+        const bool good = pg >= 0 && pg < p.P && id >= 0 && id < p.pages;
+        const uint32_t have = __ballot_sync(0xFFFFFFFFu, good);
+        Info& x = info[tile % kInfos];
+        if (lane < 8) x.page[lane] = lane < cpt ? pg : -1;
+        if (lane < 4)
+          x.good[lane] = p.page == 16 ? (have >> (2 * lane) & 1 ? 0xFFFFu : 0u) | (have >> (2 * lane + 1) & 1 ? 0xFFFF0000u : 0u)
+                                      : (have >> ((32 * lane) >> p.shift) & 1 ? 0xFFFFFFFFu : 0u);
+        if (lane == 0) {
+          x.j = j;
+          x.last = last;
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&tfull[tile % kInfos]);
+        const uint32_t row = good ? (uint32_t)id << p.shift : nowhere;
+        const int z = (int)__shfl_sync(0xFFFFFFFFu, row, chunk);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int n = 2 * tile + kv, st = n % kStages, use = n / kStages;
+          if (use > 0 && !wait_all(&empty[st], (use & 1) ^ 1, abort)) return false;
+          if (lane == 0) bar_expect(&full[st], kTileBytes);
+          __syncwarp();
+          if (half < 2) tma_load(box + st * kTileBytes, kv ? &L.v : &L.k, &full[st], half * 64, kvh, z);
+        }
+        ++tile;
+        return true;
+      };
+      for (; ok; ++units) {
+        const int ds = units % kDescs;
+        if (!wait_all(&dfull[ds], (units / kDescs) & 1, abort)) break;
+        const Desc u = desc[ds];
+        __syncwarp();
+        if (lane == 0) bar_arrive(&dempty[ds]);
+        if (u.stop) break;
+        if (units > 0 && !wait_all(qempty, (units & 1) ^ 1, abort)) break;
+        if (lane == 0) {
+          const uint32_t bytes = (uint32_t)(L.tpt * p.n * 256);
+          bar_expect(qfull, u.pair ? 2 * bytes : bytes);
+          for (int i = 0; i < (u.pair ? 4 : 2); ++i)
+            tma_load(sb + i * kHalf, &L.q, qfull, (i & 1) * 64, u.kvh * p.n, u.t0 + (i >> 1) * L.tpt);
+        }
+        __syncwarp();
+        const int32_t* table = p.tables + (int64_t)u.r * p.P;
+        auto id_of = [&](int pg) { return pg >= 0 && pg < p.P ? table[pg] : -1; };
+        if (!kSparse) {
+          // ids 32 at a time, the next 32 on their way
+          int at = u.j0 << L.log_cpt;
+          int ids = id_of(at + lane), more = id_of(at + 32 + lane);
+          int in = 0;
+          for (int j = u.j0; ok && j < u.j1; ++j) {
+            const int id = __shfl_sync(0xFFFFFFFFu, ids, in + chunk);
+            ok = load_pages(lane < cpt ? (j << L.log_cpt) + lane : -1, id, j, u.kvh, j == u.j1 - 1);
+            in += cpt;
+            if (in == 32) {
+              in = 0;
+              at += 32;
+              ids = more;
+              more = id_of(at + 32 + lane);
+            }
+          }
+        } else {
+          // the union of up to 128 lists, smallest page first; a lane has four
+          int e[4], cur[4], nxt[4];
+          const int32_t* list[4] = {};
+          auto entry = [&](int i, int x) {
+            const int v = x < p.select ? list[i][x] : -1;
+            return v < 0 || v >= u.to ? kNever : v;
+          };
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = lane + 32 * i;
+            list[i] = p.idx + ((int64_t)(u.t0 + min(t, u.ntok - 1)) * p.kv_heads + u.kvh) * p.select;
+            e[i] = 0;
+            if (t >= u.ntok) {
+              e[i] = p.select;
+            } else if (u.from > 0) {
+              int lo = 0, hi = p.select;  // the first entry at or past `from`
+              while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                const int v = list[i][mid];
+                if (v >= 0 && v < u.from)
+                  lo = mid + 1;
+                else
+                  hi = mid;
+              }
+              e[i] = lo;
+            }
+            cur[i] = entry(i, e[i]);
+            nxt[i] = cur[i] == kNever ? kNever : entry(i, e[i] + 1);
+          }
+          auto least = [&]() {
+            return __reduce_min_sync(0xFFFFFFFFu, min(min(cur[0], cur[1]), min(cur[2], cur[3])));
+          };
+          int low = least();
+          auto pop_tile = [&]() {  // lane c < cpt: the c-th page of the next tile, or -1
+            int pg = -1;
+            for (int c = 0; c < cpt && low != kNever; ++c) {
+              if (lane == c) pg = low;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (cur[i] == low) {
+                  cur[i] = nxt[i];
+                  ++e[i];
+                  nxt[i] = cur[i] == kNever ? kNever : entry(i, e[i] + 1);
+                }
+              low = least();
+            }
+            return pg;
+          };
+          int pg = pop_tile();
+          int id = id_of(pg);
+          while (ok) {
+            const bool last = low == kNever;
+            const int pg1 = last ? -1 : pop_tile();
+            const int id1 = id_of(pg1);
+            ok = load_pages(pg, id, 0, u.kvh, last);
+            if (last) break;
+            pg = pg1;
+            id = id1;
+          }
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, *abort)) {  // what is still on its way lands before the CTA ends
+        for (int n = max(0, 2 * tile - kStages); n < 2 * tile; ++n) drain(&full[n % kStages], (n / kStages) & 1);
+        if (units > 0) drain(qfull, (units - 1) & 1);
+      }
+    } else if (warp == 9) {
+      // ---- MMA.  Steps alternate between the streams; S of a step is issued two
+      // steps ahead of its P V, right behind the P V that read the weights it
+      // overwrites (products of one CTA run in the order they are issued).
+      const uint64_t qdesc = sdesc(sb, 16), kdesc = sdesc(sb + kOffKV, 16), vdesc = sdesc(sb + kOffKV, kHalf);
+      int tile = 0;       // of the next S
+      int count[2] = {0, 0};  // products P V of each stream
+      bool ok = true;
+      int units = 0;
+      for (; ok; ++units) {
+        const int ds = units % kDescs;
+        if (!wait_all(&dfull[ds], (units / kDescs) & 1, abort)) break;
+        const bool stop = desc[ds].stop, pair = desc[ds].pair;
+        __syncwarp();
+        if (lane == 0) bar_arrive(&dempty[ds]);
+        if (stop) break;
+        if (!wait_all(qfull, units & 1, abort)) break;
+        bool more = true;
+        int stream = 0;
+        int used = 0;  // streams that have an output in this unit
+        struct Step {
+          int tile, stream;  // tile -1: none
+        };
+        auto next_s = [&](Step& s) -> bool {
+          s.tile = -1;
+          if (!more) return true;
+          if (!wait_all(&tfull[tile % kInfos], (tile / kInfos) & 1, abort)) return false;
+          const bool last = info[tile % kInfos].last;
+          const int n = 2 * tile, st = n % kStages;
+          if (!wait_all(&full[st], (n / kStages) & 1, abort)) return false;
+          fence_after();
+          const bool done = !pair || stream == 1;  // with the key tile
+          if (elect_one()) {
+            mma_qk<kBf16>(tmem + stream * 128, qdesc + (uint32_t)((pair ? stream * kTileBytes : 0) >> 4),
+                          kdesc + (uint32_t)((st * kTileBytes) >> 4));
+            mma_commit(&sfull[stream]);
+            if (done) mma_commit(&empty[st]);
+            if (done && last) mma_commit(qempty);
+          }
+          __syncwarp();
+          s.tile = tile;
+          s.stream = stream;
+          stream ^= 1;
+          if (done) {
+            more = !last;
+            ++tile;
+          }
+          return true;
+        };
+        auto pv = [&](const Step& s) -> bool {
+          const int n = 2 * s.tile + 1, st = n % kStages;
+          if (!wait_all(&full[st], (n / kStages) & 1, abort)) return false;
+          if (!wait_all(&pfull[s.stream], count[s.stream] & 1, abort)) return false;
+          if (!used && units > 0 && !wait_all(ofree, (units & 1) ^ 1, abort)) return false;
+          fence_after();
+          if (elect_one()) {
+            mma_pv<kBf16>(tmem + kTmemO + s.stream * 128, tmem + s.stream * 128,
+                          vdesc + (uint32_t)((st * kTileBytes) >> 4), used >> s.stream & 1);
+            mma_commit(&pvdone[s.stream]);
+            if (!pair || s.stream == 1) mma_commit(&empty[st]);
+          }
+          __syncwarp();
+          used |= 1 << s.stream;
+          ++count[s.stream];
+          return true;
+        };
+        Step a, b, c;
+        ok = next_s(a) && next_s(b);
+        while (ok && a.tile >= 0) {
+          ok = pv(a) && next_s(c);
+          a = b;
+          b = c;
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, *abort)) {
+        if (elect_one()) mma_commit(dbar);
+        __syncwarp();
+        drain(dbar, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ---- softmax: stream `me`, row `row` of its tile
+    const int me = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const int tok = row / p.n, head = row - tok * p.n;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_addr = lanes + me * 128, o_addr = lanes + kTmemO + me * 128;
+    const float c2 = p.c2;
+    int tile = 0;
+    int count[2] = {0, 0};  // steps of each stream
+    int singles = 0;        // units of one row tile
+    for (int units = 0;; ++units) {
+      const int ds = units % kDescs;
+      if (!wait_all(&dfull[ds], (units / kDescs) & 1, abort)) break;
+      const Desc u = desc[ds];
+      __syncwarp();
+      if (lane == 0) bar_arrive(&dempty[ds]);
+      if (u.stop) break;
+      const int mytok = tok + (u.pair && me ? L.tpt : 0);
+      const bool real = tok < L.tpt && mytok < u.ntok;
+      const int t = u.t0 + mytok;
+      // a row of no token: nothing of it is masked, nor kept
+      const int pos = !real ? kNever : u.pos0 < 0 ? -1 : u.pos0 + mytok;
+      // sparse: where the row's list stands
+      const int32_t* list = nullptr;
+      int e = 0, want = kNever, next = kNever;
+      auto entry = [&](int x) {
+        const int v = x < p.select ? list[x] : -1;
+        return v < 0 ? kNever : v;
+      };
+      if (kSparse && real) {
+        list = p.idx + ((int64_t)t * p.kv_heads + u.kvh) * p.select;
+        if (u.from > 0) {
+          int hi = p.select;
+          while (e < hi) {
+            const int mid = (e + hi) / 2;
+            const int v = list[mid];
+            if (v >= 0 && v < u.from)
+              e = mid + 1;
+            else
+              hi = mid;
+          }
+        }
+        want = entry(e);
+        next = entry(e + 1);
+      }
+      float m_used = -INFINITY, l = 0.f;
+      bool ok = true, first = true;
+      int steps = 0;  // tiles of the unit
+      for (bool last = false; !last; ++tile, ++steps) {
+        if (!wait_all(&tfull[tile % kInfos], (tile / kInfos) & 1, abort)) {
+          ok = false;
+          break;
+        }
+        const Info& x = info[tile % kInfos];
+        last = x.last;
+        uint32_t words[4];
+        if (kSparse) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) words[w] = 0u;
+          const int cpt = 1 << L.log_cpt;
+          for (int c = 0; c < cpt; ++c) {
+            const int pg = x.page[c];
+            if (pg < 0 || (real && pg != want)) continue;
+            if (real) {
+              want = next;
+              ++e;
+              next = want == kNever ? kNever : entry(e + 1);
+            }
+            // positions of the page up to the row's own
+            const int64_t room = (int64_t)pos - ((int64_t)pg << p.shift) + 1;
+            const int bits = room < 0 ? 0 : room < p.page ? (int)room : p.page;
+            const int from = c * p.page;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int lo = max(from - 32 * w, 0), hi = min(from + bits - 32 * w, 32);
+              if (lo < hi && lo < 32)
+                words[w] |= (hi == 32 ? 0xFFFFFFFFu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
+            }
+          }
+        } else {
+          const int64_t room = (int64_t)pos - (int64_t)x.j * kTile + 1;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int64_t bits = room - 32 * w;
+            words[w] = bits <= 0 ? 0u : bits >= 32 ? 0xFFFFFFFFu : (1u << (int)bits) - 1u;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) words[w] &= x.good[w];
+        if (!u.pair && (steps & 1) != me) {
+          ++count[me ^ 1];
+          continue;
+        }
+        if (u.pair) ++count[me ^ 1];
+        const int k = count[me]++;
+        if (!wait_all(&sfull[me], k & 1, abort)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        uint32_t sc[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tld32(s_addr + 32 * c, sc[c]);
+        tld_wait();
+        if (p.flip) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sc[c][j] ^= 0x80000000u;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t mw = words[c];
+          if (__all_sync(0xFFFFFFFFu, mw == 0xFFFFFFFFu)) continue;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (!(mw & (1u << j))) sc[c][j] = __float_as_uint(-INFINITY);
+        }
+        // One pass against a base below the running maximum (dsa_cache.h): it moves
+        // only when a weight would pass 2^kMost; then the pass is redone and O rescaled.
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float lsum;
+        auto weights = [&](float m_eff, bool track) {
+          uint64_t ls01 = pk2(0.f, 0.f), ls23 = pk2(0.f, 0.f);
+          const uint64_t cc = pk2(c2, c2), mm = pk2(-m_eff, -m_eff);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float s0 = __uint_as_float(sc[c][j]), s1 = __uint_as_float(sc[c][j + 1]);
+              const float s2 = __uint_as_float(sc[c][j + 2]), s3 = __uint_as_float(sc[c][j + 3]);
+              if (track) {
+                mx[(j >> 2) & 1] = fmax3(mx[(j >> 2) & 1], s0, s1);
+                mx[2 + ((j >> 2) & 1)] = fmax3(mx[2 + ((j >> 2) & 1)], s2, s3);
+              }
+              float x0, x1, x2, x3;
+              if (track) {
+                upk2(ffma2(pk2(s0, s1), cc, mm), x0, x1);
+                upk2(ffma2(pk2(s2, s3), cc, mm), x2, x3);
+              } else {  // the products rounded as in the maximum: its weight is right at any magnitude
+                x0 = __fadd_rn(__fmul_rn(s0, c2), -m_eff);
+                x1 = __fadd_rn(__fmul_rn(s1, c2), -m_eff);
+                x2 = __fadd_rn(__fmul_rn(s2, c2), -m_eff);
+                x3 = __fadd_rn(__fmul_rn(s3, c2), -m_eff);
+              }
+              const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
+              ls01 = fadd2(ls01, pk2(p0, p1));
+              ls23 = fadd2(ls23, pk2(p2, p3));
+              pk[j / 2] = pair_of<kBf16>(p0, p1);
+              pk[j / 2 + 1] = pair_of<kBf16>(p2, p3);
+            }
+            tst16(s_addr + 16 * c, pk);
+          }
+          float l0, l1, l2, l3;
+          upk2(ls01, l0, l1);
+          upk2(ls23, l2, l3);
+          lsum = (l0 + l1) + (l2 + l3);
+        };
+        weights(m_used == -INFINITY ? 0.f : m_used, true);
+        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+        const bool redo = m_used == -INFINITY ? m_new > -INFINITY : m_new - m_used > kMost;
+        float alpha = 1.f;
+        // (and always for scores so large that the fused exponent is off: the
+        // product's rounding, 2^-24 of it, is not the maximum's)
+        if (__any_sync(0xFFFFFFFFu, redo || fabsf(m_used) > 65536.f)) {
+          if (redo) {
+            const float to = m_new - kLift;
+            if (m_used > -INFINITY) alpha = ex2(m_used - to);
+            m_used = to;
+          }
+          tst_wait();  // two stores to the same columns keep no order of their own
+          weights(m_used == -INFINITY ? 0.f : m_used, false);
+          if (!first && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+            ok = wait_all(&pvdone[me], (k - 1) & 1, abort);
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t ov[32];
+              tld32(o_addr + 32 * c, ov);
+              tld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+              tst32(o_addr + 32 * c, ov);
+            }
+          }
+        }
+        first = false;
+        l = l * alpha + lsum;
+        tst_wait();
+        fence_before();
+        bar_arrive(&pfull[me]);
+        if (!ok) break;
+      }
+      if (!ok) break;
+      // ---- the unit's end
+      if (u.pair) {
+        if (!wait_all(&pvdone[me], (count[me] - 1) & 1, abort)) break;
+      } else {
+        if (!wait_all(&pvdone[0], (count[0] - 1) & 1, abort)) break;
+        if (steps > 1 && !wait_all(&pvdone[1], (count[1] - 1) & 1, abort)) break;
+        xch[me * 128 + row] = make_float2(m_used, l);
+        bar_arrive(xfull);
+        if (!wait_all(xfull, singles++ & 1, abort)) break;
+      }
+      fence_after();
+      float m = m_used, sum = l, w0 = 1.f, w1 = 0.f;
+      if (!u.pair) {  // the two streams' shares of the row, in the same order by both
+        const float2 a = xch[row], b = xch[128 + row];
+        m = fmaxf(a.x, b.x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        w0 = ex2(a.x - ref);
+        w1 = ex2(b.x - ref);
+        if (a.y == 0.f) w0 = 0.f;
+        if (b.y == 0.f) w1 = 0.f;
+        sum = a.y * w0 + b.y * w1;
+      }
+      const float scale = u.slot >= 0 ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+      const int64_t out = (int64_t)t * p.H + u.kvh * p.n + head;
+      const int prow = row + (u.pair && me ? 128 : 0);
+      float* po = reinterpret_cast<float*>(L.ws + L.o_off) + ((int64_t)u.slot * L.rows + prow) * kKvDim;
+      bool odd = false;  // an element that is not finite
+      const int col0 = u.pair ? 0 : 64 * me, blocks = u.pair ? 4 : 2;
+#pragma unroll 1
+      for (int c = 0; c < blocks; ++c) {
+        const int col = col0 + 32 * c;
+        uint32_t ov[32], ow[32];
+        if (u.pair) {
+          tld32(o_addr + col, ov);
+          tld_wait();
+        } else {
+          tld32(lanes + kTmemO + col, ov);
+          tld32(lanes + kTmemO + 128 + col, ow);
+          tld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float x = w0 != 0.f ? __uint_as_float(ov[j]) * w0 : 0.f;
+            const float y = w1 != 0.f ? __uint_as_float(ow[j]) * w1 : 0.f;
+            ov[j] = __float_as_uint(x + y);
+          }
+        }
+        if (sum == 0.f) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) ov[j] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float x = __uint_as_float(ov[j]) * scale;
+          odd |= !(fabsf(x) < INFINITY);
+          ov[j] = __float_as_uint(x);
+        }
+        if (real) {
+          if (u.slot >= 0) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<uint4*>(po + col + j) = make_uint4(ov[j], ov[j + 1], ov[j + 2], ov[j + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out * kKvDim + col);
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[i] = pair_of<kBf16>(__uint_as_float(ov[j + 2 * i]), __uint_as_float(ov[j + 2 * i + 1]));
+              dst[j / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          }
+        }
+      }
+      fence_before();
+      bar_arrive(ofree);
+      if (real && (u.pair || me == 0)) {
+        if (u.slot >= 0)
+          reinterpret_cast<float2*>(L.ws + L.ml_off)[(int64_t)u.slot * L.rows + prow] = make_float2(m, sum);
+        else
+          p.lse[out] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+      }
+      __syncwarp();
+      for (uint32_t again = __ballot_sync(0xFFFFFFFFu, real && odd && sum - sum == 0.f); again; again &= again - 1) {
+        const int from = __ffs(again) - 1;
+        const int rt = __shfl_sync(0xFFFFFFFFu, t, from), rh = __shfl_sync(0xFFFFFFFFu, head, from);
+        const int rp = __shfl_sync(0xFFFFFFFFu, pos, from), pr = __shfl_sync(0xFFFFFFFFu, prow, from);
+        const float rm = __shfl_sync(0xFFFFFFFFu, m, from), rs = __shfl_sync(0xFFFFFFFFu, scale, from);
+        if (!kSparse && !odd_after<kBf16>(L, u, rp)) continue;
+        const float4 o = row_again<kBf16, kSparse>(L, u, rt, u.kvh * p.n + rh, rp, rm);
+        if (!u.pair && lane >> 4 != me) continue;  // this half of the dims
+        if (u.slot >= 0)
+          reinterpret_cast<float4*>(L.ws + L.o_off)[((int64_t)u.slot * L.rows + pr) * 32 + lane] = o;
+        else
+          reinterpret_cast<uint2*>(p.o)[((int64_t)rt * p.H + u.kvh * p.n + rh) * 32 + lane] =
+              make_uint2(pair_of<kBf16>(o.x * rs, o.y * rs), pair_of<kBf16>(o.z * rs, o.w * rs));
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 11) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+  }
+}
+
+// Joins the shares of cut units.  Block (c - 1, y) looks after the unit that CTA
+// c's share begins in, if no CTA's before c does; eight warps take every eighth
+// share, eight rows at a time.
+template <bool kBf16>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launch L) {
+  __shared__ float part[8][8][kKvDim];
+  __shared__ float part_l[8][8];
+  __shared__ int16_t pieces[kMaxCtas + 1];  // slots
+  __shared__ int s_n;
   let_next_start();
   wait_for_previous();
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int t = (int)(w / p.H), h = (int)(w % p.H), g = h / p.n;
-  if (t >= p.T) return;
-  const int r = request_of_token(p.first, p.R, t);
-  if (r < 0) return;
-  const Request rq = request_of(p.first, p.lens, r, p.T);
-  if (t < rq.a || t >= rq.b) return;
-  const int pos = rq.pos0 < 0 ? -1 : rq.pos0 + (t - rq.a);
-  const char* q = static_cast<const char*>(p.q) + 2 * (t * p.q_stride + h * kKvDim);
-  const int32_t* table = p.tables + (int64_t)r * p.P;
-  Row<kBf16> row;
-  if (p.idx) {
-    const int32_t* idx = p.idx + ((int64_t)t * p.kv_heads + g) * p.select;
-    for (int i = 0; i < p.select && idx[i] >= 0; ++i)
-      if (idx[i] < p.P && pos >= 0 && idx[i] <= pos >> p.shift)
-        row.page(p, q, g, table[idx[i]], 0, min(p.page, pos - (idx[i] << p.shift) + 1));
-  } else {
-    for (int j = 0; j < p.P && (int64_t)j * p.page <= pos; ++j)
-      row.page(p, q, g, table[j], 0, (int)min((int64_t)p.page, pos - (int64_t)j * p.page + 1));
+  const Cut* cuts = reinterpret_cast<const Cut*>(L.ws);
+  const int ctas = *reinterpret_cast<const int32_t*>(L.ws + kMaxCtas * sizeof(Cut));
+  const int c = blockIdx.x + 1;
+  if (c >= ctas) return;
+  const Cut u = cuts[c];
+  if (u.at <= 0 || u.at >= u.tiles) return;
+  auto same = [&](const Cut& x) { return x.r == u.r && x.kvh == u.kvh && x.t0 == u.t0; };
+  if (c > 1 && same(cuts[c - 1]) && cuts[c - 1].at > 0) return;
+  const KvParams& p = L.p;
+  const int rows = u.pair ? 128 + (u.ntok - L.tpt) * p.n : u.ntok * p.n;
+  if (8 * (int)blockIdx.y >= rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    int n = 0, at = u.at;
+    pieces[n++] = (int16_t)(2 * (c - 1) + 1);
+    for (int e = c; at < u.tiles; ++e) {
+      int to = u.tiles;
+      if (e + 1 < ctas) {
+        const Cut x = cuts[e + 1];
+        if (same(x)) to = x.at;
+      }
+      if (to > at) pieces[n++] = (int16_t)(2 * e);
+      at = to;
+    }
+    s_n = n;
   }
-  const float inv = row.l == 0.f ? 0.f : 1.f / row.l;
-  const int64_t out = (int64_t)t * p.H + h;
-  reinterpret_cast<uint2*>(static_cast<char*>(p.o) + 2 * kKvDim * out)[lane] =
-      make_uint2(pair_of<kBf16>(row.o[0] * inv, row.o[1] * inv), pair_of<kBf16>(row.o[2] * inv, row.o[3] * inv));
-  if (lane == 0) p.lse[out] = row.l == 0.f ? -INFINITY : (row.m + log2f(row.l)) * 0.6931471805599453f;
+  __syncthreads();
+  const int n = s_n;
+  const float2* ml = reinterpret_cast<const float2*>(L.ws + L.ml_off);
+  const float4* po = reinterpret_cast<const float4*>(L.ws + L.o_off);
+  for (int r0 = 8 * blockIdx.y; r0 < rows; r0 += 8 * gridDim.y) {
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m[i] = -INFINITY;
+      for (int x = lane; x < n; x += 32)
+        if (r0 + i < rows) m[i] = fmaxf(m[i], ml[(int64_t)pieces[x] * L.rows + r0 + i].x);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
+      if (m[i] == -INFINITY) m[i] = 0.f;
+    }
+    float4 acc[8];
+    float l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      l[i] = 0.f;
+    }
+    for (int x = warp; x < n; x += 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (r0 + i >= rows) continue;
+        const int64_t at = (int64_t)pieces[x] * L.rows + r0 + i;
+        const float2 y = ml[at];
+        const float4 o = po[at * 32 + lane];
+        if (y.y == 0.f) continue;  // nothing attended to
+        const float a = ex2(y.x - m[i]);
+        l[i] += a * y.y;
+        acc[i].x += a * o.x;
+        acc[i].y += a * o.y;
+        acc[i].z += a * o.z;
+        acc[i].w += a * o.w;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      *reinterpret_cast<float4*>(&part[warp][i][4 * lane]) = acc[i];
+      if (lane == 0) part_l[warp][i] = l[i];
+    }
+    __syncthreads();
+    // warp i finishes row i
+    const int r = r0 + warp;
+    const int in = r & 127;
+    const int tok = in / p.n + (r >= 128 ? L.tpt : 0), head = in % p.n;
+    if (r < rows && in / p.n < L.tpt) {
+      float sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        sum += part_l[w][warp];
+        const float4 x = *reinterpret_cast<const float4*>(&part[w][warp][4 * lane]);
+        o.x += x.x;
+        o.y += x.y;
+        o.z += x.z;
+        o.w += x.w;
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i == warp) top = m[i];
+      const int64_t out = (int64_t)(u.t0 + tok) * p.H + u.kvh * p.n + head;
+      reinterpret_cast<uint2*>(p.o)[out * 32 + lane] =
+          make_uint2(pair_of<kBf16>(o.x * inv, o.y * inv), pair_of<kBf16>(o.z * inv, o.w * inv));
+      if (lane == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    }
+    __syncthreads();
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }
+  return fn;
+}
+
+// [outer, heads, 128] of 16 bits with `stride` elements from one outer row to the
+// next; boxes of 64 dims by box_heads by box_rows, 128B-swizzled.  Rows past
+// `outer` read as zeros.
+bool make_map(CUtensorMap* map, bool bf16, const void* ptr, uint64_t heads, uint64_t outer, uint64_t stride,
+              uint32_t box_heads, uint32_t box_rows) {
+  const auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kKvDim, heads, outer};
+  cuuint64_t strides[2] = {2 * kKvDim, 2 * stride};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
+  cuuint32_t step[3] = {1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr),
+             dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// SMs of the current device, read once a device (0: no device).
+int device_sms() {
+  static int cache[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0) {
+    if (dev < 64 && cache[dev]) return cache[dev];
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) {
+      if (dev < 64) cache[dev] = n;
+      return n;
+    }
+  }
+  cudaGetLastError();
+  return 0;
+}
+
+// The workspace and the grid, from the shapes: as many CTAs as there may be shares
+// of kLeast, an SM each.
+Sizes sizes_of(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests, int32_t table_width,
+               int32_t select, int32_t sms) {
+  Sizes s;
+  const int64_t n = heads / cfg->kv_heads, tpt = 128 / n, tpu = select ? tpt : 2 * tpt;
+  const int64_t units = (std::min(tokens, requests) + tokens / tpu) * cfg->kv_heads;
+  const int64_t keys = select ? (int64_t)select * cfg->page_size : (int64_t)table_width * cfg->page_size;
+  const int64_t most = units * (keys + kUnitCost) / kLeast;
+  s.ctas = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxCtas), most));
+  s.rows = (int32_t)(tokens * n <= 128 || select ? std::min<int64_t>(tokens * n, 128) : 256);
+  s.ml_off = fused_align16(kMaxCtas * (int64_t)sizeof(Cut) + 16);
+  s.o_off = s.ml_off + fused_align16((int64_t)2 * s.ctas * s.rows * 8);
+  s.bytes = s.o_off + (int64_t)2 * s.ctas * s.rows * kKvDim * 4;
+  return s;
+}
+
+template <bool kBf16, bool kSparse>
+int launch(const Launch& L, const Sizes& sz, cudaStream_t stream) {
+  static bool ready[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return DSA_ERR_CUDA;
+  }
+  if (dev < 0 || dev >= 64 || !ready[dev]) {
+    cudaFuncAttributes fa;
+    if (cudaFuncSetAttribute(attend_kernel<kBf16, kSparse>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+            cudaSuccess ||
+        cudaFuncGetAttributes(&fa, attend_kernel<kBf16, kSparse>) != cudaSuccess) {
+      cudaGetLastError();
+      return DSA_ERR_CUDA;
+    }
+    // the register split needs the whole launch allocation it was sized for
+    if (fa.numRegs < kLaunchRegs) return DSA_ERR_UNSUPPORTED;
+    if (dev >= 0 && dev < 64) ready[dev] = true;
+  }
+  const int rc = launch_dependent(attend_kernel<kBf16, kSparse>, sz.ctas, kThreads, kSmem, 0, stream, L);
+  if (rc != DSA_OK || sz.ctas == 1) return rc;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(sz.ctas - 1), (unsigned)std::min(4, (sz.rows + 7) / 8));
+  lc.blockDim = dim3(256);
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, join_kernel<kBf16>, L) != cudaSuccess) {
+    cudaGetLastError();
+    return DSA_ERR_CUDA;
+  }
+  return launched();
 }
 
 int attend(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests, int32_t table_width,
@@ -112,8 +1350,17 @@ int attend(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t request
       misaligned(tables, 4) || misaligned(lse, 4))
     return DSA_ERR_INVALID_ARG;
   if (tokens > 1 && (q_stride < (int64_t)heads * kKvDim || (q_stride & 7))) return DSA_ERR_INVALID_ARG;
-  if (workspace_bytes < 16) return DSA_ERR_INVALID_ARG;
-  KvParams p;
+  if (tokens > 1 && q_stride >= (int64_t)1 << 38) return DSA_ERR_UNSUPPORTED;  // a tensor map's strides
+  // the workspace of the widest device: its size does not depend on the device
+  const Sizes most = sizes_of(cfg, tokens, heads, requests, table_width, select, kMaxCtas);
+  if (workspace_bytes < (size_t)most.bytes) return DSA_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (!sms) return DSA_ERR_CUDA;
+  const Sizes sz = sizes_of(cfg, tokens, heads, requests, table_width, select, sms);
+  const bool bf16 = cfg->dtype == DSA_BF16;
+  Launch L;
+  memset(&L, 0, sizeof(L));
+  KvParams& p = L.p;
   p.k = k_cache;
   p.v = v_cache;
   p.q = q;
@@ -123,7 +1370,7 @@ int attend(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t request
   p.tables = tables;
   p.o = o;
   p.lse = lse;
-  p.q_stride = tokens > 1 ? q_stride : 0;
+  p.q_stride = tokens > 1 ? q_stride : (int64_t)heads * kKvDim;
   p.T = tokens;
   p.H = heads;
   p.n = heads / cfg->kv_heads;
@@ -137,9 +1384,32 @@ int attend(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t request
   p.flip = c < 0.f;
   // not 0: a masked score of -inf times it stays -inf
   p.c2 = std::max(c < 0.f ? -c : c, 1.17549435e-38f);
-  const int64_t blocks = ((int64_t)tokens * heads + 7) / 8;
-  return cfg->dtype == DSA_BF16 ? launch_dependent(row_kernel<true>, blocks, 256, 0, 0, stream, p)
-                                : launch_dependent(row_kernel<false>, blocks, 256, 0, 0, stream, p);
+  L.tpt = 128 / p.n;
+  L.log_cpt = 7 - p.shift;
+  L.rows = sz.rows;
+  L.ws = static_cast<uint8_t*>(workspace);
+  L.ml_off = sz.ml_off;
+  L.o_off = sz.o_off;
+  // a cache of no pages: a map of one row that no box touches
+  const uint64_t slots = std::max<uint64_t>(1, (uint64_t)cfg->pages * cfg->page_size);
+  const void* kp = cfg->pages ? k_cache : q;
+  const void* vp = cfg->pages ? v_cache : q;
+  const uint64_t kv = cfg->pages ? (uint64_t)p.kv_heads : 1;
+  if (!make_map(&L.q, bf16, q, (uint64_t)heads, (uint64_t)tokens, (uint64_t)p.q_stride, (uint32_t)p.n, (uint32_t)L.tpt) ||
+      !make_map(&L.k, bf16, kp, kv, slots, kv * kKvDim, 1, (uint32_t)p.page) ||
+      !make_map(&L.v, bf16, vp, kv, slots, kv * kKvDim, 1, (uint32_t)p.page))
+    return DSA_ERR_CUDA;
+  if (select) return bf16 ? launch<true, true>(L, sz, stream) : launch<false, true>(L, sz, stream);
+  return bf16 ? launch<true, false>(L, sz, stream) : launch<false, false>(L, sz, stream);
+}
+
+int workspace_of(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests, int32_t table_width,
+                 int32_t select, size_t* bytes) {
+  const int rc = check_kv_step(cfg, tokens, heads, requests, table_width);
+  if (rc != DSA_OK) return rc;
+  if (!bytes) return DSA_ERR_INVALID_ARG;
+  *bytes = (size_t)sizes_of(cfg, tokens, heads, requests, table_width, select, kMaxCtas).bytes;
+  return DSA_OK;
 }
 
 }  // namespace
@@ -148,11 +1418,7 @@ extern "C" {
 
 int dsa_kv_attention_workspace(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests,
                                int32_t table_width, size_t* bytes) {
-  const int rc = check_kv_step(cfg, tokens, heads, requests, table_width);
-  if (rc != DSA_OK) return rc;
-  if (!bytes) return DSA_ERR_INVALID_ARG;
-  *bytes = 16;
-  return DSA_OK;
+  return workspace_of(cfg, tokens, heads, requests, table_width, 0, bytes);
 }
 
 int dsa_kv_attention(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests, int32_t table_width,
@@ -169,10 +1435,9 @@ int dsa_kv_block_attention_workspace(const dsa_kv_cfg* cfg, int32_t tokens, int3
                                      int32_t table_width, int32_t select, size_t* bytes) {
   const int rc = check_kv_step(cfg, tokens, heads, requests, table_width);
   if (rc != DSA_OK) return rc;
-  if (!bytes || select < 1) return DSA_ERR_INVALID_ARG;
+  if (select < 1) return DSA_ERR_INVALID_ARG;
   if (select > 4096) return DSA_ERR_UNSUPPORTED;
-  *bytes = 16;
-  return DSA_OK;
+  return workspace_of(cfg, tokens, heads, requests, table_width, select, bytes);
 }
 
 int dsa_kv_block_attention(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests,
@@ -189,6 +1454,13 @@ int dsa_kv_block_attention(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads,
                 tables, scale, workspace, workspace_bytes, o, lse, stream);
 }
 
-int dsa_kv_status(void) { return cudaDeviceSynchronize() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
+int dsa_kv_status(void) {
+  int v = 0, zero = 0;
+  // the copies alone wait for no stream but the default one and those that block it
+  if (cudaDeviceSynchronize() != cudaSuccess) return DSA_ERR_CUDA;
+  if (cudaMemcpyFromSymbol(&v, g_kv_error, sizeof(int)) != cudaSuccess) return DSA_ERR_CUDA;
+  if (v && cudaMemcpyToSymbol(g_kv_error, &zero, sizeof(int)) != cudaSuccess) return DSA_ERR_CUDA;
+  return v ? DSA_ERR_TIMEOUT : DSA_OK;
+}
 
 }  // extern "C"
