@@ -1,12 +1,12 @@
-// cache_calls.cpp -- the ordinary form of the cache's calls from Python: every
+// cache_calls.cpp -- the ordinary form of the two caches' calls from Python: every
 // tensor as the C ABI wants it, on the current device, on the current stream.
 //
 // A decode step's kernels take 2 to 6 us, and so does a call whose dozen tensors
 // are looked at attribute by attribute from Python: a plan took 8.3 us on the
 // host, an attention call 7.9, a read 5.8.  Here the same checks are made on the
 // tensors themselves.  A function returns the C ABI's status, or None for any
-// call that is not ordinary; cache.py then makes the call, or says what is wrong
-// with it.
+// call that is not ordinary; cache.py (kv.py) then makes the call, or says what is
+// wrong with it.
 
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -35,14 +35,23 @@ Library lib;
 PyObject* cfg_type;  // cache.py's dsa_cache_cfg
 bool host_tensors;   // tensors of the host stand in for a device's (the tests' stubs)
 
+struct KvLibrary {
+  decltype(&dsa_kv_append) append;
+  decltype(&dsa_kv_attention) attention;
+  decltype(&dsa_kv_select) select;
+  decltype(&dsa_kv_block_attention) blocks;
+};
+KvLibrary kv;
+PyObject* kv_type;  // kv.py's dsa_kv_cfg
+
 // The arguments of one call.
 class Call {
  public:
-  explicit Call(PyObject* cfg) {
-    ok_ = (PyObject*)Py_TYPE(cfg) == cfg_type && PyObject_GetBuffer(cfg, &view_, PyBUF_SIMPLE) == 0;
+  explicit Call(PyObject* cfg, PyObject* type = cfg_type, size_t size = sizeof(dsa_cache_cfg)) {
+    ok_ = (PyObject*)Py_TYPE(cfg) == type && PyObject_GetBuffer(cfg, &view_, PyBUF_SIMPLE) == 0;
     held_ = ok_;
     if (!ok_) PyErr_Clear();
-    ok_ = ok_ && view_.len == (Py_ssize_t)sizeof(dsa_cache_cfg);
+    ok_ = ok_ && view_.len == (Py_ssize_t)size;
   }
   ~Call() {
     if (held_) PyBuffer_Release(&view_);
@@ -52,6 +61,7 @@ class Call {
 
   explicit operator bool() const { return ok_; }
   const dsa_cache_cfg* cfg() const { return static_cast<const dsa_cache_cfg*>(view_.buf); }
+  const dsa_kv_cfg* kv() const { return static_cast<const dsa_kv_cfg*>(view_.buf); }
 
   // A tensor without surprises, on the device of the others.
   const at::Tensor* tensor(PyObject* o) {
@@ -262,6 +272,190 @@ PyObject* prompt(PyObject* const* a) {
   });
 }
 
+// ---------------------------------------------------------------------------
+// the 16-bit cache
+
+// A call on it, its type and limits as kv.py and the C ABI check them.
+class KvCall : public Call {
+ public:
+  explicit KvCall(PyObject* cfg) : Call(cfg, kv_type, sizeof(dsa_kv_cfg)) {
+    if (!*this) return;
+    const dsa_kv_cfg* c = kv();
+    type_ = c->dtype == DSA_BF16 ? at::kBFloat16 : at::kHalf;
+    if ((c->dtype != DSA_BF16 && c->dtype != DSA_F16) || c->pages < 0 || c->page_size < 1 || c->page_size > 4096 ||
+        c->kv_heads < 1 || c->kv_heads > 64)
+      number(-1);
+  }
+  void* pool(PyObject* o, int64_t positions) {
+    return *this ? even(data<void>(o, type_, kv()->pages * positions * kv()->kv_heads * kDim)) : nullptr;
+  }
+  // Memory on a 16-byte boundary.
+  template <typename T>
+  T* even(T* p) {
+    if ((uintptr_t)p & 15) number(-1);
+    return p;
+  }
+  // Rows [T, H, 128] of the cache's type whose heads and dims are packed.
+  struct Rows {
+    const void* p;
+    int64_t T, H, stride;
+  };
+  Rows rows(PyObject* o) {
+    Rows r = {nullptr, 0, 0, 0};
+    const at::Tensor* t = tensor(o);
+    if (!t || t->scalar_type() != type_ || t->dim() != 3 || t->size(2) != kDim) {
+      number(-1);
+      return r;
+    }
+    r.T = t->size(0);
+    r.H = t->size(1);
+    r.stride = token_stride(*t, r.T, r.H);
+    r.p = even(t->data_ptr());
+    if (r.stride < 0 || r.stride & 7 || r.T > INT32_MAX || r.H > INT32_MAX || r.T * r.H > INT32_MAX) number(-1);
+    return r;
+  }
+  at::ScalarType type() const { return type_; }
+
+ private:
+  at::ScalarType type_ = at::kHalf;
+};
+
+// What the calls of a step share.
+struct KvStep {
+  KvCall::Rows q;
+  int32_t T, H, R, P;
+  const int32_t *first, *lens, *tables;
+  uint8_t* workspace;
+  size_t bytes;
+};
+bool kv_step(KvCall& c, PyObject* q, PyObject* first, PyObject* lens, PyObject* tables, PyObject* workspace, KvStep* s) {
+  s->q = c.rows(q);
+  const at::Tensor* l = c.tensor(lens);
+  const at::Tensor* t = c.tensor(tables);
+  const at::Tensor* w = c.tensor(workspace);
+  if (!c || t->dim() != 2 || t->size(0) != l->numel()) return false;
+  s->T = (int32_t)s->q.T;
+  s->H = (int32_t)s->q.H;
+  s->R = c.number(l->numel());
+  s->P = c.number(t->size(1));
+  s->lens = c.ints(lens, 0);
+  s->first = c.ints(first, (int64_t)s->R + 1);
+  s->tables = c.ints(tables, 0);
+  s->workspace = c.even(c.data<uint8_t>(workspace, at::kByte, 0));
+  s->bytes = (size_t)w->numel();
+  return (bool)c;
+}
+// idx [T, kv_heads, select]
+int32_t* kv_lists(KvCall& c, PyObject* o, int64_t T, int32_t* select) {
+  const at::Tensor* t = c.tensor(o);
+  if (!c || t->dim() != 3 || t->size(0) != T || t->size(1) != c.kv()->kv_heads) {
+    c.number(-1);
+    return nullptr;
+  }
+  *select = c.number(t->size(2));
+  return c.ints(o, 0);
+}
+int32_t kv_int(KvCall& c, PyObject* o) {
+  const long x = PyLong_CheckExact(o) ? PyLong_AsLong(o) : -1;
+  if (x < 0 || x > INT32_MAX) {
+    PyErr_Clear();
+    c.number(-1);
+  }
+  return (int32_t)x;
+}
+
+// cfg, q, k, v, ends, slots, turns, neighbours, gain, q_out, k_cache, v_cache, means
+PyObject* kv_append(PyObject* const* a) {
+  KvCall c(a[0]);
+  const at::Tensor* slots = c.tensor(a[5]);
+  const at::Tensor* turns = c.tensor(a[6]);
+  if (!c || !PyBool_Check(a[7])) Py_RETURN_NONE;
+  const int32_t T = c.number(slots->numel()), rotary = c.number(2 * turns->numel());
+  const bool queries = a[1] != Py_None;
+  KvCall::Rows q = {nullptr, T, 0, 0};
+  if (queries) q = c.rows(a[1]);
+  const KvCall::Rows k = c.rows(a[2]), v = c.rows(a[3]);
+  const int32_t *ends = c.ints(a[4], T), *at = c.ints(a[5], 0);
+  const int64_t* tn = c.data<int64_t>(a[6], at::kLong, 0);
+  const float gain = c.real(a[8]);
+  if (!c || q.T != T || k.T != T || v.T != T || k.H != c.kv()->kv_heads || v.H != k.H) Py_RETURN_NONE;
+  void* out = queries ? c.even(c.data<void>(a[9], c.type(), q.T * q.H * kDim)) : nullptr;
+  void *kc = c.pool(a[10], c.kv()->page_size), *vc = c.pool(a[11], c.kv()->page_size);
+  void* means = a[12] != Py_None ? c.pool(a[12], 1) : nullptr;
+  const bool turned = a[7] == Py_True;
+  CUstream_st* s = c.stream();
+  return launch(c, [&] {
+    return kv.append(c.kv(), T, (int32_t)q.H, rotary, turned, gain, q.p, q.stride, k.p, k.stride, v.p, v.stride, ends, at,
+                     tn, out, kc, vc, means, s);
+  });
+}
+
+// cfg, k_cache, v_cache, q, first, lens, tables, scale, workspace, o, lse
+PyObject* kv_attention(PyObject* const* a) {
+  KvCall c(a[0]);
+  KvStep x;
+  if (!kv_step(c, a[3], a[4], a[5], a[6], a[8], &x)) Py_RETURN_NONE;
+  const void *k = c.pool(a[1], c.kv()->page_size), *v = c.pool(a[2], c.kv()->page_size);
+  const float scale = c.real(a[7]);
+  void* o = c.even(c.data<void>(a[9], c.type(), x.q.T * x.q.H * kDim));
+  float* lse = c.data<float>(a[10], at::kFloat, x.q.T * x.q.H);
+  CUstream_st* s = c.stream();
+  return launch(c, [&] {
+    return kv.attention(c.kv(), x.T, x.H, x.R, x.P, k, v, x.q.p, x.q.stride, x.first, x.lens, x.tables, scale, x.workspace,
+                        x.bytes, o, lse, s);
+  });
+}
+
+// cfg, means, q, first, lens, tables, lead, trail, workspace, idx
+PyObject* kv_select(PyObject* const* a) {
+  KvCall c(a[0]);
+  KvStep x;
+  if (!kv_step(c, a[2], a[3], a[4], a[5], a[8], &x)) Py_RETURN_NONE;
+  const void* means = c.pool(a[1], 1);
+  const int32_t lead = kv_int(c, a[6]), trail = kv_int(c, a[7]);
+  int32_t n = 0;
+  int32_t* idx = kv_lists(c, a[9], x.T, &n);
+  CUstream_st* s = c.stream();
+  return launch(c, [&] {
+    return kv.select(c.kv(), x.T, x.H, x.R, x.P, n, lead, trail, means, x.q.p, x.q.stride, x.first, x.lens, x.tables,
+                     x.workspace, x.bytes, idx, s);
+  });
+}
+
+// cfg, k_cache, v_cache, q, idx, first, lens, tables, scale, workspace, o, lse
+PyObject* kv_blocks(PyObject* const* a) {
+  KvCall c(a[0]);
+  KvStep x;
+  if (!kv_step(c, a[3], a[5], a[6], a[7], a[9], &x)) Py_RETURN_NONE;
+  const void *k = c.pool(a[1], c.kv()->page_size), *v = c.pool(a[2], c.kv()->page_size);
+  int32_t n = 0;
+  const int32_t* idx = kv_lists(c, a[4], x.T, &n);
+  const float scale = c.real(a[8]);
+  void* o = c.even(c.data<void>(a[10], c.type(), x.q.T * x.q.H * kDim));
+  float* lse = c.data<float>(a[11], at::kFloat, x.q.T * x.q.H);
+  CUstream_st* s = c.stream();
+  return launch(c, [&] {
+    return kv.blocks(c.kv(), x.T, x.H, x.R, x.P, n, k, v, x.q.p, x.q.stride, idx, x.first, x.lens, x.tables, scale,
+                     x.workspace, x.bytes, o, lse, s);
+  });
+}
+
+// bind_kv(cfg type, host tensors, addresses of the four functions in KvLibrary's order)
+PyObject* bind_kv(PyObject*, PyObject* args) {
+  PyObject* type;
+  int host;
+  unsigned long long p[4];
+  if (!PyArg_ParseTuple(args, "OpKKKK", &type, &host, &p[0], &p[1], &p[2], &p[3])) return nullptr;
+  Py_INCREF(type);
+  Py_XSETREF(kv_type, type);
+  host_tensors = host != 0;
+  kv.append = reinterpret_cast<decltype(kv.append)>((uintptr_t)p[0]);
+  kv.attention = reinterpret_cast<decltype(kv.attention)>((uintptr_t)p[1]);
+  kv.select = reinterpret_cast<decltype(kv.select)>((uintptr_t)p[2]);
+  kv.blocks = reinterpret_cast<decltype(kv.blocks)>((uintptr_t)p[3]);
+  Py_RETURN_NONE;
+}
+
 // bind(cfg type, host tensors, addresses of the six functions in Library's order)
 PyObject* bind(PyObject*, PyObject* args) {
   PyObject* type;
@@ -288,11 +482,16 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, nullptr},
+    {"bind_kv", bind_kv, METH_VARARGS, nullptr},
     method<plan, 12>("plan"),
     method<write, 5>("write"),
     method<read, 5>("read"),
     method<attention, 9>("attention"),
     method<prompt, 9>("prompt"),
+    method<kv_append, 13>("kv_append"),
+    method<kv_attention, 11>("kv_attention"),
+    method<kv_select, 10>("kv_select"),
+    method<kv_blocks, 12>("kv_blocks"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "cache_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1133,9 +1133,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 template <bool kBf16>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launch L) {
   __shared__ float part[8][8][kKvDim];
-  __shared__ float part_l[8][8];
-  __shared__ int16_t pieces[kMaxCtas + 1];  // slots
-  __shared__ int s_n;
+  __shared__ float part_l[8][8], top[8];
+  __shared__ int16_t slots[kMaxCtas + 1];  // of the workspace, -1: an empty share
+  __shared__ int s_last;
   let_next_start();
   wait_for_previous();
   const Cut* cuts = reinterpret_cast<const Cut*>(L.ws);
@@ -1145,40 +1145,39 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launc
   const Cut u = cuts[c];
   if (u.at <= 0 || u.at >= u.tiles) return;
   auto same = [&](const Cut& x) { return x.r == u.r && x.kvh == u.kvh && x.t0 == u.t0; };
-  if (c > 1 && same(cuts[c - 1]) && cuts[c - 1].at > 0) return;
+  if (c > 1) {
+    const Cut x = cuts[c - 1];
+    if (same(x) && x.at > 0) return;
+  }
   const KvParams& p = L.p;
   const int rows = u.pair ? 128 + (u.ntok - L.tpt) * p.n : u.ntok * p.n;
   if (8 * (int)blockIdx.y >= rows) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    int n = 0, at = u.at;
-    pieces[n++] = (int16_t)(2 * (c - 1) + 1);
-    for (int e = c; at < u.tiles; ++e) {
-      int to = u.tiles;
-      if (e + 1 < ctas) {
-        const Cut x = cuts[e + 1];
-        if (same(x)) to = x.at;
-      }
-      if (to > at) pieces[n++] = (int16_t)(2 * e);
-      at = to;
-    }
-    s_n = n;
+  if (threadIdx.x == 0) s_last = c;
+  __syncthreads();
+  // the unit's last share is that of the last CTA whose own begins in it
+  for (int e = c + 1 + (int)threadIdx.x; e < ctas; e += 256)
+    if (same(cuts[e])) atomicMax(&s_last, e);
+  __syncthreads();
+  const int n = s_last - c + 2;
+  for (int x = threadIdx.x; x < n; x += 256) {  // share x: CTA c - 1 + x's
+    const int e = c - 1 + x;
+    const int from = x == 0 ? 0 : cuts[e].at, to = e == s_last ? u.tiles : cuts[e + 1].at;
+    slots[x] = (int16_t)(to <= from ? -1 : x == 0 ? 2 * e + 1 : 2 * e);
   }
   __syncthreads();
-  const int n = s_n;
   const float2* ml = reinterpret_cast<const float2*>(L.ws + L.ml_off);
   const float4* po = reinterpret_cast<const float4*>(L.ws + L.o_off);
   for (int r0 = 8 * blockIdx.y; r0 < rows; r0 += 8 * gridDim.y) {
-    float m[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m[i] = -INFINITY;
+    {  // warp i: the largest maximum of row i
+      float m = -INFINITY;
       for (int x = lane; x < n; x += 32)
-        if (r0 + i < rows) m[i] = fmaxf(m[i], ml[(int64_t)pieces[x] * L.rows + r0 + i].x);
+        if (slots[x] >= 0 && r0 + warp < rows) m = fmaxf(m, ml[(int64_t)slots[x] * L.rows + r0 + warp].x);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
-      if (m[i] == -INFINITY) m[i] = 0.f;
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      if (lane == 0) top[warp] = m == -INFINITY ? 0.f : m;
     }
+    __syncthreads();
     float4 acc[8];
     float l[8];
 #pragma unroll
@@ -1187,19 +1186,25 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launc
       l[i] = 0.f;
     }
     for (int x = warp; x < n; x += 8) {
+      const int slot = slots[x];
+      if (slot < 0) continue;
+      float2 y[8];
+      float4 o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (r0 + i >= rows) continue;
-        const int64_t at = (int64_t)pieces[x] * L.rows + r0 + i;
-        const float2 y = ml[at];
-        const float4 o = po[at * 32 + lane];
-        if (y.y == 0.f) continue;  // nothing attended to
-        const float a = ex2(y.x - m[i]);
-        l[i] += a * y.y;
-        acc[i].x += a * o.x;
-        acc[i].y += a * o.y;
-        acc[i].z += a * o.z;
-        acc[i].w += a * o.w;
+        const int64_t at = (int64_t)slot * L.rows + min(r0 + i, rows - 1);
+        y[i] = ml[at];
+        o[i] = po[at * 32 + lane];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (y[i].y == 0.f) continue;  // nothing attended to
+        const float a = ex2(y[i].x - top[i]);
+        l[i] += a * y[i].y;
+        acc[i].x += a * o[i].x;
+        acc[i].y += a * o[i].y;
+        acc[i].z += a * o[i].z;
+        acc[i].w += a * o[i].w;
       }
     }
 #pragma unroll
@@ -1225,14 +1230,10 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launc
         o.w += x.w;
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i == warp) top = m[i];
       const int64_t out = (int64_t)(u.t0 + tok) * p.H + u.kvh * p.n + head;
       reinterpret_cast<uint2*>(p.o)[out * 32 + lane] =
           make_uint2(pair_of<kBf16>(o.x * inv, o.y * inv), pair_of<kBf16>(o.z * inv, o.w * inv));
-      if (lane == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      if (lane == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top[warp] + log2f(sum)) * 0.6931471805599453f;
     }
     __syncthreads();
   }

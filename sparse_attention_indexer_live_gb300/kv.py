@@ -5,18 +5,20 @@
 As in cache.py, every argument is checked here before a pointer reaches the C
 ABI: TypeError for a wrong type, ValueError for a wrong device, layout or size.
 The work runs on the current stream of the tensors' own device unless a stream
-of that device is given.
+of that device is given.  Ordinary calls are checked and made by the module built
+from csrc/cache_calls.cpp, as cache.py's are (FIGURES).
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
 import math
+import warnings
 
 import torch
 
 from . import binding
-from .cache import _I32, _count, _device_of, _need, cache_cfg, dsa_cache_plan, refusal
+from .cache import _I32, _count, _device_of, _load_calls, _made, _need, cache_cfg, dsa_cache_plan, refusal
 
 _DIM = 128
 _TYPES = {torch.bfloat16: 0, torch.float16: 1}
@@ -117,8 +119,23 @@ def _table(tables, R, dev):
     return _count("tables", tables.shape[1])
 
 
+_calls = None  # the module of ordinary calls, once the library is loaded; False where there is none
+
+
+def _bound(functions=None, host=False):
+    """The module of ordinary calls, bound to the library's functions (or those
+    given, with tensors of the host in place of a device's)."""
+    m = _load_calls()
+    if functions is None:
+        L = binding.load()
+        functions = [getattr(L, "dsa_kv_" + n) for n in ("append", "attention", "select", "block_attention")]
+    m.bind_kv(dsa_kv_cfg, host, *(ctypes.cast(f, ctypes.c_void_p).value for f in functions))
+    return m
+
+
 def _call(name, dev, stream, *args):
     """The library's `name`(*args, stream) with `dev` current."""
+    global _calls
     if stream is None:
         s = torch.cuda.current_stream(dev).cuda_stream
     else:
@@ -126,6 +143,13 @@ def _call(name, dev, stream, *args):
             raise ValueError(f"stream: of cuda:{stream.device.index}, the tensors are on cuda:{dev}")
         s = stream.cuda_stream
     fn = getattr(binding.load(), name)
+    if _calls is None:
+        try:
+            _calls = _bound()
+        except (OSError, ImportError) as e:
+            _calls = False
+            warnings.warn(f"cache_calls is not used, the cache's calls take a few us more each: {e}", RuntimeWarning,
+                          stacklevel=3)
     with torch.cuda.device(dev):
         binding._check(fn(*args, s), name)
 
@@ -180,6 +204,10 @@ def dsa_kv_append(cfg: dsa_kv_cfg, q, k, v, ends, slots, turns, neighbours: bool
     v [T, kv_heads, 128] to the slots [T] int32 of k_cache and v_cache; ends
     [T] int32 the positions + 1, turns [rotary / 2] int64 (rotary_turns).
     means (or None): the mean keys of the pages that this fills."""
+    if stream is None and _calls and _made(
+            _calls.kv_append(cfg, q, k, v, ends, slots, turns, neighbours, gain, q_out, k_cache, v_cache, means),
+            "dsa_kv_append"):
+        return
     dtype = _cfg(cfg)
     dev = _device_of("slots", slots, _I32)
     T = _count("slots", slots.numel())
@@ -217,6 +245,10 @@ def dsa_kv_attention(cfg: dsa_kv_cfg, k_cache, v_cache, q, first, lens, tables, 
     """Causal attention of a step's tokens q [T, H, 128], request after
     request: first [R + 1], lens [R], tables [R, P] int32 (a plan's); writes o
     [T, H, 128] and lse [T, H] f32."""
+    if stream is None and _calls and _made(
+            _calls.kv_attention(cfg, k_cache, v_cache, q, first, lens, tables, scale, workspace, o, lse),
+            "dsa_kv_attention"):
+        return
     dtype, dev, T, H, stride, R, P = _step(cfg, q, first, lens, tables, workspace)
     _pool(cfg, "k_cache", k_cache, dtype, dev, cfg.page_size)
     _pool(cfg, "v_cache", v_cache, dtype, dev, cfg.page_size)
@@ -237,6 +269,9 @@ def dsa_kv_select(cfg: dsa_kv_cfg, means, q, first, lens, tables, lead: int, tra
     """The pages that each token's queries score highest by the mean keys,
     the first `lead` and the last `trail` taken always: idx [T, kv_heads,
     select] int32, ascending page numbers of the request, then -1."""
+    if stream is None and _calls and _made(
+            _calls.kv_select(cfg, means, q, first, lens, tables, lead, trail, workspace, idx), "dsa_kv_select"):
+        return
     dtype, dev, T, H, stride, R, P = _step(cfg, q, first, lens, tables, workspace)
     _pool(cfg, "means", means, dtype, dev, 1)
     n = _lists(cfg, idx, T, dev)
@@ -259,6 +294,10 @@ def dsa_kv_block_attention(cfg: dsa_kv_cfg, k_cache, v_cache, q, idx, first, len
                            lse, stream=None):
     """dsa_kv_attention to the pages idx [T, kv_heads, select] int32 (strictly
     ascending, then -1; a selection of dsa_kv_select's) lists."""
+    if stream is None and _calls and _made(
+            _calls.kv_blocks(cfg, k_cache, v_cache, q, idx, first, lens, tables, scale, workspace, o, lse),
+            "dsa_kv_block_attention"):
+        return
     dtype, dev, T, H, stride, R, P = _step(cfg, q, first, lens, tables, workspace)
     _pool(cfg, "k_cache", k_cache, dtype, dev, cfg.page_size)
     _pool(cfg, "v_cache", v_cache, dtype, dev, cfg.page_size)
