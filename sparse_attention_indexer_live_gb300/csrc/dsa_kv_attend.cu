@@ -15,11 +15,12 @@
 //   * one warp issues tcgen05.mma: S = Q K^T (both in shared memory) and O += P V,
 //     P in tensor memory over the scores it came from;
 //   * two softmax warpgroups, a thread a row.
-// The two warpgroups have a stream of tiles each, so that the tensor cores have one's
-// product while the other's scores are weighed: with two row tiles in the unit, a
-// row tile each against the same keys (PAIR); with one, every other tile of its
-// positions, joined at the end.  A selection of pages is walked as the union of
-// the tile's tokens' lists, each row masked to its own.
+// Steps (a row tile against a tile of positions) go to two streams in turn, each with
+// a softmax warpgroup and tensor memory of its own, so that the tensor cores have
+// one's products while the other's scores are weighed: with two row tiles in the unit
+// a stream is a row tile (pair); with one it is every other tile of positions, and the
+// two are joined at the end.  A selection of pages is walked as the union of the
+// tile's tokens' lists, each row masked to its own.
 // Every mbarrier wait is bounded by a clock limit.
 
 #include <cuda.h>
@@ -32,10 +33,11 @@
 
 namespace {
 
-constexpr int kThreads = 384;  // warps 0-7 softmax, 8 TMA, 9 MMA, 10 scheduler, 11 tensor memory
+constexpr int kThreads = 384;  // warps 0-7 softmax, 8 TMA, 9 scheduler, 10 MMA
+constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
 // Registers (setmaxnreg): 168 a thread at launch; 256 x 200 + 128 x 104 = 384 x 168.
 constexpr int kLaunchRegs = 168, kSoftRegs = 200, kSideRegs = 104;
-static_assert(256 * kSoftRegs + 128 * kSideRegs <= kThreads * kLaunchRegs, "register split exceeds the launch's");
+static_assert(kSoft * kSoftRegs + 128 * kSideRegs <= kThreads * kLaunchRegs, "register split exceeds the launch's");
 constexpr int kTile = 128;
 constexpr int kHalf = 128 * 128;     // bytes of one half of the dims of a tile: 128 rows of 128
 constexpr int kTileBytes = 2 * kHalf;
@@ -44,11 +46,10 @@ constexpr int kOffKV = 2 * kTileBytes;  // after two Q tiles
 constexpr int kOffInfo = kOffKV + kStages * kTileBytes;
 struct Info {            // of one tile of positions
   int32_t page[8];       // sparse: its pages, by number in the request (-1: none)
-  uint32_t good[4];      // positions whose page is there
   int32_t j;             // dense: the tile's number
-  int32_t last;          // of the unit
-  int32_t spare[2];
+  int32_t flags;         // bits 0-7: its pages that are there; bit 8: the last of the unit
 };
+constexpr int kLast = 256;
 struct Desc {            // of one unit, or of a CTA's share of one
   int32_t stop, r, kvh, t0, ntok, pos0, pair, slot;  // slot: of the workspace, -1: a whole unit
   int32_t j0, j1;        // dense: tiles
@@ -59,7 +60,7 @@ constexpr int kOffDesc = kOffInfo + kInfos * (int)sizeof(Info);
 constexpr int kOffXch = kOffDesc + kDescs * (int)sizeof(Desc);  // [stream][row] maximum and sum
 constexpr int kOffScan = kOffXch;                               // (before the first unit) warps' sums
 constexpr int kOffBars = kOffXch + 2 * 128 * 8;
-constexpr int kNumBars = 2 + 2 * kStages + kInfos + 2 * kDescs + 6 + 3;
+constexpr int kNumBars = 4 + 2 * kStages + kInfos + 2 * kDescs + 6 + 3;
 constexpr int kOffWord = kOffBars + kNumBars * 8;  // tensor memory's address, abort flag
 constexpr int kSmem = kOffWord + 16;
 static_assert(kSmem <= 232448, "shared memory");
@@ -114,6 +115,15 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(su32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {  // without a pause
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(su32(b)), "r"(parity)
       : "memory");
@@ -214,15 +224,12 @@ __device__ __forceinline__ void tld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tst32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
 }
 __device__ __forceinline__ void tst16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -375,8 +382,11 @@ struct RowAgain {
     }
   }
 };
+struct Share {  // of a unit
+  int32_t r, kvh, j0, j1, from, to;
+};
 template <bool kBf16>
-__device__ __noinline__ bool odd_after(const Launch& L, const Desc& d, int pos) {
+__device__ __noinline__ bool odd_after(const Launch& L, const Share& d, int pos) {
   const KvParams& p = L.p;
   const int32_t* table = p.tables + (int64_t)d.r * p.P;
   const int64_t end = min((int64_t)d.j1 * kTile, (int64_t)p.P << p.shift);
@@ -398,7 +408,7 @@ __device__ __noinline__ bool odd_after(const Launch& L, const Desc& d, int pos) 
   return false;
 }
 template <bool kBf16, bool kSparse>
-__device__ __noinline__ float4 row_again(const Launch& L, const Desc& d, int t, int h, int pos, float m) {
+__device__ __noinline__ float4 row_again(const Launch& L, const Share& d, int t, int h, int pos, float m) {
   const KvParams& p = L.p;
   const char* q = static_cast<const char*>(p.q) + 2 * (t * p.q_stride + h * kKvDim);
   const int32_t* table = p.tables + (int64_t)d.r * p.P;
@@ -430,16 +440,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   Info* info = reinterpret_cast<Info*>(base + kOffInfo);
   Desc* desc = reinterpret_cast<Desc*>(base + kOffDesc);
   float2* xch = reinterpret_cast<float2*>(base + kOffXch);
-  uint64_t* qfull = reinterpret_cast<uint64_t*>(base + kOffBars);
-  uint64_t* qempty = qfull + 1;            // every S of the unit done
-  uint64_t* full = qempty + 1;             // [5] a key or value tile has landed
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(base + kOffBars);  // [2] a Q tile has landed
+  uint64_t* qempty = qfull + 2;            // [2] every S of it done
+  uint64_t* full = qempty + 2;             // [5] a key or value tile has landed
   uint64_t* empty = full + kStages;        // [5] its products are done
   uint64_t* tfull = empty + kStages;       // [8] a tile's Info is written
   uint64_t* dfull = tfull + kInfos;        // [2] a unit's Desc is written
   uint64_t* dempty = dfull + kDescs;       // [2] read by all warps
   uint64_t* sfull = dempty + kDescs;       // [2] scores of a stream
   uint64_t* pfull = sfull + 2;             // [2] weights written over them
-  uint64_t* pvdone = pfull + 2;            // [2] their product done
+  uint64_t* pvdone = pfull + 2;            // [2] a unit's last product of a stream done
   uint64_t* ofree = pvdone + 2;            // both outputs of a unit read
   uint64_t* xfull = ofree + 1;             // both streams' maxima and sums are there
   uint64_t* dbar = xfull + 1;              // products in flight when the CTA gives up
@@ -454,8 +464,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     *abort = 0;
     *start_req = -1;
-    bar_init(qfull, 1);
-    bar_init(qempty, 1);
     for (int i = 0; i < kStages; ++i) {
       bar_init(&full[i], 1);
       bar_init(&empty[i], 1);
@@ -463,19 +471,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     for (int i = 0; i < kInfos; ++i) bar_init(&tfull[i], 1);
     for (int i = 0; i < kDescs; ++i) {
       bar_init(&dfull[i], 1);
-      bar_init(&dempty[i], 10);
+      bar_init(&dempty[i], 2 + kSoftWarps);
     }
     for (int i = 0; i < 2; ++i) {
+      bar_init(&qfull[i], 1);
+      bar_init(&qempty[i], 1);
       bar_init(&sfull[i], 1);
       bar_init(&pfull[i], kPArrivals);
       bar_init(&pvdone[i], 1);
     }
-    bar_init(ofree, 256);
-    bar_init(xfull, 256);
+    bar_init(ofree, kSoft);
+    bar_init(xfull, kSoft);
     bar_init(dbar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 11) {
+  if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)),
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -513,13 +523,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   const int ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, all / kLeast));
   const bool has = (int)blockIdx.x < ctas && all > 0;
-  const int64_t x0 = has ? share_at(all, blockIdx.x, ctas) : 0, x1 = has ? share_at(all, blockIdx.x + 1, ctas) : 0;
-  if (has && x0 >= upto - mine && x0 < upto) {
+  // A selection's units cost the same: all but one to two a CTA are dealt out whole,
+  // one after another, so that those in work at a time are neighbours, whose pages
+  // the L2 holds; the rest is shared out.
+  const int64_t each = kSparse ? (int64_t)p.select * p.page + kUnitCost : 1;
+  const int waves = kSparse ? (int)max((int64_t)0, all / each / ctas - 1) : 0;
+  const int64_t dealt = waves * each * ctas;
+  const int64_t x0 = has ? dealt + share_at(all - dealt, blockIdx.x, ctas) : 0;
+  const int64_t x1 = has ? dealt + share_at(all - dealt, blockIdx.x + 1, ctas) : 0;
+  const int64_t begin = waves ? blockIdx.x * each : x0;
+  if (has && begin >= upto - mine && begin < upto) {
     int64_t at = upto - mine;
     for (int i = 0; i < per; ++i) {
       const int r = threadIdx.x * per + i;
       const int64_t w = r < p.R ? Units<kSparse>(L, r).head() * p.kv_heads : 0;
-      if (x0 < at + w) {
+      if (begin < at + w) {
         *start_req = r;
         *start_x = at;
         break;
@@ -534,9 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   const int64_t req0_x = *start_x;
   __syncthreads();  // the scheduler writes over them
 
-  if (warp >= 8) {
+  if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
-    if (warp == 10) {
+    if (warp == 9) {
       // ---- scheduler
       int d = 0;
       bool ok = true;
@@ -552,55 +570,79 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         return true;
       };
       int64_t x = req0_x;  // where request r begins
-      for (int r = req0; ok && has && r >= 0 && r < p.R && x < x1; ++r) {
-        const Units<kSparse> u(L, r);
-        const int64_t head = u.head();
-        if (head == 0) continue;
-        const int64_t rel = max((int64_t)0, x0 - x);
-        int g = (int)(rel / head);
-        int i = u.find(rel - g * head);
-        for (; ok && g < p.kv_heads && x + g * head < x1; ++g, i = 0) {
-          for (; ok && i < u.n; ++i) {
-            const int64_t at = x + g * head + u.before(i), end = at + u.cost(i);
-            if (at >= x1) break;
-            Desc e;
-            e.stop = 0;
-            e.r = r;
-            e.kvh = g;
-            e.t0 = u.q.a + i * u.tpu;
-            e.ntok = min(u.tpu, u.q.b - e.t0);
-            e.pos0 = u.q.pos0 < 0 ? -1 : u.q.pos0 + i * u.tpu;
-            e.pair = e.ntok > L.tpt;
-            const int n = u.tiles(L, i);
-            e.j0 = x0 > at ? cut_at(x0 - at, n) : 0;
-            e.j1 = x1 < end ? cut_at(x1 - at, n) : n;
-            e.from = 0;
-            e.to = kNever;
-            if (x0 >= at && x0 < end && lane == 0 && blockIdx.x > 0) {
-              Cut c;
-              c.r = r;
-              c.kvh = g;
-              c.t0 = e.t0;
-              c.ntok = e.ntok;
-              c.at = e.j0;
-              c.tiles = n;
-              c.pair = e.pair;
-              c.spare = 0;
-              reinterpret_cast<Cut*>(L.ws)[blockIdx.x] = c;
-            }
-            if (e.j0 >= e.j1) continue;
-            e.slot = e.j0 > 0 ? 2 * (int)blockIdx.x : e.j1 < n ? 2 * (int)blockIdx.x + 1 : -1;
-            if (kSparse) {
-              // shares are cut where the first token's list is
-              const int32_t* list = p.idx + ((int64_t)e.t0 * p.kv_heads + g) * p.select;
-              const int a = e.j0 << L.log_cpt, b = e.j1 << L.log_cpt;
-              if (e.j0 > 0) e.from = list[a] < 0 ? kNever : list[a];
-              if (e.j1 < n) e.to = list[b] < 0 ? kNever : list[b];
-            }
-            ok = publish(e);
+      int r = req0;
+      for (int w = 0; ok && has && r >= 0 && w <= waves; ++w) {
+        const int64_t from = w < waves ? ((int64_t)w * ctas + blockIdx.x) * each : x0;
+        const int64_t to = w < waves ? from + each : x1;
+        while (r < p.R && x < to) {
+          // the first of the next 32 requests that goes past `from`
+          const int64_t mine32 = r + lane < p.R ? Units<kSparse>(L, r + lane).head() * p.kv_heads : 0;
+          int64_t end32 = mine32;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, end32, o);
+            if (lane >= o) end32 += y;
           }
+          const uint32_t past = __ballot_sync(0xFFFFFFFFu, end32 > max((int64_t)0, from - x));
+          if (!past) {
+            x += __shfl_sync(0xFFFFFFFFu, end32, 31);
+            r += 32;
+            continue;
+          }
+          const int skip = __ffs(past) - 1;
+          x += __shfl_sync(0xFFFFFFFFu, end32 - mine32, skip);
+          r += skip;
+          if (x >= to) break;
+          const Units<kSparse> u(L, r);
+          const int64_t head = u.head();
+          const int64_t rel = max((int64_t)0, from - x);
+          int g = (int)(rel / head);
+          int i = u.find(rel - g * head);
+          for (; ok && g < p.kv_heads && x + g * head < to; ++g, i = 0) {
+            for (; ok && i < u.n; ++i) {
+              const int64_t at = x + g * head + u.before(i), end = at + u.cost(i);
+              if (at >= to) break;
+              Desc e;
+              e.stop = 0;
+              e.r = r;
+              e.kvh = g;
+              e.t0 = u.q.a + i * u.tpu;
+              e.ntok = min(u.tpu, u.q.b - e.t0);
+              e.pos0 = u.q.pos0 < 0 ? -1 : u.q.pos0 + i * u.tpu;
+              e.pair = e.ntok > L.tpt;
+              const int n = u.tiles(L, i);
+              e.j0 = from > at ? cut_at(from - at, n) : 0;
+              e.j1 = to < end ? cut_at(to - at, n) : n;
+              e.from = 0;
+              e.to = kNever;
+              if (w == waves && from >= at && from < end && lane == 0 && blockIdx.x > 0) {
+                Cut c;
+                c.r = r;
+                c.kvh = g;
+                c.t0 = e.t0;
+                c.ntok = e.ntok;
+                c.at = e.j0;
+                c.tiles = n;
+                c.pair = e.pair;
+                c.spare = 0;
+                reinterpret_cast<Cut*>(L.ws)[blockIdx.x] = c;
+              }
+              if (e.j0 >= e.j1) continue;
+              e.slot = e.j0 > 0 ? 2 * (int)blockIdx.x : e.j1 < n ? 2 * (int)blockIdx.x + 1 : -1;
+              if (kSparse) {
+                // shares are cut where the first token's list is
+                const int32_t* list = p.idx + ((int64_t)e.t0 * p.kv_heads + g) * p.select;
+                const int a = e.j0 << L.log_cpt, b = e.j1 << L.log_cpt;
+                if (e.j0 > 0) e.from = list[a] < 0 ? kNever : list[a];
+                if (e.j1 < n) e.to = list[b] < 0 ? kNever : list[b];
+              }
+              ok = publish(e);
+            }
+          }
+          if (!ok || w < waves || x + head * p.kv_heads >= to) break;  // (the next share may begin in this request)
+          x += head * p.kv_heads;
+          ++r;
         }
-        x += head * p.kv_heads;
       }
       if (ok) {
         Desc e;
@@ -613,7 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const int chunk = lane & (cpt - 1), half = lane >> L.log_cpt;
       const uint32_t box = sb + kOffKV + (half & 1) * kHalf + chunk * p.page * 128;
       const uint32_t nowhere = (uint32_t)p.pages << p.shift;  // past the cache: zeros
-      int tile = 0, units = 0;
+      int tile = 0, units = 0, singles = 0;
+      int quse[2] = {0, 0};  // loads of each Q tile
+      int asked = 0;         // key and value tiles asked for
       bool ok = true;
       auto load_pages = [&](int pg, int id, int j, int kvh, bool last) -> bool {
         // pg: lanes' page numbers (cpt lanes), id: their ids
@@ -621,12 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         const uint32_t have = __ballot_sync(0xFFFFFFFFu, good);
         Info& x = info[tile % kInfos];
         if (lane < 8) x.page[lane] = lane < cpt ? pg : -1;
-        if (lane < 4)
-          x.good[lane] = p.page == 16 ? (have >> (2 * lane) & 1 ? 0xFFFFu : 0u) | (have >> (2 * lane + 1) & 1 ? 0xFFFF0000u : 0u)
-                                      : (have >> ((32 * lane) >> p.shift) & 1 ? 0xFFFFFFFFu : 0u);
         if (lane == 0) {
           x.j = j;
-          x.last = last;
+          x.flags = (int)(have & ((1u << cpt) - 1u)) | (last ? kLast : 0);
         }
         __syncwarp();
         if (lane == 0) bar_arrive(&tfull[tile % kInfos]);
@@ -639,8 +680,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           if (lane == 0) bar_expect(&full[st], kTileBytes);
           __syncwarp();
           if (half < 2) tma_load(box + st * kTileBytes, kv ? &L.v : &L.k, &full[st], half * 64, kvh, z);
+          ++asked;
         }
         ++tile;
+        return true;
+      };
+      auto load_q = [&](int slot, int kvh, int t) -> bool {
+        if (quse[slot] > 0 && !wait_all(&qempty[slot], (quse[slot] & 1) ^ 1, abort)) return false;
+        ++quse[slot];
+        if (lane == 0) bar_expect(&qfull[slot], (uint32_t)(L.tpt * p.n * 256));
+        __syncwarp();
+        if (lane < 2) tma_load(sb + slot * kTileBytes + lane * kHalf, &L.q, &qfull[slot], lane * 64, kvh * p.n, t);
         return true;
       };
       for (; ok; ++units) {
@@ -650,20 +700,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) bar_arrive(&dempty[ds]);
         if (u.stop) break;
-        if (units > 0 && !wait_all(qempty, (units & 1) ^ 1, abort)) break;
-        if (lane == 0) {
-          const uint32_t bytes = (uint32_t)(L.tpt * p.n * 256);
-          bar_expect(qfull, u.pair ? 2 * bytes : bytes);
-          for (int i = 0; i < (u.pair ? 4 : 2); ++i)
-            tma_load(sb + i * kHalf, &L.q, qfull, (i & 1) * 64, u.kvh * p.n, u.t0 + (i >> 1) * L.tpt);
-        }
-        __syncwarp();
         const int32_t* table = p.tables + (int64_t)u.r * p.P;
         auto id_of = [&](int pg) { return pg >= 0 && pg < p.P ? table[pg] : -1; };
         if (!kSparse) {
           // ids 32 at a time, the next 32 on their way
           int at = u.j0 << L.log_cpt;
           int ids = id_of(at + lane), more = id_of(at + 32 + lane);
+          ok = u.pair ? load_q(0, u.kvh, u.t0) && load_q(1, u.kvh, u.t0 + L.tpt) : load_q(singles++ & 1, u.kvh, u.t0);
           int in = 0;
           for (int j = u.j0; ok && j < u.j1; ++j) {
             const int id = __shfl_sync(0xFFFFFFFFu, ids, in + chunk);
@@ -706,6 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             cur[i] = entry(i, e[i]);
             nxt[i] = cur[i] == kNever ? kNever : entry(i, e[i] + 1);
           }
+          ok = load_q(singles++ & 1, u.kvh, u.t0);
           auto least = [&]() {
             return __reduce_min_sync(0xFFFFFFFFu, min(min(cur[0], cur[1]), min(cur[2], cur[3])));
           };
@@ -739,81 +783,123 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
       }
       if (__any_sync(0xFFFFFFFFu, *abort)) {  // what is still on its way lands before the CTA ends
-        for (int n = max(0, 2 * tile - kStages); n < 2 * tile; ++n) drain(&full[n % kStages], (n / kStages) & 1);
-        if (units > 0) drain(qfull, (units - 1) & 1);
+        for (int n = max(0, asked - kStages); n < asked; ++n) drain(&full[n % kStages], (n / kStages) & 1);
+        for (int i = 0; i < 2; ++i)
+          if (quse[i] > 0) drain(&qfull[i], (quse[i] - 1) & 1);
       }
-    } else if (warp == 9) {
-      // ---- MMA.  Steps alternate between the streams; S of a step is issued two
-      // steps ahead of its P V, right behind the P V that read the weights it
-      // overwrites (products of one CTA run in the order they are issued).
+    } else if (warp == 10) {
+      // ---- MMA.  S is issued up to two steps ahead of P V; a stream's next S comes
+      // right behind the P V that reads the weights it overwrites (products of one
+      // CTA run in the order they are issued, so its end is that P V's end too).  The
+      // queue of issued products is short and a wait costs the warp some 150 cycles
+      // even when it is over: a pair's tile takes four, none of them twice.
       const uint64_t qdesc = sdesc(sb, 16), kdesc = sdesc(sb + kOffKV, 16), vdesc = sdesc(sb + kOffKV, kHalf);
-      int tile = 0;       // of the next S
-      int count[2] = {0, 0};  // products P V of each stream
+      int tile = 0, turn = 0, singles = 0;
+      int quse0 = 0, quse1 = 0;    // units of each Q tile
+      int count0 = 0, count1 = 0;  // steps of each stream
       bool ok = true;
-      int units = 0;
-      for (; ok; ++units) {
-        const int ds = units % kDescs;
-        if (!wait_all(&dfull[ds], (units / kDescs) & 1, abort)) break;
+      auto k_full = [&](int t) { return wait_all(&full[(2 * t) % kStages], ((2 * t) / kStages) & 1, abort); };
+      auto v_full = [&](int t) { return wait_all(&full[(2 * t + 1) % kStages], ((2 * t + 1) / kStages) & 1, abort); };
+      auto p_full = [&](int s) { return wait_all(&pfull[s], (s ? count1 : count0) & 1, abort); };
+      auto issue_s = [&](int s, int slot, int st, bool free_k, bool free_q) {
+        fence_after();
+        if (elect_one()) {
+          mma_qk<kBf16>(tmem + s * 128, qdesc + (uint32_t)((slot * kTileBytes) >> 4),
+                        kdesc + (uint32_t)((st * kTileBytes) >> 4));
+          mma_commit(&sfull[s]);
+          if (free_k) mma_commit(&empty[st]);
+          if (free_q) mma_commit(&qempty[slot]);
+        }
+        __syncwarp();
+      };
+      auto issue_pv = [&](int s, int st, bool add, bool free_v, int ended) {  // ended: streams that are at their end
+        fence_after();
+        if (elect_one()) {
+          mma_pv<kBf16>(tmem + kTmemO + s * 128, tmem + s * 128, vdesc + (uint32_t)((st * kTileBytes) >> 4), add);
+          if (free_v) mma_commit(&empty[st]);
+          if (ended & 1) mma_commit(&pvdone[0]);
+          if (ended & 2) mma_commit(&pvdone[1]);
+        }
+        __syncwarp();
+      };
+      for (int unit = 0; ok; ++unit) {
+        const int ds = unit % kDescs;
+        if (!(ok = wait_all(&dfull[ds], (unit / kDescs) & 1, abort))) break;
         const bool stop = desc[ds].stop, pair = desc[ds].pair;
         __syncwarp();
         if (lane == 0) bar_arrive(&dempty[ds]);
         if (stop) break;
-        if (!wait_all(qfull, units & 1, abort)) break;
-        bool more = true;
-        int stream = 0;
-        int used = 0;  // streams that have an output in this unit
-        struct Step {
-          int tile, stream;  // tile -1: none
-        };
-        auto next_s = [&](Step& s) -> bool {
-          s.tile = -1;
-          if (!more) return true;
-          if (!wait_all(&tfull[tile % kInfos], (tile / kInfos) & 1, abort)) return false;
-          const bool last = info[tile % kInfos].last;
-          const int n = 2 * tile, st = n % kStages;
-          if (!wait_all(&full[st], (n / kStages) & 1, abort)) return false;
-          fence_after();
-          const bool done = !pair || stream == 1;  // with the key tile
-          if (elect_one()) {
-            mma_qk<kBf16>(tmem + stream * 128, qdesc + (uint32_t)((pair ? stream * kTileBytes : 0) >> 4),
-                          kdesc + (uint32_t)((st * kTileBytes) >> 4));
-            mma_commit(&sfull[stream]);
-            if (done) mma_commit(&empty[st]);
-            if (done && last) mma_commit(qempty);
+        auto outputs_free = [&]() { return unit == 0 || wait_all(ofree, (unit & 1) ^ 1, abort); };
+        // (a tile's Info is written before its keys are asked for)
+        if (pair) {
+          ok = wait_all(&qfull[0], quse0++ & 1, abort) && wait_all(&qfull[1], quse1++ & 1, abort) && k_full(tile);
+          if (!ok) break;
+          bool last = info[tile % kInfos].flags & kLast;
+          issue_s(0, 0, (2 * tile) % kStages, false, last);
+          issue_s(1, 1, (2 * tile) % kStages, true, last);
+          if (!(ok = outputs_free())) break;
+          for (bool add = false;; add = true) {
+            const int sv = (2 * tile + 1) % kStages, sk = (2 * tile + 2) % kStages;
+            const bool end = last;
+            if (!(ok = (end || k_full(tile + 1)) && v_full(tile))) break;
+            if (!end) last = info[(tile + 1) % kInfos].flags & kLast;
+            if (!(ok = p_full(0))) break;
+            ++count0;
+            issue_pv(0, sv, add, false, end ? 1 : 0);
+            if (!end) issue_s(0, 0, sk, false, last);
+            if (!(ok = p_full(1))) break;
+            ++count1;
+            issue_pv(1, sv, add, true, end ? 2 : 0);
+            ++tile;
+            if (end) break;
+            issue_s(1, 1, sk, true, last);
           }
-          __syncwarp();
-          s.tile = tile;
-          s.stream = stream;
-          stream ^= 1;
-          if (done) {
+        } else {
+          const int slot = singles++ & 1;
+          if (!(ok = wait_all(&qfull[slot], (slot ? quse1 : quse0) & 1, abort))) break;
+          if (slot)
+            ++quse1;
+          else
+            ++quse0;
+          int ahead = tile, had = 0;  // the next S's tile; streams that have an output
+          bool more = true, last = false;
+          int s_turn = turn;          // its stream
+          auto next_s = [&]() {       // with its keys there
+            last = info[ahead % kInfos].flags & kLast;
+            issue_s(s_turn, slot, (2 * ahead) % kStages, true, last);
             more = !last;
+            s_turn ^= 1;
+            ++ahead;
+          };
+          if (!(ok = k_full(ahead))) break;
+          next_s();
+          const long long t0 = clock64();
+          while (ok && (more || tile < ahead)) {
+            if (more && ahead - tile < 2 &&
+                __all_sync(0xFFFFFFFFu, bar_test(&full[(2 * ahead) % kStages], ((2 * ahead) / kStages) & 1))) {
+              next_s();
+              continue;
+            }
+            if (tile == ahead) {  // no S in hand
+              ok = k_full(ahead);
+              continue;
+            }
+            // with one S ahead, whichever comes first: its weights, or the next S's keys
+            if (more && ahead - tile == 1 &&
+                !__all_sync(0xFFFFFFFFu, bar_test(&pfull[turn], (turn ? count1 : count0) & 1)) &&
+                !__any_sync(0xFFFFFFFFu, *abort || clock64() - t0 > kWaitCycles))
+              continue;
+            if (!(ok = v_full(tile) && (had || outputs_free()) && p_full(turn))) break;
+            const bool add = had >> turn & 1;
+            had |= 1 << turn;
+            issue_pv(turn, (2 * tile + 1) % kStages, add, true, !more && tile + 1 == ahead ? had : 0);
+            if (turn)
+              ++count1;
+            else
+              ++count0;
+            turn ^= 1;
             ++tile;
           }
-          return true;
-        };
-        auto pv = [&](const Step& s) -> bool {
-          const int n = 2 * s.tile + 1, st = n % kStages;
-          if (!wait_all(&full[st], (n / kStages) & 1, abort)) return false;
-          if (!wait_all(&pfull[s.stream], count[s.stream] & 1, abort)) return false;
-          if (!used && units > 0 && !wait_all(ofree, (units & 1) ^ 1, abort)) return false;
-          fence_after();
-          if (elect_one()) {
-            mma_pv<kBf16>(tmem + kTmemO + s.stream * 128, tmem + s.stream * 128,
-                          vdesc + (uint32_t)((st * kTileBytes) >> 4), used >> s.stream & 1);
-            mma_commit(&pvdone[s.stream]);
-            if (!pair || s.stream == 1) mma_commit(&empty[st]);
-          }
-          __syncwarp();
-          used |= 1 << s.stream;
-          ++count[s.stream];
-          return true;
-        };
-        Step a, b, c;
-        ok = next_s(a) && next_s(b);
-        while (ok && a.tile >= 0) {
-          ok = pv(a) && next_s(c);
-          a = b;
-          b = c;
         }
       }
       if (__any_sync(0xFFFFFFFFu, *abort)) {
@@ -832,21 +918,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_addr = lanes + me * 128, o_addr = lanes + kTmemO + me * 128;
     const float c2 = p.c2;
-    int tile = 0;
-    int count[2] = {0, 0};  // steps of each stream
-    int singles = 0;        // units of one row tile
+    int tile = 0, turn = 0;  // turn: the stream of the next tile of a single row tile
+    int count = 0;           // steps of this stream
+    int ends[2] = {0, 0};    // units in which each stream had a step
+    int singles = 0;         // units of one row tile
     for (int units = 0;; ++units) {
       const int ds = units % kDescs;
       if (!wait_all(&dfull[ds], (units / kDescs) & 1, abort)) break;
-      const Desc u = desc[ds];
+      const bool stop = desc[ds].stop, pair = desc[ds].pair;
+      const int t0 = desc[ds].t0, ntok = desc[ds].ntok, pos0 = desc[ds].pos0, slot = desc[ds].slot;
+      const int kvh = desc[ds].kvh, req = desc[ds].r, jend = desc[ds].j1, jbeg = desc[ds].j0;
+      const int from = desc[ds].from, to = desc[ds].to;
       __syncwarp();
       if (lane == 0) bar_arrive(&dempty[ds]);
-      if (u.stop) break;
-      const int mytok = tok + (u.pair && me ? L.tpt : 0);
-      const bool real = tok < L.tpt && mytok < u.ntok;
-      const int t = u.t0 + mytok;
+      if (stop) break;
+      const int mytok = tok + (pair && me ? L.tpt : 0);
+      const bool real = tok < L.tpt && mytok < ntok;
+      const int t = t0 + mytok;
       // a row of no token: nothing of it is masked, nor kept
-      const int pos = !real ? kNever : u.pos0 < 0 ? -1 : u.pos0 + mytok;
+      const int pos = !real ? kNever : pos0 < 0 ? -1 : pos0 + mytok;
       // sparse: where the row's list stands
       const int32_t* list = nullptr;
       int e = 0, want = kNever, next = kNever;
@@ -855,13 +945,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         return v < 0 ? kNever : v;
       };
       if (kSparse && real) {
-        list = p.idx + ((int64_t)t * p.kv_heads + u.kvh) * p.select;
-        if (u.from > 0) {
+        list = p.idx + ((int64_t)t * p.kv_heads + kvh) * p.select;
+        if (from > 0) {
           int hi = p.select;
           while (e < hi) {
             const int mid = (e + hi) / 2;
             const int v = list[mid];
-            if (v >= 0 && v < u.from)
+            if (v >= 0 && v < from)
               e = mid + 1;
             else
               hi = mid;
@@ -872,18 +962,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
       float m_used = -INFINITY, l = 0.f;
       bool ok = true, first = true;
-      int steps = 0;  // tiles of the unit
-      for (bool last = false; !last; ++tile, ++steps) {
+      int had = 0;  // streams that had a step
+      for (bool last = false; !last; ++tile) {
         if (!wait_all(&tfull[tile % kInfos], (tile / kInfos) & 1, abort)) {
           ok = false;
           break;
         }
         const Info& x = info[tile % kInfos];
-        last = x.last;
-        uint32_t words[4];
+        const int flags = x.flags;
+        last = flags & kLast;
+        uint32_t words[4] = {0u, 0u, 0u, 0u};  // the positions that the row attends to
         if (kSparse) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) words[w] = 0u;
           const int cpt = 1 << L.log_cpt;
           for (int c = 0; c < cpt; ++c) {
             const int pg = x.page[c];
@@ -893,34 +982,45 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               ++e;
               next = want == kNever ? kNever : entry(e + 1);
             }
+            if (!(flags >> c & 1)) continue;
             // positions of the page up to the row's own
             const int64_t room = (int64_t)pos - ((int64_t)pg << p.shift) + 1;
             const int bits = room < 0 ? 0 : room < p.page ? (int)room : p.page;
-            const int from = c * p.page;
+            const int a = c * p.page;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const int lo = max(from - 32 * w, 0), hi = min(from + bits - 32 * w, 32);
+              const int lo = max(a - 32 * w, 0), hi = min(a + bits - 32 * w, 32);
               if (lo < hi && lo < 32)
                 words[w] |= (hi == 32 ? 0xFFFFFFFFu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
             }
           }
         } else {
-          const int64_t room = (int64_t)pos - (int64_t)x.j * kTile + 1;
+          const int64_t far = (int64_t)pos - (int64_t)x.j * kTile + 1;
+          const int room = (int)min((int64_t)128, max((int64_t)0, far));
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const int64_t bits = room - 32 * w;
-            words[w] = bits <= 0 ? 0u : bits >= 32 ? 0xFFFFFFFFu : (1u << (int)bits) - 1u;
+            const int bits = room - 32 * w;
+            words[w] = bits <= 0 ? 0u : bits >= 32 ? 0xFFFFFFFFu : (1u << bits) - 1u;
+          }
+          const int all_there = (1 << (1 << L.log_cpt)) - 1;
+          if ((flags & all_there) != all_there) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+              for (int b = 0; b < 32; b += 16)
+                if (!(flags >> ((32 * w + b) >> p.shift) & 1)) words[w] &= ~(0xFFFFu << b);
           }
         }
-#pragma unroll
-        for (int w = 0; w < 4; ++w) words[w] &= x.good[w];
-        if (!u.pair && (steps & 1) != me) {
-          ++count[me ^ 1];
-          continue;
+        const bool whole = __all_sync(0xFFFFFFFFu, (words[0] & words[1] & words[2] & words[3]) == 0xFFFFFFFFu);
+        const int who = pair ? me : turn;  // whose step this tile is
+        if (pair) {
+          had = 3;
+        } else {
+          turn ^= 1;
+          had |= 1 << who;
+          if (who != me) continue;
         }
-        if (u.pair) ++count[me ^ 1];
-        const int k = count[me]++;
-        if (!wait_all(&sfull[me], k & 1, abort)) {
+        if (!wait_all(&sfull[me], count++ & 1, abort)) {
           ok = false;
           break;
         }
@@ -935,42 +1035,70 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll
             for (int j = 0; j < 32; ++j) sc[c][j] ^= 0x80000000u;
         }
+        if (!whole) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t mw = words[c];
-          if (__all_sync(0xFFFFFFFFu, mw == 0xFFFFFFFFu)) continue;
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t mw = words[c];
+            if (__all_sync(0xFFFFFFFFu, mw == 0xFFFFFFFFu)) continue;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (!(mw & (1u << j))) sc[c][j] = __float_as_uint(-INFINITY);
+            for (int j = 0; j < 32; ++j)
+              if (!(mw & (1u << j))) sc[c][j] = __float_as_uint(-INFINITY);
+          }
         }
-        // One pass against a base below the running maximum (dsa_cache.h): it moves
-        // only when a weight would pass 2^kMost; then the pass is redone and O rescaled.
+        // Weights against a base below the running maximum (dsa_cache.h), which moves
+        // only when a weight would pass 2^kMost; O is then rescaled (what was added to
+        // it came before this step's scores).
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mx[i] = fmax3(mx[i], __uint_as_float(sc[c][j + 2 * i]), __uint_as_float(sc[c][j + 2 * i + 1]));
+        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+        const bool move = m_used == -INFINITY ? m_new > -INFINITY : m_new - m_used > kMost;
+        float alpha = 1.f, mul = c2;
+        if (__any_sync(0xFFFFFFFFu, move || fabsf(m_used) > 65536.f)) {
+          if (move) {
+            const float up = m_new - kLift;
+            if (m_used > -INFINITY) alpha = ex2(m_used - up);
+            m_used = up;
+          }
+          if (!first && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t ov[16];
+              tld16(o_addr + 16 * c, ov);
+              tld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+              tst16(o_addr + 16 * c, ov);
+            }
+          }
+          // scores so large that the fused exponent is off by more than the maximum's
+          // rounding (2^-24 of it): their products are rounded as the maximum's was
+          if (__any_sync(0xFFFFFFFFu, fabsf(m_used) > 65536.f)) {
+            mul = 1.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sc[c][j] = __float_as_uint(__fmul_rn(__uint_as_float(sc[c][j]), c2));
+          }
+        }
         float lsum;
-        auto weights = [&](float m_eff, bool track) {
+        {
+          const float m_eff = m_used == -INFINITY ? 0.f : m_used;  // (all masked: zeros)
           uint64_t ls01 = pk2(0.f, 0.f), ls23 = pk2(0.f, 0.f);
-          const uint64_t cc = pk2(c2, c2), mm = pk2(-m_eff, -m_eff);
+          const uint64_t cc = pk2(mul, mul), mm = pk2(-m_eff, -m_eff);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const float s0 = __uint_as_float(sc[c][j]), s1 = __uint_as_float(sc[c][j + 1]);
-              const float s2 = __uint_as_float(sc[c][j + 2]), s3 = __uint_as_float(sc[c][j + 3]);
-              if (track) {
-                mx[(j >> 2) & 1] = fmax3(mx[(j >> 2) & 1], s0, s1);
-                mx[2 + ((j >> 2) & 1)] = fmax3(mx[2 + ((j >> 2) & 1)], s2, s3);
-              }
               float x0, x1, x2, x3;
-              if (track) {
-                upk2(ffma2(pk2(s0, s1), cc, mm), x0, x1);
-                upk2(ffma2(pk2(s2, s3), cc, mm), x2, x3);
-              } else {  // the products rounded as in the maximum: its weight is right at any magnitude
-                x0 = __fadd_rn(__fmul_rn(s0, c2), -m_eff);
-                x1 = __fadd_rn(__fmul_rn(s1, c2), -m_eff);
-                x2 = __fadd_rn(__fmul_rn(s2, c2), -m_eff);
-                x3 = __fadd_rn(__fmul_rn(s3, c2), -m_eff);
-              }
+              upk2(ffma2(pk2(__uint_as_float(sc[c][j]), __uint_as_float(sc[c][j + 1])), cc, mm), x0, x1);
+              upk2(ffma2(pk2(__uint_as_float(sc[c][j + 2]), __uint_as_float(sc[c][j + 3])), cc, mm), x2, x3);
               const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
               ls01 = fadd2(ls01, pk2(p0, p1));
               ls23 = fadd2(ls23, pk2(p2, p3));
@@ -983,79 +1111,48 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           upk2(ls01, l0, l1);
           upk2(ls23, l2, l3);
           lsum = (l0 + l1) + (l2 + l3);
-        };
-        weights(m_used == -INFINITY ? 0.f : m_used, true);
-        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
-        const bool redo = m_used == -INFINITY ? m_new > -INFINITY : m_new - m_used > kMost;
-        float alpha = 1.f;
-        // (and always for scores so large that the fused exponent is off: the
-        // product's rounding, 2^-24 of it, is not the maximum's)
-        if (__any_sync(0xFFFFFFFFu, redo || fabsf(m_used) > 65536.f)) {
-          if (redo) {
-            const float to = m_new - kLift;
-            if (m_used > -INFINITY) alpha = ex2(m_used - to);
-            m_used = to;
-          }
-          tst_wait();  // two stores to the same columns keep no order of their own
-          weights(m_used == -INFINITY ? 0.f : m_used, false);
-          if (!first && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
-            ok = wait_all(&pvdone[me], (k - 1) & 1, abort);
-            fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t ov[32];
-              tld32(o_addr + 32 * c, ov);
-              tld_wait();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
-              tst32(o_addr + 32 * c, ov);
-            }
-          }
         }
         first = false;
         l = l * alpha + lsum;
         tst_wait();
         fence_before();
         bar_arrive(&pfull[me]);
-        if (!ok) break;
       }
       if (!ok) break;
       // ---- the unit's end
-      if (u.pair) {
-        if (!wait_all(&pvdone[me], (count[me] - 1) & 1, abort)) break;
-      } else {
-        if (!wait_all(&pvdone[0], (count[0] - 1) & 1, abort)) break;
-        if (steps > 1 && !wait_all(&pvdone[1], (count[1] - 1) & 1, abort)) break;
-        xch[me * 128 + row] = make_float2(m_used, l);
+      if ((pair ? me == 0 : had & 1) && !wait_all(&pvdone[0], ends[0] & 1, abort)) break;
+      if ((pair ? me == 1 : had & 2) && !wait_all(&pvdone[1], ends[1] & 1, abort)) break;
+      ends[0] += had & 1;
+      ends[1] += had >> 1;
+      float m = m_used, sum = l, w0 = 1.f, w1 = 0.f;
+      if (!pair) {  // the two streams' shares of the row, in the same order by both
+        if (units > 0 && !wait_all(ofree, (units & 1) ^ 1, abort)) break;  // the unit before is done with xch
+        xch[me * 128 + row] = make_float2(m, l);
         bar_arrive(xfull);
         if (!wait_all(xfull, singles++ & 1, abort)) break;
-      }
-      fence_after();
-      float m = m_used, sum = l, w0 = 1.f, w1 = 0.f;
-      if (!u.pair) {  // the two streams' shares of the row, in the same order by both
         const float2 a = xch[row], b = xch[128 + row];
         m = fmaxf(a.x, b.x);
-        const float ref = m == -INFINITY ? 0.f : m;
-        w0 = ex2(a.x - ref);
-        w1 = ex2(b.x - ref);
-        if (a.y == 0.f) w0 = 0.f;
-        if (b.y == 0.f) w1 = 0.f;
+        const float top = m == -INFINITY ? 0.f : m;
+        w0 = a.y == 0.f ? 0.f : ex2(a.x - top);
+        w1 = b.y == 0.f ? 0.f : ex2(b.x - top);
         sum = a.y * w0 + b.y * w1;
       }
-      const float scale = u.slot >= 0 ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-      const int64_t out = (int64_t)t * p.H + u.kvh * p.n + head;
-      const int prow = row + (u.pair && me ? 128 : 0);
-      float* po = reinterpret_cast<float*>(L.ws + L.o_off) + ((int64_t)u.slot * L.rows + prow) * kKvDim;
+      fence_after();
+      const float scale = slot >= 0 ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+      const int64_t out = (int64_t)t * p.H + kvh * p.n + head;
+      const int prow = row + (pair && me ? 128 : 0);
+      float* po = reinterpret_cast<float*>(L.ws + L.o_off) + ((int64_t)slot * L.rows + prow) * kKvDim;
       bool odd = false;  // an element that is not finite
-      const int col0 = u.pair ? 0 : 64 * me, blocks = u.pair ? 4 : 2;
+      // with one row tile half of the dims each
+      const int col0 = pair ? 0 : 64 * me, cols = pair ? 128 : 64;
 #pragma unroll 1
-      for (int c = 0; c < blocks; ++c) {
-        const int col = col0 + 32 * c;
-        uint32_t ov[32], ow[32];
-        if (u.pair) {
-          tld32(o_addr + col, ov);
+      for (int col = col0; col < col0 + cols; col += 32) {
+        uint32_t ov[32];
+        if (pair) {
+          tld32(lanes + kTmemO + me * 128 + col, ov);
           tld_wait();
         } else {
+          uint32_t ow[32];
           tld32(lanes + kTmemO + col, ov);
           tld32(lanes + kTmemO + 128 + col, ow);
           tld_wait();
@@ -1077,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           ov[j] = __float_as_uint(x);
         }
         if (real) {
-          if (u.slot >= 0) {
+          if (slot >= 0) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
               *reinterpret_cast<uint4*>(po + col + j) = make_uint4(ov[j], ov[j + 1], ov[j + 2], ov[j + 3]);
@@ -1096,32 +1193,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
       fence_before();
       bar_arrive(ofree);
-      if (real && (u.pair || me == 0)) {
-        if (u.slot >= 0)
-          reinterpret_cast<float2*>(L.ws + L.ml_off)[(int64_t)u.slot * L.rows + prow] = make_float2(m, sum);
+      if (real && (pair || me == 0)) {
+        if (slot >= 0)
+          reinterpret_cast<float2*>(L.ws + L.ml_off)[(int64_t)slot * L.rows + prow] = make_float2(m, sum);
         else
           p.lse[out] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
       }
       __syncwarp();
       for (uint32_t again = __ballot_sync(0xFFFFFFFFu, real && odd && sum - sum == 0.f); again; again &= again - 1) {
-        const int from = __ffs(again) - 1;
-        const int rt = __shfl_sync(0xFFFFFFFFu, t, from), rh = __shfl_sync(0xFFFFFFFFu, head, from);
-        const int rp = __shfl_sync(0xFFFFFFFFu, pos, from), pr = __shfl_sync(0xFFFFFFFFu, prow, from);
-        const float rm = __shfl_sync(0xFFFFFFFFu, m, from), rs = __shfl_sync(0xFFFFFFFFu, scale, from);
-        if (!kSparse && !odd_after<kBf16>(L, u, rp)) continue;
-        const float4 o = row_again<kBf16, kSparse>(L, u, rt, u.kvh * p.n + rh, rp, rm);
-        if (!u.pair && lane >> 4 != me) continue;  // this half of the dims
-        if (u.slot >= 0)
-          reinterpret_cast<float4*>(L.ws + L.o_off)[((int64_t)u.slot * L.rows + pr) * 32 + lane] = o;
+        const int src = __ffs(again) - 1;
+        const int rt = __shfl_sync(0xFFFFFFFFu, t, src), rh = __shfl_sync(0xFFFFFFFFu, head, src);
+        const int rp = __shfl_sync(0xFFFFFFFFu, pos, src), pr = __shfl_sync(0xFFFFFFFFu, prow, src);
+        const float rm = __shfl_sync(0xFFFFFFFFu, m, src), rs = __shfl_sync(0xFFFFFFFFu, scale, src);
+        const Share d = {req, kvh, jbeg, jend, from, to};
+        if (!kSparse && !odd_after<kBf16>(L, d, rp)) continue;
+        const float4 o = row_again<kBf16, kSparse>(L, d, rt, kvh * p.n + rh, rp, rm);
+        if (4 * lane < col0 || 4 * lane >= col0 + cols) continue;  // this warp's dims
+        if (slot >= 0)
+          reinterpret_cast<float4*>(L.ws + L.o_off)[((int64_t)slot * L.rows + pr) * 32 + lane] = o;
         else
-          reinterpret_cast<uint2*>(p.o)[((int64_t)rt * p.H + u.kvh * p.n + rh) * 32 + lane] =
+          reinterpret_cast<uint2*>(p.o)[((int64_t)rt * p.H + kvh * p.n + rh) * 32 + lane] =
               make_uint2(pair_of<kBf16>(o.x * rs, o.y * rs), pair_of<kBf16>(o.z * rs, o.w * rs));
       }
     }
   }
   fence_before();
   __syncthreads();
-  if (warp == 11) {
+  if (warp == 9) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
   }
