@@ -321,29 +321,37 @@ __device__ __forceinline__ int cut_at(int64_t x, int n) {
   const int64_t j = max((int64_t)0, x - kUnitCost + kTile / 2) / kTile;
   return j < kSnap ? 0 : n - j < kSnap ? n : (int)j;
 }
-__device__ __forceinline__ int64_t share_at(int64_t all, int c, int ctas) {
-  return all / ctas * c + all % ctas * c / ctas;
+// a / b, 32 bits wide where they hold a (a 64-bit division takes a few hundred cycles)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
 
 // ---------------------------------------------------------------------------
 // one row on the CUDA cores
 
-// The output of one row (before the normaliser) by a warp: sum_j 2^(s_j - m) v_j
-// over its positions, four dims a lane.  0 times a NaN or an infinity of the values
-// is a NaN in the tensor cores' product, so a row whose output is not finite
-// although its sum is may owe that to a position that it does not attend to: such a
-// row is computed again from those that it does.  (Without a selection: if one of
-// the positions after its own, up to the end of the unit's tiles, is to blame.)
+// One row's share of a unit by a warp, four dims a lane: sum_j 2^(s_j - m) v_j over
+// its positions; m is given, or (a NaN) found on the way with the sum of the weights.
+// 0 times a NaN or an infinity is a NaN in the tensor cores' product and in a masked
+// exponent, so a row whose sum or output is not finite may owe that to a position
+// that it does not attend to: such a row is computed again from those that it does.
+// (Without a selection: if one of the positions after its own, up to the end of the
+// unit's tiles, is to blame.)
+struct Again {
+  float4 o;
+  float m, l;
+};
 template <bool kBf16>
 struct RowAgain {
-  float o[4];
-  __device__ void page(const KvParams& p, const char* q, int g, int id, int from, int to, float m) {
+  float o[4], m, l;
+  bool given;
+  __device__ void page(const KvParams& p, const char* q, int g, int id, int from, int to) {
     const int lane = threadIdx.x & 31;
     if (id < 0 || id >= p.pages) return;
 #pragma unroll 1
     for (int j0 = from; j0 < to; j0 += 32) {
       const int64_t at = ((int64_t)id * p.page + j0) * p.kv_heads + g;
-      float w = 0.f;
+      float s = -INFINITY;
       if (j0 + lane < to) {
         const char* k = static_cast<const char*>(p.k) + 2 * kKvDim * (at + (int64_t)lane * p.kv_heads);
         float d = 0.f;
@@ -358,8 +366,26 @@ struct RowAgain {
 #pragma unroll
           for (int e = 0; e < 8; ++e) d = fmaf(x[e], y[e], d);
         }
-        w = ex2((p.flip ? -d : d) * p.c2 - m);
+        s = (p.flip ? -d : d) * p.c2;
       }
+      float base = m;
+      if (!given) {
+        float top = s;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        const float next = fmaxf(m, top);
+        base = next == -INFINITY ? 0.f : next;
+        const float alpha = m == -INFINITY ? 0.f : ex2(m - base);
+        m = next;
+        l *= alpha;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= alpha;
+      }
+      const float w = ex2(s - base);
+      float sum = w;
+#pragma unroll
+      for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+      l += sum;
       const int n = min(32, to - j0);
 #pragma unroll 1
       for (int j = 0; j < n; j += 8) {
@@ -395,12 +421,12 @@ __device__ __noinline__ bool odd_after(const Launch& L, const Share& d, int pos)
     bool odd = false;
     const int id = x < end ? table[x >> p.shift] : -1;
     if (id >= 0 && id < p.pages) {
-      const char* v = static_cast<const char*>(p.v) +
-                      2 * kKvDim * ((((int64_t)id << p.shift) + (x & (p.page - 1))) * p.kv_heads + d.kvh);
+      const int64_t at = 2 * kKvDim * ((((int64_t)id << p.shift) + (x & (p.page - 1))) * p.kv_heads + d.kvh);
       for (int c = 0; c < kKvDim / 8; ++c) {
-        const Eight e = load8(v + 16 * c);
+        const Eight e = load8(static_cast<const char*>(p.k) + at + 16 * c), f = load8(static_cast<const char*>(p.v) + at + 16 * c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) odd |= (e.w[i] & top) == top || (e.w[i] >> 16 & top) == top;
+        for (int i = 0; i < 4; ++i)
+          odd |= (e.w[i] & top) == top || (e.w[i] >> 16 & top) == top || (f.w[i] & top) == top || (f.w[i] >> 16 & top) == top;
       }
     }
     if (__any_sync(0xFFFFFFFFu, odd)) return true;
@@ -408,25 +434,27 @@ __device__ __noinline__ bool odd_after(const Launch& L, const Share& d, int pos)
   return false;
 }
 template <bool kBf16, bool kSparse>
-__device__ __noinline__ float4 row_again(const Launch& L, const Share& d, int t, int h, int pos, float m) {
+__device__ __noinline__ Again row_again(const Launch& L, const Share& d, int t, int h, int pos, float m) {
   const KvParams& p = L.p;
   const char* q = static_cast<const char*>(p.q) + 2 * (t * p.q_stride + h * kKvDim);
   const int32_t* table = p.tables + (int64_t)d.r * p.P;
   RowAgain<kBf16> row;
-  row.o[0] = row.o[1] = row.o[2] = row.o[3] = 0.f;
+  row.o[0] = row.o[1] = row.o[2] = row.o[3] = row.l = 0.f;
+  row.given = m == m;
+  row.m = row.given ? m : -INFINITY;
   if (kSparse) {
     const int32_t* idx = p.idx + ((int64_t)t * p.kv_heads + d.kvh) * p.select;
     for (int i = 0; i < p.select && idx[i] >= 0; ++i) {
       const int j = idx[i];
       if (j >= d.from && j < d.to && j < p.P && j <= pos >> p.shift)
-        row.page(p, q, d.kvh, table[j], 0, min(p.page, pos - (j << p.shift) + 1), m);
+        row.page(p, q, d.kvh, table[j], 0, min(p.page, pos - (j << p.shift) + 1));
     }
   } else {
     const int64_t end = min((int64_t)d.j1 * kTile, min((int64_t)pos + 1, (int64_t)p.P << p.shift));
     for (int64_t x = (int64_t)d.j0 * kTile; x < end; x += p.page)
-      row.page(p, q, d.kvh, table[x >> p.shift], 0, (int)min((int64_t)p.page, end - x), m);
+      row.page(p, q, d.kvh, table[x >> p.shift], 0, (int)min((int64_t)p.page, end - x));
   }
-  return make_float4(row.o[0], row.o[1], row.o[2], row.o[3]);
+  return {make_float4(row.o[0], row.o[1], row.o[2], row.o[3]), row.m, row.l};
 }
 
 // ---------------------------------------------------------------------------
@@ -493,33 +521,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   if (warp == 8 && lane < 3)
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)(lane == 0 ? &L.q : lane == 1 ? &L.k : &L.v)) : "memory");
   // rows of Q tiles that no token fills stay zeros
-  for (int i = threadIdx.x; i < 2 * kTileBytes / 16; i += kThreads)
-    *reinterpret_cast<uint4*>(base + 16 * i) = make_uint4(0, 0, 0, 0);
-  fence_async_smem();
+  if (const int rest = (128 - L.tpt * p.n) * 8; rest) {  // 16-byte chunks of them, in each half of a tile
+    for (int i = threadIdx.x; i < 4 * rest; i += kThreads)
+      *reinterpret_cast<uint4*>(base + (i / rest + 1) * kHalf - 16 * (i % rest + 1)) = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+  }
   wait_for_previous();
 
-  // this CTA's share of all requests' work
-  const int per = (p.R + kThreads - 1) / kThreads;
-  int64_t mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int r = threadIdx.x * per + i;
-    if (r < p.R) mine += Units<kSparse>(L, r).head() * p.kv_heads;
-  }
-  int64_t upto = mine;
+  // All requests' work and where this CTA's share of it begins: by the scheduler
+  // alone for few requests, else by all threads.
+  constexpr int kFew = 128;
+  const bool few = p.R <= kFew;
+  const int per = few ? (p.R + 31) / 32 : (p.R + kThreads - 1) / kThreads;
+  const int first_r = (few ? lane : (int)threadIdx.x) * per;
+  int64_t mine = 0, upto = 0, all = 0;
+  if (!few || warp == 9) {
+    for (int i = 0; i < per; ++i)
+      if (first_r + i < p.R) mine += Units<kSparse>(L, first_r + i).head() * p.kv_heads;
+    upto = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-    if (lane >= o) upto += x;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    if (!few && lane == 31) warp_sum[warp] = upto;
   }
-  if (lane == 31) warp_sum[warp] = upto;
   fence_before();
   __syncthreads();
   fence_after();
-  int64_t all = 0;
+  const uint32_t tmem = *tmem_slot;
+  if (!few) {
+    all = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w == warp) upto += all;
-    all += warp_sum[w];
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w == warp) upto += all;
+      all += warp_sum[w];
+    }
   }
   const int ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, all / kLeast));
   const bool has = (int)blockIdx.x < ctas && all > 0;
@@ -527,30 +565,44 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   // one after another, so that those in work at a time are neighbours, whose pages
   // the L2 holds; the rest is shared out.
   const int64_t each = kSparse ? (int64_t)p.select * p.page + kUnitCost : 1;
-  const int waves = kSparse ? (int)max((int64_t)0, all / each / ctas - 1) : 0;
+  const int waves = kSparse ? (int)max((int64_t)0, quotient(quotient(all, each), ctas) - 1) : 0;
   const int64_t dealt = waves * each * ctas;
-  const int64_t x0 = has ? dealt + share_at(all - dealt, blockIdx.x, ctas) : 0;
-  const int64_t x1 = has ? dealt + share_at(all - dealt, blockIdx.x + 1, ctas) : 0;
+  const int64_t step = quotient(all - dealt + ctas - 1, ctas);
+  const int64_t x0 = has ? min(all, dealt + step * blockIdx.x) : 0;
+  const int64_t x1 = has ? min(all, dealt + step * (blockIdx.x + 1)) : 0;
   const int64_t begin = waves ? blockIdx.x * each : x0;
-  if (has && begin >= upto - mine && begin < upto) {
+  int req0 = -1;
+  int64_t req0_x = 0;
+  if (!few || warp == 9) {
+    const bool here = has && begin >= upto - mine && begin < upto;
     int64_t at = upto - mine;
-    for (int i = 0; i < per; ++i) {
-      const int r = threadIdx.x * per + i;
-      const int64_t w = r < p.R ? Units<kSparse>(L, r).head() * p.kv_heads : 0;
+    for (int i = 0; here && i < per; ++i) {
+      const int r = first_r + i;
+      const int64_t w = per == 1 ? mine : r < p.R ? Units<kSparse>(L, r).head() * p.kv_heads : 0;
       if (begin < at + w) {
-        *start_req = r;
-        *start_x = at;
+        req0 = r;
+        req0_x = at;
         break;
       }
       at += w;
     }
+    if (few) {
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, here);
+      const int src = who ? __ffs(who) - 1 : 0;
+      req0 = __shfl_sync(0xFFFFFFFFu, req0, src);
+      req0_x = __shfl_sync(0xFFFFFFFFu, req0_x, src);
+    } else if (here) {
+      *start_req = req0;
+      *start_x = req0_x;
+    }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<int32_t*>(L.ws + kMaxCtas * sizeof(Cut)) = has ? ctas : 0;
-  __syncthreads();
-  const uint32_t tmem = *tmem_slot;
-  const int req0 = *start_req;
-  const int64_t req0_x = *start_x;
-  __syncthreads();  // the scheduler writes over them
+  if (blockIdx.x == 0 && threadIdx.x == 9 * 32) *reinterpret_cast<int32_t*>(L.ws + kMaxCtas * sizeof(Cut)) = has ? ctas : 0;
+  if (!few) {
+    __syncthreads();
+    req0 = *start_req;
+    req0_x = *start_x;
+    __syncthreads();  // the scheduler writes over them
+  }
 
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
@@ -569,34 +621,42 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         ++d;
         return true;
       };
+      if (lane == 0 && has && blockIdx.x > 0 && x0 >= all) {  // nothing left for it
+        Cut c = {};
+        c.r = -1;
+        reinterpret_cast<Cut*>(L.ws)[blockIdx.x] = c;
+      }
       int64_t x = req0_x;  // where request r begins
       int r = req0;
       for (int w = 0; ok && has && r >= 0 && w <= waves; ++w) {
         const int64_t from = w < waves ? ((int64_t)w * ctas + blockIdx.x) * each : x0;
         const int64_t to = w < waves ? from + each : x1;
-        while (r < p.R && x < to) {
-          // the first of the next 32 requests that goes past `from`
-          const int64_t mine32 = r + lane < p.R ? Units<kSparse>(L, r + lane).head() * p.kv_heads : 0;
-          int64_t end32 = mine32;
+        for (bool known = w == 0; r < p.R && x < to; known = false) {
+          // (the share begins in a request that is known; else:) the first of the next
+          // 32 that goes past `from`
+          if (!known) {
+            const int64_t mine32 = r + lane < p.R ? Units<kSparse>(L, r + lane).head() * p.kv_heads : 0;
+            int64_t end32 = mine32;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, end32, o);
-            if (lane >= o) end32 += y;
+            for (int o = 1; o < 32; o <<= 1) {
+              const int64_t y = __shfl_up_sync(0xFFFFFFFFu, end32, o);
+              if (lane >= o) end32 += y;
+            }
+            const uint32_t past = __ballot_sync(0xFFFFFFFFu, end32 > max((int64_t)0, from - x));
+            if (!past) {
+              x += __shfl_sync(0xFFFFFFFFu, end32, 31);
+              r += 32;
+              continue;
+            }
+            const int skip = __ffs(past) - 1;
+            x += __shfl_sync(0xFFFFFFFFu, end32 - mine32, skip);
+            r += skip;
+            if (x >= to) break;
           }
-          const uint32_t past = __ballot_sync(0xFFFFFFFFu, end32 > max((int64_t)0, from - x));
-          if (!past) {
-            x += __shfl_sync(0xFFFFFFFFu, end32, 31);
-            r += 32;
-            continue;
-          }
-          const int skip = __ffs(past) - 1;
-          x += __shfl_sync(0xFFFFFFFFu, end32 - mine32, skip);
-          r += skip;
-          if (x >= to) break;
           const Units<kSparse> u(L, r);
           const int64_t head = u.head();
           const int64_t rel = max((int64_t)0, from - x);
-          int g = (int)(rel / head);
+          int g = (int)quotient(rel, head);
           int i = u.find(rel - g * head);
           for (; ok && g < p.kv_heads && x + g * head < to; ++g, i = 0) {
             for (; ok && i < u.n; ++i) {
@@ -937,6 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const int t = t0 + mytok;
       // a row of no token: nothing of it is masked, nor kept
       const int pos = !real ? kNever : pos0 < 0 ? -1 : pos0 + mytok;
+      const int own = pos < 0 ? -1 : pos >> p.shift, own_bits = (pos & (p.page - 1)) + 1;  // its page, positions in it
       // sparse: where the row's list stands
       const int32_t* list = nullptr;
       int e = 0, want = kNever, next = kNever;
@@ -984,8 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             }
             if (!(flags >> c & 1)) continue;
             // positions of the page up to the row's own
-            const int64_t room = (int64_t)pos - ((int64_t)pg << p.shift) + 1;
-            const int bits = room < 0 ? 0 : room < p.page ? (int)room : p.page;
+            const int bits = pg > own ? 0 : pg < own ? p.page : own_bits;
             const int a = c * p.page;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -1035,28 +1095,38 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll
             for (int j = 0; j < 32; ++j) sc[c][j] ^= 0x80000000u;
         }
+        // Sixteen positions at a time: where none of them is attended to their exponents
+        // get -inf for a base; where some are, they are told apart.  (A NaN among the
+        // first stays one: the row then has no finite sum and is computed again.)
+        auto group = [&](int i) { return words[i >> 1] >> (16 * (i & 1)) & 0xFFFFu; };
         if (!whole) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t mw = words[c];
-            if (__all_sync(0xFFFFFFFFu, mw == 0xFFFFFFFFu)) continue;
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t g = group(i);
+            if (__all_sync(0xFFFFFFFFu, g == 0u || g == 0xFFFFu)) continue;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(mw & (1u << j))) sc[c][j] = __float_as_uint(-INFINITY);
+            for (int j = 0; j < 16; ++j)
+              if (!(g >> j & 1u)) sc[i >> 1][16 * (i & 1) + j] = __float_as_uint(-INFINITY);
           }
         }
         // Weights against a base below the running maximum (dsa_cache.h), which moves
         // only when a weight would pass 2^kMost; O is then rescaled (what was added to
         // it came before this step's scores).
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float m_new = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int j = 0; j < 32; j += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mx[i] = fmax3(mx[i], __uint_as_float(sc[c][j + 2 * i]), __uint_as_float(sc[c][j + 2 * i + 1]));
-        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t* x = &sc[i >> 1][16 * (i & 1)];
+          float a = fmax3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+          float b = fmax3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+          a = fmax3(a, __uint_as_float(x[6]), __uint_as_float(x[7]));
+          b = fmax3(b, __uint_as_float(x[8]), __uint_as_float(x[9]));
+          a = fmax3(a, __uint_as_float(x[10]), __uint_as_float(x[11]));
+          b = fmax3(b, __uint_as_float(x[12]), __uint_as_float(x[13]));
+          a = fmax3(a, __uint_as_float(x[14]), __uint_as_float(x[15]));
+          if (!whole && group(i) == 0u) a = b = -INFINITY;
+          m_new = fmax3(m_new, a, b);
+        }
+        m_new *= c2;
         const bool move = m_used == -INFINITY ? m_new > -INFINITY : m_new - m_used > kMost;
         float alpha = 1.f, mul = c2;
         if (__any_sync(0xFFFFFFFFu, move || fabsf(m_used) > 65536.f)) {
@@ -1090,12 +1160,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         {
           const float m_eff = m_used == -INFINITY ? 0.f : m_used;  // (all masked: zeros)
           uint64_t ls01 = pk2(0.f, 0.f), ls23 = pk2(0.f, 0.f);
-          const uint64_t cc = pk2(mul, mul), mm = pk2(-m_eff, -m_eff);
+          const uint64_t cc = pk2(mul, mul);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
+              const float less = !whole && group(2 * c + j / 16) == 0u ? -INFINITY : -m_eff;
+              const uint64_t mm = pk2(less, less);
               float x0, x1, x2, x3;
               upk2(ffma2(pk2(__uint_as_float(sc[c][j]), __uint_as_float(sc[c][j + 1])), cc, mm), x0, x1);
               upk2(ffma2(pk2(__uint_as_float(sc[c][j + 2]), __uint_as_float(sc[c][j + 3])), cc, mm), x2, x3);
@@ -1200,20 +1272,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           p.lse[out] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
       }
       __syncwarp();
-      for (uint32_t again = __ballot_sync(0xFFFFFFFFu, real && odd && sum - sum == 0.f); again; again &= again - 1) {
+      for (uint32_t again = __ballot_sync(0xFFFFFFFFu, real && pos >= 0 && (odd || !(sum - sum == 0.f))); again;
+           again &= again - 1) {
         const int src = __ffs(again) - 1;
         const int rt = __shfl_sync(0xFFFFFFFFu, t, src), rh = __shfl_sync(0xFFFFFFFFu, head, src);
         const int rp = __shfl_sync(0xFFFFFFFFu, pos, src), pr = __shfl_sync(0xFFFFFFFFu, prow, src);
-        const float rm = __shfl_sync(0xFFFFFFFFu, m, src), rs = __shfl_sync(0xFFFFFFFFu, scale, src);
+        const float rm = __shfl_sync(0xFFFFFFFFu, m, src), rs = __shfl_sync(0xFFFFFFFFu, sum, src);
+        const bool whole_row = !(rs - rs == 0.f);  // its sum too
         const Share d = {req, kvh, jbeg, jend, from, to};
         if (!kSparse && !odd_after<kBf16>(L, d, rp)) continue;
-        const float4 o = row_again<kBf16, kSparse>(L, d, rt, kvh * p.n + rh, rp, rm);
+        const Again y = row_again<kBf16, kSparse>(L, d, rt, kvh * p.n + rh, rp, whole_row ? __int_as_float(0x7FFFFFFF) : rm);
+        const float rl = whole_row ? y.l : rs, top = whole_row ? y.m : rm;
+        const int64_t at = (int64_t)rt * p.H + kvh * p.n + rh;
+        if (whole_row && lane == 0 && (pair || me == 0)) {
+          if (slot >= 0)
+            reinterpret_cast<float2*>(L.ws + L.ml_off)[(int64_t)slot * L.rows + pr] = make_float2(top, rl);
+          else
+            p.lse[at] = rl == 0.f ? -INFINITY : (top + log2f(rl)) * 0.6931471805599453f;
+        }
         if (4 * lane < col0 || 4 * lane >= col0 + cols) continue;  // this warp's dims
+        const float inv = rl == 0.f ? 0.f : 1.f / rl;
         if (slot >= 0)
-          reinterpret_cast<float4*>(L.ws + L.o_off)[((int64_t)slot * L.rows + pr) * 32 + lane] = o;
+          reinterpret_cast<float4*>(L.ws + L.o_off)[((int64_t)slot * L.rows + pr) * 32 + lane] = y.o;
         else
-          reinterpret_cast<uint2*>(p.o)[((int64_t)rt * p.H + kvh * p.n + rh) * 32 + lane] =
-              make_uint2(pair_of<kBf16>(o.x * rs, o.y * rs), pair_of<kBf16>(o.z * rs, o.w * rs));
+          reinterpret_cast<uint2*>(p.o)[at * 32 + lane] =
+              make_uint2(pair_of<kBf16>(y.o.x * inv, y.o.y * inv), pair_of<kBf16>(y.o.z * inv, y.o.w * inv));
       }
     }
   }
@@ -1226,12 +1309,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 }
 
 // Joins the shares of cut units.  Block (c - 1, y) looks after the unit that CTA
-// c's share begins in, if no CTA's before c does; eight warps take every eighth
-// share, eight rows at a time.
+// c's share begins in, if no CTA's before c does.
 template <bool kBf16>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launch L) {
-  __shared__ float part[8][8][kKvDim];
-  __shared__ float part_l[8][8], top[8];
+  __shared__ __align__(16) float part[8][kKvDim];
+  __shared__ float part_l[8];
   __shared__ int16_t slots[kMaxCtas + 1];  // of the workspace, -1: an empty share
   __shared__ int s_last;
   let_next_start();
@@ -1249,7 +1331,6 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launc
   }
   const KvParams& p = L.p;
   const int rows = u.pair ? 128 + (u.ntok - L.tpt) * p.n : u.ntok * p.n;
-  if (8 * (int)blockIdx.y >= rows) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) s_last = c;
   __syncthreads();
@@ -1266,72 +1347,69 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launc
   __syncthreads();
   const float2* ml = reinterpret_cast<const float2*>(L.ws + L.ml_off);
   const float4* po = reinterpret_cast<const float4*>(L.ws + L.o_off);
-  for (int r0 = 8 * blockIdx.y; r0 < rows; r0 += 8 * gridDim.y) {
-    {  // warp i: the largest maximum of row i
-      float m = -INFINITY;
-      for (int x = lane; x < n; x += 32)
-        if (slots[x] >= 0 && r0 + warp < rows) m = fmaxf(m, ml[(int64_t)slots[x] * L.rows + r0 + warp].x);
+  // the output of row r from its sum and weighted outputs, by a warp
+  auto finish = [&](int r, float m, float sum, const float4& o) {
+    const int in = r & 127, tok = in / p.n;
+    if (r >= rows || tok >= L.tpt) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t out = (int64_t)(u.t0 + tok + (r >= 128 ? L.tpt : 0)) * p.H + u.kvh * p.n + in % p.n;
+    reinterpret_cast<uint2*>(p.o)[out * 32 + lane] =
+        make_uint2(pair_of<kBf16>(o.x * inv, o.y * inv), pair_of<kBf16>(o.z * inv, o.w * inv));
+    if (lane == 0) p.lse[out] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+  };
+  // As many warps a row as there are four shares for, 1 to 8, each every `split`-th.
+  int split = 1;
+  while (split < 8 && n > 4 * split) split *= 2;
+  const int rows_at = 8 / split, part_of = warp % split, mine = warp / split;
+  for (int r0 = rows_at * (int)blockIdx.y; r0 < rows; r0 += rows_at * gridDim.y) {
+    const int r = min(r0 + mine, rows - 1);
+    float m = -INFINITY;
+    for (int x = lane; x < n; x += 32)
+      if (slots[x] >= 0) m = fmaxf(m, ml[(int64_t)slots[x] * L.rows + r].x);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      if (lane == 0) top[warp] = m == -INFINITY ? 0.f : m;
-    }
-    __syncthreads();
-    float4 acc[8];
-    float l[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      l[i] = 0.f;
-    }
-    for (int x = warp; x < n; x += 8) {
-      const int slot = slots[x];
-      if (slot < 0) continue;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if (m == -INFINITY) m = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int x0 = part_of; x0 < n; x0 += 8 * split) {
       float2 y[8];
       float4 o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int64_t at = (int64_t)slot * L.rows + min(r0 + i, rows - 1);
-        y[i] = ml[at];
+        const int x = x0 + i * split, slot = x < n ? slots[x] : -1;
+        const int64_t at = (int64_t)max(slot, 0) * L.rows + r;
+        y[i] = ml[at];  // (of an empty share another's, which is not looked at)
         o[i] = po[at * 32 + lane];
+        if (slot < 0) y[i].y = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (y[i].y == 0.f) continue;  // nothing attended to
-        const float a = ex2(y[i].x - top[i]);
-        l[i] += a * y[i].y;
-        acc[i].x += a * o[i].x;
-        acc[i].y += a * o[i].y;
-        acc[i].z += a * o[i].z;
-        acc[i].w += a * o[i].w;
+        const float a = ex2(y[i].x - m);
+        l += a * y[i].y;
+        acc.x += a * o[i].x;
+        acc.y += a * o[i].y;
+        acc.z += a * o[i].z;
+        acc.w += a * o[i].w;
       }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      *reinterpret_cast<float4*>(&part[warp][i][4 * lane]) = acc[i];
-      if (lane == 0) part_l[warp][i] = l[i];
+    if (split == 1) {
+      finish(r0 + mine, m, l, acc);
+      continue;
     }
+    *reinterpret_cast<float4*>(&part[warp][4 * lane]) = acc;
+    if (lane == 0) part_l[warp] = l;
     __syncthreads();
-    // warp i finishes row i
-    const int r = r0 + warp;
-    const int in = r & 127;
-    const int tok = in / p.n + (r >= 128 ? L.tpt : 0), head = in % p.n;
-    if (r < rows && in / p.n < L.tpt) {
-      float sum = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        sum += part_l[w][warp];
-        const float4 x = *reinterpret_cast<const float4*>(&part[w][warp][4 * lane]);
-        o.x += x.x;
-        o.y += x.y;
-        o.z += x.z;
-        o.w += x.w;
+    if (part_of == 0) {
+      for (int w = 1; w < split; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(&part[warp + w][4 * lane]);
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+        l += part_l[warp + w];
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const int64_t out = (int64_t)(u.t0 + tok) * p.H + u.kvh * p.n + head;
-      reinterpret_cast<uint2*>(p.o)[out * 32 + lane] =
-          make_uint2(pair_of<kBf16>(o.x * inv, o.y * inv), pair_of<kBf16>(o.z * inv, o.w * inv));
-      if (lane == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top[warp] + log2f(sum)) * 0.6931471805599453f;
+      finish(r0 + mine, m, l, acc);
     }
     __syncthreads();
   }
@@ -1420,7 +1498,7 @@ int launch(const Launch& L, const Sizes& sz, cudaStream_t stream) {
   const int rc = launch_dependent(attend_kernel<kBf16, kSparse>, sz.ctas, kThreads, kSmem, 0, stream, L);
   if (rc != DSA_OK || sz.ctas == 1) return rc;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)(sz.ctas - 1), (unsigned)std::min(4, (sz.rows + 7) / 8));
+  lc.gridDim = dim3((unsigned)(sz.ctas - 1), (unsigned)std::min(8, sz.rows));
   lc.blockDim = dim3(256);
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
