@@ -1071,7 +1071,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                 if (!(flags >> ((32 * w + b) >> p.shift) & 1)) words[w] &= ~(0xFFFFu << b);
           }
         }
+        // Sixteen positions at a time: where none of them is attended to their exponents
+        // get -inf for a base; where some are, they are told apart.  (A NaN among the
+        // first stays one: the row then has no finite sum and is computed again.)
+        auto group = [&](int i) { return words[i >> 1] >> (16 * (i & 1)) & 0xFFFFu; };
         const bool whole = __all_sync(0xFFFFFFFFu, (words[0] & words[1] & words[2] & words[3]) == 0xFFFFFFFFu);
+        uint32_t none = 0, some = 0;  // groups without a position of the row's; with some, of any row of the warp
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t g = group(i);
+            none |= (uint32_t)(g == 0u) << i;
+            some |= (uint32_t)(g != 0u && g != 0xFFFFu) << i;
+          }
+          some = __reduce_or_sync(0xFFFFFFFFu, some);
+        }
         const int who = pair ? me : turn;  // whose step this tile is
         if (pair) {
           had = 3;
@@ -1095,15 +1109,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll
             for (int j = 0; j < 32; ++j) sc[c][j] ^= 0x80000000u;
         }
-        // Sixteen positions at a time: where none of them is attended to their exponents
-        // get -inf for a base; where some are, they are told apart.  (A NaN among the
-        // first stays one: the row then has no finite sum and is computed again.)
-        auto group = [&](int i) { return words[i >> 1] >> (16 * (i & 1)) & 0xFFFFu; };
-        if (!whole) {
+        if (some) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
+            if (!(some >> i & 1u)) continue;
             const uint32_t g = group(i);
-            if (__all_sync(0xFFFFFFFFu, g == 0u || g == 0xFFFFu)) continue;
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               if (!(g >> j & 1u)) sc[i >> 1][16 * (i & 1) + j] = __float_as_uint(-INFINITY);
@@ -1123,7 +1133,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           a = fmax3(a, __uint_as_float(x[10]), __uint_as_float(x[11]));
           b = fmax3(b, __uint_as_float(x[12]), __uint_as_float(x[13]));
           a = fmax3(a, __uint_as_float(x[14]), __uint_as_float(x[15]));
-          if (!whole && group(i) == 0u) a = b = -INFINITY;
+          if (none >> i & 1u) a = b = -INFINITY;
           m_new = fmax3(m_new, a, b);
         }
         m_new *= c2;
@@ -1166,7 +1176,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const float less = !whole && group(2 * c + j / 16) == 0u ? -INFINITY : -m_eff;
+              const float less = none >> (2 * c + j / 16) & 1u ? -INFINITY : -m_eff;
               const uint64_t mm = pk2(less, less);
               float x0, x1, x2, x3;
               upk2(ffma2(pk2(__uint_as_float(sc[c][j]), __uint_as_float(sc[c][j + 1])), cc, mm), x0, x1);
