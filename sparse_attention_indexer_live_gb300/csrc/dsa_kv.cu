@@ -225,8 +225,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 // select
 
 constexpr int kScoreTokens = 64, kScorePages = 128, kScoreThreads = 256;
-constexpr int kPitch = 2 * 2 * kKvDim + 16;  // bytes of a row of both halves in shared memory
-constexpr int kPickThreads = 256, kPickList = 512;
+constexpr int kPitch = 2 * 2 * kKvDim + 16;             // bytes of a row of both halves in shared memory
+constexpr int kMeanTile = kScorePages * 2 * kKvDim;     // bytes of a tile of mean keys
+constexpr int kScoreSmem = kScoreTokens * kPitch + 2 * kMeanTile;
+constexpr int kPickThreads = 256;
 constexpr int64_t kScoreBytes = 64 << 20;  // scores of the tokens in work: they stay in L2
 
 struct SelectParams {
@@ -235,7 +237,7 @@ struct SelectParams {
   int32_t* idx;
   float* scores;     // [tokens in work, kv_heads, width]
   float* row_norm;   // [tokens in work, kv_heads]
-  float* tile_norm;  // [slots, kv_heads, tiles, 2]
+  float* tile_norm;  // [slots, kv_heads, tiles]
   int64_t q_stride;
   int32_t T, H, n, kv_heads, R, P, pages, page, shift, select, lead, trail;
   int32_t width, tiles;  // of a row of scores
@@ -272,8 +274,11 @@ __device__ __forceinline__ int own_page(int pos, int shift, int P) { return pos 
 // whole batch), slot R + j those of the request that goes on into block j.
 template <bool kBf16>
 __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams p) {
-  __shared__ __align__(16) uint8_t sums[kScoreTokens * kPitch];
-  __shared__ int piece[3];
+  extern __shared__ __align__(16) uint8_t sums[];  // the heads' sums | two tiles of means
+  __shared__ int piece[3], top_norm[2];
+  __shared__ uint32_t there[2][kScoreThreads / 32];
+  const uint8_t* means = sums + kScoreTokens * kPitch;
+  const uint32_t means_at = (uint32_t)__cvta_generic_to_shared(means);
   let_next_start();
   wait_for_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -366,12 +371,35 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
     }
   }
   __syncthreads();
-  // a warp: 16 tokens (warp & 3) by 64 pages (warp >> 2) of a tile.  Fragments'
-  // dims are taken in the order that makes a lane's pages' loads 16 bytes: dims
-  // 8 (c + 4 i) + 4 s .. + 3 for lane c of a row, step 2 i + s.
+  // Tiles of 128 means come through two stages of shared memory, half a row a
+  // thread, and a row's 64-byte quarters trade places by its parity so that the eight
+  // lanes of a phase below read different banks.
+  const int32_t* table = p.tables + (int64_t)r * p.P;
+  const int prow = threadIdx.x >> 1, phalf = threadIdx.x & 1;
+  auto id_at = [&](int tile) {
+    const int j = tile * kScorePages + prow;
+    return j < end ? table[j] : -1;
+  };
+  auto copy = [&](int stage, int id) {
+    const bool ok = id >= 0 && id < p.pages;
+    const char* src = static_cast<const char*>(p.means) + 2 * (((int64_t)(ok ? id : 0) * p.kv_heads + head) * kKvDim) + 128 * phalf;
+    const uint32_t dst = means_at + stage * kMeanTile + prow * 256;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (((8 * phalf + i) ^ ((prow & 1) << 2)) << 4)),
+                   "l"(ok ? src + 16 * i : static_cast<const char*>(p.q)), "r"(ok ? 16 : 0)
+                   : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const uint32_t have = __ballot_sync(0xFFFFFFFFu, ok);  // two lanes a page
+    if (lane == 0) there[stage][warp] = have;
+  };
+  // The warps: 1, 2 or 4 groups of 16 tokens, and as many groups of a tile's pages as
+  // that leaves.  Fragments' dims are taken in the order that makes a lane's loads 16
+  // bytes: dims 8 (c + 4 i) + 4 s .. + 3 for lane c of a row, step 2 i + s.
   const int gq = lane >> 2, c = lane & 3;
-  const int wm = warp & 3, wn = warp >> 2;
-  if (a + 16 * wm >= b) return;
+  const int groups = b - a > 32 ? 4 : b - a > 16 ? 2 : 1;
+  const int wm = warp % groups, wn = warp / groups;
+  const int pages_each = kScorePages * groups / 8;
   uint32_t fa[2][8][4];
 #pragma unroll
   for (int half = 0; half < 2; ++half)
@@ -385,36 +413,39 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
       fa[half][st][2] = x.y;
       fa[half][st][3] = y.y;
     }
-  const int32_t* table = p.tables + (int64_t)r * p.P;
-  const bool norms = wm == 0;
   const int ta = a + 16 * wm + gq, tb = ta + 8;
   float* rowa = p.scores + ((int64_t)(ta - p.t0) * p.kv_heads + head) * p.width;
   float* rowb = p.scores + ((int64_t)(tb - p.t0) * p.kv_heads + head) * p.width;
-  for (int tile = split; tile < tiles; tile += p.splits) {
+  copy(0, id_at(split));
+  int next = split + p.splits;
+  int id = id_at(next);
+  for (int tile = split, stage = 0; tile < tiles; tile = next, stage ^= 1) {
+    next = tile + p.splits;
+    if (next < tiles) copy(stage ^ 1, id);
+    id = id_at(next + p.splits);
+    if (threadIdx.x == 0) top_norm[stage] = 0;
+    if (next < tiles)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
     float top = 0.f;
-    const int j0 = tile * kScorePages + 64 * wn;
-#pragma unroll 2
-    for (int u = 0; u < 8; ++u) {
-      const int j = j0 + 8 * u + gq;
-      if (j0 + 8 * u >= end) break;
-      const int id = j < end ? table[j] : -1;
-      const bool ok = id >= 0 && id < p.pages;
+#pragma unroll 1
+    for (int u = 0; u < pages_each / 8; ++u) {
+      const int j8 = wn * pages_each + 8 * u;  // in the tile
+      if (tile * kScorePages + j8 >= end) break;
+      const int row = j8 + gq;
       Eight e[4];
-      if (ok) {
-        const char* src = static_cast<const char*>(p.means) + 2 * (((int64_t)id * p.kv_heads + head) * kKvDim + 8 * c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = load8(src + 64 * i);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = Eight{{0u, 0u, 0u, 0u}};
-      }
+      for (int i = 0; i < 4; ++i)
+        e[i] = load8(means + stage * kMeanTile + row * 256 + (((c + 4 * i) ^ ((row & 1) << 2)) << 4));
       float d[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int st = 0; st < 8; ++st) {
         mma16816<kBf16>(d, fa[0][st], e[st >> 1].w[2 * (st & 1)], e[st >> 1].w[2 * (st & 1) + 1]);
         mma16816<kBf16>(d1, fa[1][st], e[st >> 1].w[2 * (st & 1)], e[st >> 1].w[2 * (st & 1) + 1]);
       }
-      if (norms) {
+      if ((u & (groups - 1)) == wm) {  // the norms: the token groups take turns
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -428,10 +459,10 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
         top = fmaxf(top, s);
       }
       // columns 2 c and 2 c + 1; a page without an id scores a NaN
-      const uint32_t have = __ballot_sync(0xFFFFFFFFu, ok);
+      const uint32_t have = there[stage][j8 >> 4] >> (2 * (j8 & 15));
       const float nan = __int_as_float(0x7FFFFFFF);
-      const bool h0 = have >> (8 * c) & 1u, h1 = have >> (8 * c + 4) & 1u;
-      const int col = j0 + 8 * u + 2 * c;
+      const bool h0 = have >> (4 * c) & 1u, h1 = have >> (4 * c + 2) & 1u;
+      const int col = tile * kScorePages + j8 + 2 * c;
       if (col < p.width) {
         if (ta < b)
           *reinterpret_cast<float2*>(rowa + col) = make_float2(h0 ? d[0] + d1[0] : nan, h1 ? d[1] + d1[1] : nan);
@@ -439,11 +470,12 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
           *reinterpret_cast<float2*>(rowb + col) = make_float2(h0 ? d[2] + d1[2] : nan, h1 ? d[3] + d1[3] : nan);
       }
     }
-    if (norms) {
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      if (lane == 0) p.tile_norm[(((int64_t)blockIdx.x * p.kv_heads + head) * p.tiles + tile) * 2 + wn] = sqrtf(top);
-    }
+    for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (lane == 0) atomicMax(&top_norm[stage], __float_as_int(top));  // (not negative)
+    __syncthreads();
+    if (threadIdx.x == 0)
+      p.tile_norm[((int64_t)blockIdx.x * p.kv_heads + head) * p.tiles + tile] = sqrtf(__int_as_float(top_norm[stage]));
   }
 }
 
@@ -454,36 +486,52 @@ __device__ __forceinline__ int64_t rank_key(double x) {
   return b < 0 ? (b ^ 0x7FFFFFFFFFFFFFFFll) : b;
 }
 
-// The best pages of one token and key/value head.  Scores are known to within e:
-// of each thread's largest lower bound the m-th largest is a floor of the m-th
-// best, whatever reaches it goes on a short list, and of that list those that e
+// The best pages of one token and key/value head, by W warps.  Scores are known to
+// within e: the m-th best is not below the m-th largest of 256 groups' largest lower
+// bounds, whatever may reach that goes on a short list, and of that list those that e
 // leaves open are scored again in fp64.  A list that does not fit (many equal
-// scores) is taken 256 pages at a time, all in fp64, against the best so far.
-template <bool kBf16>
+// scores) is taken a part at a time, all in fp64, against the best so far.
+template <int W>
+struct Pick {
+  static constexpr int kList = W == 1 ? 128 : 512;
+  static constexpr int kMost = W == 1 ? 48 : kPickThreads;  // m
+  double qs[kKvDim];
+  int64_t key[kList];
+  float score[kList];
+  int page[kList];
+  float group[W == 1 ? 1 : kPickThreads];
+  float norm[W];
+  uint16_t open_list[kList];
+  uint8_t state[kList];  // 0 out, 1 in, 2 open
+  int count, open, sure;
+};
+
+// The order of floats as unsigned numbers; no NaN.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float float_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+template <bool kBf16, int W>
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectParams p) {
-  __shared__ int s_req, s_count, s_open, s_sure;
-  __shared__ float s_floor, s_norm[kPickThreads / 32];
-  __shared__ float best[kPickThreads];
-  __shared__ int page_of[kPickList];
-  __shared__ float low[kPickList], high[kPickList];
-  __shared__ uint8_t state[kPickList];  // 0 out, 1 in, 2 open
-  __shared__ int open_list[kPickList];
-  __shared__ int64_t key[kPickList];
-  __shared__ double qs[kKvDim];
-  __shared__ int chosen[kPickThreads];
+  constexpr int kT = 32 * W;  // threads a row
+  __shared__ Pick<W> rows[kPickThreads / kT];
   let_next_start();
   wait_for_previous();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t = p.t0 + (int)blockIdx.x / p.kv_heads, head = (int)blockIdx.x % p.kv_heads;
-  if (warp == 0) {
-    const int r = request_of_token(p.first, p.R, t);
-    if (lane == 0) {
-      s_req = r;
-      s_count = s_open = s_sure = 0;
-    }
-  }
-  __syncthreads();
-  const int r = s_req;
+  const int tid = threadIdx.x % kT, warp = tid >> 5, lane = tid & 31;
+  Pick<W>& x = rows[threadIdx.x / kT];
+  auto sync = [&]() {
+    if (W == 1)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+  const int64_t row_id = (int64_t)blockIdx.x * (kPickThreads / kT) + threadIdx.x / kT;
+  const int t = (int)min((int64_t)p.t1, p.t0 + row_id / p.kv_heads), head = (int)(row_id % p.kv_heads);
+  const int r = t < p.t1 ? request_of_token(p.first, p.R, t) : -1;
   if (r < 0) return;
   const Request rq = request_of(p.first, p.lens, r, p.T);
   if (t < rq.a || t >= rq.b) return;
@@ -491,170 +539,223 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectParams p
   int32_t* out = p.idx + ((int64_t)t * p.kv_heads + head) * p.select;
   const int n = own + 1;
   if (n <= p.select) {
-    for (int i = tid; i < p.select; i += kPickThreads) out[i] = i < n ? i : -1;
+    for (int i = tid; i < p.select; i += kT) out[i] = i < n ? i : -1;
     return;
   }
   // free pages [lead, end), of which m are taken; n > select, so there are more than m
   const int end = n - p.trail, m = p.select - p.lead - p.trail;
-  for (int i = tid; i < p.lead; i += kPickThreads) out[i] = i;
-  for (int i = tid; i < p.trail; i += kPickThreads) out[p.select - p.trail + i] = end + i;
+  for (int i = tid; i < p.lead; i += kT) out[i] = i;
+  for (int i = tid; i < p.trail; i += kT) out[p.select - p.trail + i] = end + i;
   if (m <= 0) return;
-  const float* row = p.scores + ((int64_t)(t - p.t0) * p.kv_heads + head) * p.width;
+  const float* scores = p.scores + ((int64_t)(t - p.t0) * p.kv_heads + head) * p.width;
   const int32_t* table = p.tables + (int64_t)r * p.P;
-  float norm = 0.f;
-  const int norms = 2 * ((end + kScorePages - 1) / kScorePages);
+  if (tid == 0) x.count = x.open = x.sure = 0;
   const int slot = t / kScoreTokens == rq.a / kScoreTokens ? r : p.R + (t - p.t0) / kScoreTokens;
-  for (int i = tid; i < norms; i += kPickThreads)
-    if ((i >> 1) * kScorePages + 64 * (i & 1) < end)
-      norm = fmaxf(norm, p.tile_norm[((int64_t)slot * p.kv_heads + head) * p.tiles * 2 + i]);
+  const float* norms = p.tile_norm + ((int64_t)slot * p.kv_heads + head) * p.tiles;
+  float norm = 0.f;
+  for (int i = tid; i * kScorePages < end; i += kT) norm = fmaxf(norm, norms[i]);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) norm = fmaxf(norm, __shfl_xor_sync(0xFFFFFFFFu, norm, o));
-  if (lane == 0) s_norm[warp] = norm;
-  __syncthreads();
+  if (W > 1) {
+    if (lane == 0) x.norm[warp] = norm;
+    sync();
 #pragma unroll
-  for (int w = 0; w < kPickThreads / 32; ++w) norm = fmaxf(norm, s_norm[w]);
+    for (int w = 0; w < W; ++w) norm = fmaxf(norm, x.norm[w]);
+  }
   // more than 2^-14.5 of the norms, and of what their squares may have lost below 2^-126
   const float e = norm * p.row_norm[(int64_t)(t - p.t0) * p.kv_heads + head] * 4.4e-5f + 0x1p-50f;
   auto fine = [&](float s) { return fabsf(s) < INFINITY && e < INFINITY; };
-  float mine = -INFINITY;
-  for (int j = p.lead + tid; j < end; j += kPickThreads) {
-    const float s = row[j];
-    if (fine(s)) mine = fmaxf(mine, s - e);
-  }
-  best[tid] = mine;
-  __syncthreads();
-  {
-    int above = 0;
-    for (int i = 0; i < kPickThreads; ++i) {
-      const float x = best[i];
-      above += x > mine || (x == mine && i < tid);
+  auto four_at = [&](int j) { return *reinterpret_cast<const float4*>(scores + j); };  // (rows are padded to eight)
+  const int from = p.lead & ~3;
+  float best[8];  // of eight groups (of one, with more warps)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) best[i] = -INFINITY;
+#pragma unroll 2
+  for (int j0 = from + 4 * tid; j0 < end; j0 += 8 * kT) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = j0 + 4 * kT * h;
+      if (j >= end) break;
+      const float4 f = four_at(j);
+      const float s[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j + i >= p.lead && j + i < end && fine(s[i])) best[4 * h + i] = fmaxf(best[4 * h + i], s[i] - e);
     }
-    if (above == m - 1) s_floor = mine;
   }
-  __syncthreads();
-  const float least = s_floor;
-  for (int j = p.lead + tid; j < end; j += kPickThreads) {
-    const float s = row[j];
-    const bool f = fine(s);
-    if (!f || s + e >= least) {
-      const int at = atomicAdd(&s_count, 1);
-      if (at < kPickList) {
-        page_of[at] = j;
-        low[at] = f ? s - e : -INFINITY;
-        high[at] = f ? s + e : INFINITY;
+  if (W > 1) {
+    float top = best[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, best[i]);
+    x.group[tid] = top;
+    sync();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) best[i] = x.group[lane + 32 * i];
+  } else {
+    sync();
+  }
+  // a floor that m of the 256 reach, and few more: by halves between their extremes
+  float least;
+  {
+    uint32_t o[8], hi = 0, lo = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[i] = order_of(best[i]);
+      hi = max(hi, o[i]);
+      lo = min(lo, o[i]);
+    }
+    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    while (lo < hi) {  // at least m reach lo
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      int reach = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) reach += o[i] >= mid;
+      reach = __reduce_add_sync(0xFFFFFFFFu, reach);
+      if (reach >= m) {
+        lo = mid;
+        if (reach <= m + 4) break;
+      } else {
+        hi = mid - 1;
       }
     }
+    least = float_of(lo);
   }
-  __syncthreads();
-  const int count = s_count;
+#pragma unroll 2
+  for (int j = from + 4 * tid; j - 4 * tid < end; j += 4 * kT) {
+    const float4 f = j < end ? four_at(j) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float s[4] = {f.x, f.y, f.z, f.w};
+    uint32_t in = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      in |= (uint32_t)(j + i >= p.lead && j + i < end && (!fine(s[i]) || s[i] + e >= least)) << i;
+    if (!__any_sync(0xFFFFFFFFu, in)) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (in >> i & 1u) {
+        const int at = atomicAdd(&x.count, 1);
+        if (at < Pick<W>::kList) {
+          x.page[at] = j + i;
+          x.score[at] = s[i];
+        }
+      }
+  }
+  sync();
+  const int count = x.count;
   // the group's sum in fp64, when a score has to be told exactly
   auto sum_heads = [&]() {
-    if (tid < kKvDim) {
-      double x = 0.0;
-      const char* src = static_cast<const char*>(p.q) + 2 * (t * p.q_stride + head * p.n * kKvDim + (tid & ~1));
+    for (int d = tid; d < kKvDim / 2; d += kT) {
+      double y = 0.0, z = 0.0;
+      const char* src = static_cast<const char*>(p.q) + 2 * (t * p.q_stride + head * p.n * kKvDim + 2 * d);
       for (int h = 0; h < p.n; ++h) {
         const float2 f = pair_f32<kBf16>(*reinterpret_cast<const uint32_t*>(src + 2 * h * kKvDim));
-        x += (double)(tid & 1 ? f.y : f.x);
+        y += (double)f.x;
+        z += (double)f.y;
       }
-      qs[tid] = x;
+      x.qs[2 * d] = y;
+      x.qs[2 * d + 1] = z;
     }
-    __syncthreads();
+    sync();
   };
   auto exact_key = [&](int j) -> int64_t {  // by a warp
     const int id = table[j];
-    double x = __longlong_as_double(0x7FF8000000000000ll);
+    double y = __longlong_as_double(0x7FF8000000000000ll);
     if (id >= 0 && id < p.pages) {
       const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const char*>(p.means) +
                                                       2 * (((int64_t)id * p.kv_heads + head) * kKvDim + 4 * lane));
       const float2 f = pair_f32<kBf16>(w.x), g = pair_f32<kBf16>(w.y);
-      x = qs[4 * lane] * f.x + qs[4 * lane + 1] * f.y + qs[4 * lane + 2] * g.x + qs[4 * lane + 3] * g.y;
+      y = x.qs[4 * lane] * f.x + x.qs[4 * lane + 1] * f.y + x.qs[4 * lane + 2] * g.x + x.qs[4 * lane + 3] * g.y;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+      for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
     }
-    return rank_key(x);
+    return rank_key(y);
   };
-  int taken;
-  if (count <= kPickList) {
-    for (int i = tid; i < count; i += kPickThreads) {
+  if (count <= Pick<W>::kList) {
+    for (int i = tid; i < count; i += kT) {
+      const bool f = fine(x.score[i]);
+      const float low = f ? x.score[i] - e : -INFINITY, high = f ? x.score[i] + e : INFINITY;
       int maybe = 0, sure = 0;
       for (int k = 0; k < count; ++k) {
-        sure += low[k] > high[i];
-        maybe += k != i && high[k] >= low[i];
+        const float s = x.score[k];
+        const bool g = fine(s);
+        sure += g && s - e > high;
+        maybe += k != i && (!g || s + e >= low);
       }
       const int st = maybe < m ? 1 : sure >= m ? 0 : 2;
-      state[i] = (uint8_t)st;
-      if (st == 1) atomicAdd(&s_sure, 1);
-      if (st == 2) open_list[atomicAdd(&s_open, 1)] = i;
+      x.state[i] = (uint8_t)st;
+      if (st == 1) atomicAdd(&x.sure, 1);
+      if (st == 2) x.open_list[atomicAdd(&x.open, 1)] = (uint16_t)i;
     }
-    __syncthreads();
-    const int open = s_open, room = m - s_sure;
+    sync();
+    const int open = x.open, room = m - x.sure;
     if (open > 0) {
       sum_heads();
-      for (int i = warp; i < open; i += kPickThreads / 32) {
-        const int64_t x = exact_key(page_of[open_list[i]]);
-        if (lane == 0) key[i] = x;
+      for (int i = warp; i < open; i += W) {
+        const int64_t y = exact_key(x.page[x.open_list[i]]);
+        if (lane == 0) x.key[i] = y;
       }
-      __syncthreads();
-      for (int i = tid; i < open; i += kPickThreads) {
-        const int j = page_of[open_list[i]];
+      sync();
+      for (int i = tid; i < open; i += kT) {
+        const int j = x.page[x.open_list[i]];
         int above = 0;
-        for (int k = 0; k < open; ++k) above += key[k] > key[i] || (key[k] == key[i] && page_of[open_list[k]] < j);
-        if (above < room) state[open_list[i]] = 1;  // (a 2 of another entry is not looked at here)
+        for (int k = 0; k < open; ++k) above += x.key[k] > x.key[i] || (x.key[k] == x.key[i] && x.page[x.open_list[k]] < j);
+        if (above < room) x.state[x.open_list[i]] = 1;  // (a 2 of another entry is not looked at here)
       }
-      __syncthreads();
+      sync();
     }
     // in page order
-    for (int i = tid; i < count; i += kPickThreads) {
-      if (state[i] != 1) continue;
+    for (int i = tid; i < count; i += kT) {
+      if (x.state[i] != 1) continue;
       int at = 0;
-      for (int k = 0; k < count; ++k) at += state[k] == 1 && page_of[k] < page_of[i];
-      out[p.lead + at] = page_of[i];
+      for (int k = 0; k < count; ++k) at += x.state[k] == 1 && x.page[k] < x.page[i];
+      out[p.lead + at] = x.page[i];
     }
     return;
   }
-  // page_of and key: the best so far, then the next 256
+  // page and key: the best so far, then as many more as there is room for
   sum_heads();
-  taken = 0;
-  for (int j0 = p.lead; j0 < end; j0 += kPickThreads) {
-    const int more = min(kPickThreads, end - j0);
-    __syncthreads();
-    for (int i = warp; i < more; i += kPickThreads / 32) {
-      const int64_t x = exact_key(j0 + i);
+  int taken = 0;
+  for (int j0 = p.lead; j0 < end;) {
+    const int more = min(Pick<W>::kList - Pick<W>::kMost, end - j0);
+    sync();
+    for (int i = warp; i < more; i += W) {
+      const int64_t y = exact_key(j0 + i);
       if (lane == 0) {
-        key[taken + i] = x;
-        page_of[taken + i] = j0 + i;
+        x.key[taken + i] = y;
+        x.page[taken + i] = j0 + i;
       }
     }
-    __syncthreads();
+    sync();
     const int all = taken + more;
-    int64_t kk[2];
-    int pp[2], to[2] = {-1, -1};
+    constexpr int kEach = Pick<W>::kList / kT;
+    int64_t kk[kEach];
+    int pp[kEach], to[kEach];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int i = tid + u * kPickThreads;
+    for (int u = 0; u < kEach; ++u) {
+      const int i = tid + u * kT;
+      to[u] = -1;
       if (i >= all) continue;
-      kk[u] = key[i];
-      pp[u] = page_of[i];
+      kk[u] = x.key[i];
+      pp[u] = x.page[i];
       int above = 0;
-      for (int k = 0; k < all; ++k) above += key[k] > kk[u] || (key[k] == kk[u] && page_of[k] < pp[u]);
+      for (int k = 0; k < all; ++k) above += x.key[k] > kk[u] || (x.key[k] == kk[u] && x.page[k] < pp[u]);
       if (above < m) to[u] = above;
     }
-    __syncthreads();
+    sync();
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kEach; ++u)
       if (to[u] >= 0) {
-        key[to[u]] = kk[u];
-        page_of[to[u]] = pp[u];
+        x.key[to[u]] = kk[u];
+        x.page[to[u]] = pp[u];
       }
     taken = min(all, m);
+    j0 += more;
   }
-  __syncthreads();
-  if (tid < taken) chosen[tid] = page_of[tid];
-  __syncthreads();
-  if (tid < taken) {
+  sync();
+  for (int i = tid; i < taken; i += kT) {
     int at = 0;
-    for (int k = 0; k < taken; ++k) at += chosen[k] < chosen[tid];
-    out[p.lead + at] = chosen[tid];
+    for (int k = 0; k < taken; ++k) at += x.page[k] < x.page[i];
+    out[p.lead + at] = x.page[i];
   }
 }
 
@@ -668,11 +769,14 @@ SelectSizes select_sizes(const dsa_kv_cfg* cfg, int32_t tokens, int32_t requests
   s.width = ((int64_t)table_width + 7) & ~(int64_t)7;
   s.tiles = (table_width + kScorePages - 1) / kScorePages;
   const int64_t row = std::max<int64_t>(1, s.width * cfg->kv_heads * 4);
-  s.tokens = std::max<int64_t>(1, kScoreBytes / row / kScoreTokens) * kScoreTokens;
-  s.tokens = std::min<int64_t>(s.tokens, ((int64_t)tokens + kScoreTokens - 1) / kScoreTokens * kScoreTokens);
+  // equal parts of a step, each of blocks of 64 tokens
+  const int64_t blocks = ((int64_t)tokens + kScoreTokens - 1) / kScoreTokens;
+  const int64_t most = std::max<int64_t>(1, kScoreBytes / row / kScoreTokens);
+  const int64_t parts = std::max<int64_t>(1, (blocks + most - 1) / most);
+  s.tokens = (blocks + parts - 1) / parts * kScoreTokens;
   s.norm_off = fused_align16(s.tokens * row);
   s.tile_off = s.norm_off + fused_align16(s.tokens * cfg->kv_heads * 4);
-  s.bytes = s.tile_off + fused_align16((requests + s.tokens / kScoreTokens) * cfg->kv_heads * s.tiles * 8);
+  s.bytes = s.tile_off + fused_align16((requests + s.tokens / kScoreTokens) * cfg->kv_heads * s.tiles * 4);
   return s;
 }
 
@@ -692,6 +796,24 @@ int sms_of_device() {
     cache[dev] = n;
   }
   return cache[dev];
+}
+
+// Lets the score kernels take their shared memory, once a device.
+int select_ready() {
+  static bool done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return DSA_ERR_CUDA;
+  }
+  if (dev >= 0 && dev < 64 && done[dev]) return DSA_OK;
+  if (cudaFuncSetAttribute(score_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(score_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return DSA_ERR_CUDA;
+  }
+  if (dev >= 0 && dev < 64) done[dev] = true;
+  return DSA_OK;
 }
 
 }  // namespace
@@ -784,6 +906,8 @@ int dsa_kv_select(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t 
   if (workspace_bytes < (size_t)sz.bytes) return DSA_ERR_INVALID_ARG;
   const int sms = sms_of_device();
   if (!sms) return DSA_ERR_CUDA;
+  const int ready = select_ready();
+  if (ready != DSA_OK) return ready;
   SelectParams p;
   p.means = means;
   p.q = q;
@@ -828,6 +952,7 @@ int dsa_kv_select(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t 
       attr[0].val.programmaticStreamSerializationAllowed = 1;
       lc.attrs = attr;
       lc.numAttrs = 1;
+      lc.dynamicSmemBytes = kScoreSmem;
       const cudaError_t err = cfg->dtype == DSA_BF16 ? cudaLaunchKernelEx(&lc, score_kernel<true>, p)
                                                      : cudaLaunchKernelEx(&lc, score_kernel<false>, p);
       if (err != cudaSuccess) {
@@ -835,9 +960,17 @@ int dsa_kv_select(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t 
         return DSA_ERR_CUDA;
       }
     }
+    // a warp a row, where there are rows enough to fill the SMs with warps and their
+    // lists are short; else eight
     const int64_t rows = (int64_t)(p.t1 - p.t0) * cfg->kv_heads;
-    st = cfg->dtype == DSA_BF16 ? launch_dependent(pick_kernel<true>, rows, kPickThreads, 0, 0, stream, p)
-                                : launch_dependent(pick_kernel<false>, rows, kPickThreads, 0, 0, stream, p);
+    const bool one = select - lead - trail <= Pick<1>::kMost && rows >= 16 * (int64_t)sms && table_width <= 8192;
+    const int64_t blocks = one ? (rows + 7) / 8 : rows;
+    if (one)
+      st = cfg->dtype == DSA_BF16 ? launch_dependent(pick_kernel<true, 1>, blocks, kPickThreads, 0, 0, stream, p)
+                                  : launch_dependent(pick_kernel<false, 1>, blocks, kPickThreads, 0, 0, stream, p);
+    else
+      st = cfg->dtype == DSA_BF16 ? launch_dependent(pick_kernel<true, 8>, blocks, kPickThreads, 0, 0, stream, p)
+                                  : launch_dependent(pick_kernel<false, 8>, blocks, kPickThreads, 0, 0, stream, p);
     if (st != DSA_OK) return st;
   }
   return DSA_OK;
