@@ -224,12 +224,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 // ---------------------------------------------------------------------------
 // select
 
-constexpr int kScoreTokens = 64, kScorePages = 128, kScoreThreads = 256;
+constexpr int kScoreTokens = 64, kScorePages = 64, kScoreThreads = 256, kScoreStages = 4;
 constexpr int kPitch = 2 * 2 * kKvDim + 16;             // bytes of a row of both halves in shared memory
 constexpr int kMeanTile = kScorePages * 2 * kKvDim;     // bytes of a tile of mean keys
-constexpr int kScoreSmem = kScoreTokens * kPitch + 2 * kMeanTile;
+constexpr int kScoreIds = 32;  // tiles whose page ids are looked up at a time
+constexpr int kScoreSmem = kScoreTokens * kPitch + kScoreStages * kMeanTile + kScoreIds * kScorePages * 4;
 constexpr int kPickThreads = 256;
-constexpr int64_t kScoreBytes = 64 << 20;  // scores of the tokens in work: they stay in L2
+constexpr int64_t kScoreBytes = 96 << 20;  // scores of the tokens in work: most of them stay in L2
 
 struct SelectParams {
   const void *means, *q;
@@ -273,10 +274,10 @@ __device__ __forceinline__ int own_page(int pos, int shift, int P) { return pos 
 // Slot x < R is request x's tokens in its first block of 64 (blocks are of the
 // whole batch), slot R + j those of the request that goes on into block j.
 template <bool kBf16>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams p) {
-  extern __shared__ __align__(16) uint8_t sums[];  // the heads' sums | two tiles of means
-  __shared__ int piece[3], top_norm[2];
-  __shared__ uint32_t there[2][kScoreThreads / 32];
+__global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectParams p) {
+  extern __shared__ __align__(16) uint8_t sums[];  // the heads' sums | tiles of means
+  __shared__ int piece[3], top_norm[kScoreStages];
+  __shared__ uint32_t there[kScoreStages][kScoreThreads / 32];
   const uint8_t* means = sums + kScoreTokens * kPitch;
   const uint32_t means_at = (uint32_t)__cvta_generic_to_shared(means);
   let_next_start();
@@ -318,6 +319,42 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
   const int tiles = (end + kScorePages - 1) / kScorePages;
   if (split >= tiles) return;
 
+  // Tiles of 64 means come through four stages of shared memory, a quarter of a row a
+  // thread; a row's halves trade places by its parity so that the eight lanes of a
+  // phase below read different banks.
+  const int32_t* table = p.tables + (int64_t)r * p.P;
+  const int prow = threadIdx.x >> 2, quarter = threadIdx.x & 3;
+  int32_t* ids = reinterpret_cast<int32_t*>(sums + kScoreTokens * kPitch + kScoreStages * kMeanTile);
+  auto look_up = [&](int i0) {  // of this CTA's tiles i0 .. i0 + 31
+#pragma unroll
+    for (int k = 0; k < kScoreIds * kScorePages / kScoreThreads; ++k) {
+      const int x = threadIdx.x + k * kScoreThreads, tile = split + (i0 + x / kScorePages) * p.splits;
+      const int j = tile * kScorePages + x % kScorePages;
+      ids[x] = tile < tiles && j < end ? table[j] : -1;
+    }
+    __syncthreads();
+  };
+  auto copy = [&](int stage, int i) {  // this CTA's i-th tile
+    if (split + i * p.splits < tiles) {
+      const int id = ids[i % kScoreIds * kScorePages + prow];
+      const bool ok = id >= 0 && id < p.pages;
+      const char* src = static_cast<const char*>(p.means) + 2 * (((int64_t)(ok ? id : 0) * p.kv_heads + head) * kKvDim) + 64 * quarter;
+      const uint32_t dst = means_at + stage * kMeanTile + prow * 256;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (((4 * quarter + i) ^ ((prow & 1) << 2)) << 4)),
+                     "l"(ok ? src + 16 * i : static_cast<const char*>(p.q)), "r"(ok ? 16 : 0)
+                     : "memory");
+      const uint32_t have = __ballot_sync(0xFFFFFFFFu, ok);  // four lanes a page
+      if (lane == 0) there[stage][warp] = have;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (threadIdx.x < kScoreStages) top_norm[threadIdx.x] = 0;
+  look_up(0);
+#pragma unroll
+  for (int i = 0; i < kScoreStages - 1; ++i) copy(i, i);
+
   // the heads' sums: four lanes a row, 32 dims each
   {
     const int row = threadIdx.x >> 2, part = threadIdx.x & 3;
@@ -329,17 +366,25 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
     for (int i = 0; i < 32; ++i) m[i] = 0.f;
     if (a + row < b) {
       const char* src = static_cast<const char*>(p.q) + 2 * ((a + row) * p.q_stride + head * p.n * kKvDim + 32 * part);
-      for (int h = 0; h < p.n; ++h) {
+      for (int h0 = 0; h0 < p.n; h0 += 2) {
+        Eight y[2][4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float x[8];
-          unpack8<kBf16>(load8(src + 2 * h * kKvDim + 16 * c), x);
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            f[8 * c + e] += x[e];
-            m[8 * c + e] += fabsf(x[e]);
+          for (int c = 0; c < 4; ++c)
+            y[h][c] = h0 + h < p.n ? load8(src + 2 * (h0 + h) * kKvDim + 16 * c) : Eight{{0u, 0u, 0u, 0u}};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float x[8];
+            unpack8<kBf16>(y[h][c], x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              f[8 * c + e] += x[e];
+              m[8 * c + e] += fabsf(x[e]);
+            }
           }
-        }
       }
     }
     float top = 0.f;
@@ -371,28 +416,6 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
     }
   }
   __syncthreads();
-  // Tiles of 128 means come through two stages of shared memory, half a row a
-  // thread, and a row's 64-byte quarters trade places by its parity so that the eight
-  // lanes of a phase below read different banks.
-  const int32_t* table = p.tables + (int64_t)r * p.P;
-  const int prow = threadIdx.x >> 1, phalf = threadIdx.x & 1;
-  auto id_at = [&](int tile) {
-    const int j = tile * kScorePages + prow;
-    return j < end ? table[j] : -1;
-  };
-  auto copy = [&](int stage, int id) {
-    const bool ok = id >= 0 && id < p.pages;
-    const char* src = static_cast<const char*>(p.means) + 2 * (((int64_t)(ok ? id : 0) * p.kv_heads + head) * kKvDim) + 128 * phalf;
-    const uint32_t dst = means_at + stage * kMeanTile + prow * 256;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (((8 * phalf + i) ^ ((prow & 1) << 2)) << 4)),
-                   "l"(ok ? src + 16 * i : static_cast<const char*>(p.q)), "r"(ok ? 16 : 0)
-                   : "memory");
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    const uint32_t have = __ballot_sync(0xFFFFFFFFu, ok);  // two lanes a page
-    if (lane == 0) there[stage][warp] = have;
-  };
   // The warps: 1, 2 or 4 groups of 16 tokens, and as many groups of a tile's pages as
   // that leaves.  Fragments' dims are taken in the order that makes a lane's loads 16
   // bytes: dims 8 (c + 4 i) + 4 s .. + 3 for lane c of a row, step 2 i + s.
@@ -416,19 +439,18 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
   const int ta = a + 16 * wm + gq, tb = ta + 8;
   float* rowa = p.scores + ((int64_t)(ta - p.t0) * p.kv_heads + head) * p.width;
   float* rowb = p.scores + ((int64_t)(tb - p.t0) * p.kv_heads + head) * p.width;
-  copy(0, id_at(split));
-  int next = split + p.splits;
-  int id = id_at(next);
-  for (int tile = split, stage = 0; tile < tiles; tile = next, stage ^= 1) {
-    next = tile + p.splits;
-    if (next < tiles) copy(stage ^ 1, id);
-    id = id_at(next + p.splits);
-    if (threadIdx.x == 0) top_norm[stage] = 0;
-    if (next < tiles)
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
+  float* norms = p.tile_norm + ((int64_t)blockIdx.x * p.kv_heads + head) * p.tiles;
+  int stage = 0, i = 0;
+  for (int tile = split; tile < tiles; tile += p.splits, stage = (stage + 1) % kScoreStages, ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - 2) : "memory");
+    __syncthreads();  // the tile is there; all are done with the one before
+    const int last = (stage + kScoreStages - 1) % kScoreStages;
+    if (threadIdx.x == 0 && tile != split) {
+      norms[tile - p.splits] = sqrtf(__int_as_float(top_norm[last]));
+      top_norm[last] = 0;
+    }
+    if ((i + kScoreStages - 1) % kScoreIds == 0) look_up(i + kScoreStages - 1);
+    copy(last, i + kScoreStages - 1);
     float top = 0.f;
 #pragma unroll 1
     for (int u = 0; u < pages_each / 8; ++u) {
@@ -459,9 +481,9 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
         top = fmaxf(top, s);
       }
       // columns 2 c and 2 c + 1; a page without an id scores a NaN
-      const uint32_t have = there[stage][j8 >> 4] >> (2 * (j8 & 15));
+      const uint32_t have = there[stage][j8 >> 3];
       const float nan = __int_as_float(0x7FFFFFFF);
-      const bool h0 = have >> (4 * c) & 1u, h1 = have >> (4 * c + 2) & 1u;
+      const bool h0 = have >> (8 * c) & 1u, h1 = have >> (8 * c + 4) & 1u;
       const int col = tile * kScorePages + j8 + 2 * c;
       if (col < p.width) {
         if (ta < b)
@@ -473,10 +495,11 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     if (lane == 0) atomicMax(&top_norm[stage], __float_as_int(top));  // (not negative)
-    __syncthreads();
-    if (threadIdx.x == 0)
-      p.tile_norm[((int64_t)blockIdx.x * p.kv_heads + head) * p.tiles + tile] = sqrtf(__int_as_float(top_norm[stage]));
   }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    norms[split + (tiles - 1 - split) / p.splits * p.splits] =
+        sqrtf(__int_as_float(top_norm[(stage + kScoreStages - 1) % kScoreStages]));
 }
 
 // A double's place in the order of ranks: NaN lowest, then -inf .. inf.
@@ -516,7 +539,7 @@ __device__ __forceinline__ float float_of(uint32_t o) {
 }
 
 template <bool kBf16, int W>
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(const SelectParams p) {
   constexpr int kT = 32 * W;  // threads a row
   __shared__ Pick<W> rows[kPickThreads / kT];
   let_next_start();
@@ -565,22 +588,30 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectParams p
   // more than 2^-14.5 of the norms, and of what their squares may have lost below 2^-126
   const float e = norm * p.row_norm[(int64_t)(t - p.t0) * p.kv_heads + head] * 4.4e-5f + 0x1p-50f;
   auto fine = [&](float s) { return fabsf(s) < INFINITY && e < INFINITY; };
-  auto four_at = [&](int j) { return *reinterpret_cast<const float4*>(scores + j); };  // (rows are padded to eight)
+  // scores a few loads a thread at a time; rows of no more stay there
+  constexpr int kLoads = W == 1 ? 8 : 16, kAtOnce = 4 * kLoads * kT;
   const int from = p.lead & ~3;
+  float4 f[kLoads];
+  auto read = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int j = j0 + 4 * (tid + i * kT);  // (rows are padded to eight)
+      f[i] = j < end ? *reinterpret_cast<const float4*>(scores + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  auto is_free = [&](int j) { return j >= p.lead && j < end; };
   float best[8];  // of eight groups (of one, with more warps)
 #pragma unroll
   for (int i = 0; i < 8; ++i) best[i] = -INFINITY;
-#pragma unroll 2
-  for (int j0 = from + 4 * tid; j0 < end; j0 += 8 * kT) {
+  for (int j0 = from; j0 < end; j0 += kAtOnce) {
+    read(j0);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = j0 + 4 * kT * h;
-      if (j >= end) break;
-      const float4 f = four_at(j);
-      const float s[4] = {f.x, f.y, f.z, f.w};
+    for (int i = 0; i < kLoads; ++i) {
+      const int j = j0 + 4 * (tid + i * kT);
+      const float s[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (j + i >= p.lead && j + i < end && fine(s[i])) best[4 * h + i] = fmaxf(best[4 * h + i], s[i] - e);
+      for (int u = 0; u < 4; ++u)
+        if (is_free(j + u) && fine(s[u])) best[4 * (i & 1) + u] = fmaxf(best[4 * (i & 1) + u], s[u] - e);
     }
   }
   if (W > 1) {
@@ -621,24 +652,26 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectParams p
     }
     least = float_of(lo);
   }
-#pragma unroll 2
-  for (int j = from + 4 * tid; j - 4 * tid < end; j += 4 * kT) {
-    const float4 f = j < end ? four_at(j) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float s[4] = {f.x, f.y, f.z, f.w};
-    uint32_t in = 0;
+  for (int j0 = from; j0 < end; j0 += kAtOnce) {
+    if (end - from > kAtOnce) read(j0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      in |= (uint32_t)(j + i >= p.lead && j + i < end && (!fine(s[i]) || s[i] + e >= least)) << i;
-    if (!__any_sync(0xFFFFFFFFu, in)) continue;
+    for (int i = 0; i < kLoads; ++i) {
+      const int j = j0 + 4 * (tid + i * kT);
+      const float s[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
+      uint32_t in = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (in >> i & 1u) {
-        const int at = atomicAdd(&x.count, 1);
-        if (at < Pick<W>::kList) {
-          x.page[at] = j + i;
-          x.score[at] = s[i];
+      for (int u = 0; u < 4; ++u) in |= (uint32_t)(is_free(j + u) && (!fine(s[u]) || s[u] + e >= least)) << u;
+      if (!in) continue;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (in >> u & 1u) {
+          const int at = atomicAdd(&x.count, 1);
+          if (at < Pick<W>::kList) {
+            x.page[at] = j + u;
+            x.score[at] = s[u];
+          }
         }
-      }
+    }
   }
   sync();
   const int count = x.count;
@@ -647,10 +680,17 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectParams p
     for (int d = tid; d < kKvDim / 2; d += kT) {
       double y = 0.0, z = 0.0;
       const char* src = static_cast<const char*>(p.q) + 2 * (t * p.q_stride + head * p.n * kKvDim + 2 * d);
-      for (int h = 0; h < p.n; ++h) {
-        const float2 f = pair_f32<kBf16>(*reinterpret_cast<const uint32_t*>(src + 2 * h * kKvDim));
-        y += (double)f.x;
-        z += (double)f.y;
+      for (int h0 = 0; h0 < p.n; h0 += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+          w[h] = h0 + h < p.n ? *reinterpret_cast<const uint32_t*>(src + 2 * (h0 + h) * kKvDim) : 0u;
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          const float2 g = pair_f32<kBf16>(w[h]);
+          y += (double)g.x;
+          z += (double)g.y;
+        }
       }
       x.qs[2 * d] = y;
       x.qs[2 * d + 1] = z;
@@ -940,9 +980,9 @@ int dsa_kv_select(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t 
     const int64_t slots = requests + (p.t1 - p.t0 + kScoreTokens - 1) / kScoreTokens;
     int st = DSA_OK;
     if (table_width > select) {
-      // page tiles over as many CTAs as it takes to have four an SM
+      // page tiles over as many CTAs as are at home at once, eight tiles or more each
       const int64_t pieces = slots * cfg->kv_heads;
-      p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>(sz.tiles, (4 * sms + pieces - 1) / pieces));
+      p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>((sz.tiles + 7) / 8, 2 * sms / pieces));
       cudaLaunchConfig_t lc = {};
       lc.gridDim = dim3((unsigned)slots, (unsigned)(cfg->kv_heads * p.splits));
       lc.blockDim = dim3(kScoreThreads);
