@@ -23,9 +23,11 @@ INCLUDE = os.path.join(ROOT, "include")
 SOURCES = [os.path.join(PKG, "csrc", "dsa_select.cu"), os.path.join(PKG, "csrc", "dsa_indexer.cu"),
            os.path.join(PKG, "csrc", "dsa_attention.cu"), os.path.join(PKG, "csrc", "dsa_cache.cu"),
            os.path.join(PKG, "csrc", "dsa_cache_attention.cu"), os.path.join(PKG, "csrc", "dsa_cache_tile.cu"),
-           os.path.join(PKG, "csrc", "dsa_kv.cu"), os.path.join(PKG, "csrc", "dsa_kv_attend.cu")]
+           os.path.join(PKG, "csrc", "dsa_kv.cu"), os.path.join(PKG, "csrc", "dsa_kv_attend.cu"),
+           os.path.join(PKG, "csrc", "dsa_kv_select.cu")]
 HEADERS = [os.path.join(INCLUDE, "dsa_select.h"), os.path.join(PKG, "csrc", "dsa_internal.h"),
-           os.path.join(PKG, "csrc", "dsa_cache.h"), os.path.join(PKG, "csrc", "dsa_kv.h")]
+           os.path.join(PKG, "csrc", "dsa_cache.h"), os.path.join(PKG, "csrc", "dsa_kv.h"),
+           os.path.join(PKG, "csrc", "dsa_kv_mma.h")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libdsa_select.so")
 CALLS_SOURCE = os.path.join(PKG, "csrc", "cache_calls.cpp")

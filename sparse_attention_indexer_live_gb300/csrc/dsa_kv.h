@@ -51,6 +51,9 @@ struct KvParams {
   int32_t flip;  // the softmax scale is negative
 };
 
+// The selection kernels' error word (dsa_kv_select.cu), read and cleared.
+DSA_HIDDEN int dsa_kv_select_error(int* v);
+
 #ifdef __CUDACC__
 
 // Eight elements of a row.
