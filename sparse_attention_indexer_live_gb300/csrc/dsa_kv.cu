@@ -21,7 +21,9 @@ struct AppendParams {
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendBatch = 3;  // groups of four rows whose loads a warp has in flight
+constexpr int kMeansWithin = 512;  // tokens
+template <bool kMeans>
+constexpr int kAppendBatch = kMeans ? 3 : 2;  // groups of four rows whose loads a warp has in flight
 
 // One row is two 16-byte chunks in each of eight lanes.  Pairs of dims half a
 // rotation apart lie in chunks l and l + rotary / 16 of the same lane, neighbours
@@ -85,6 +87,25 @@ __device__ __forceinline__ void rotate(Eight& a, Eight& b, const Turn& t, int ne
   }
   a = pack8<kBf16>(x);
   b = pack8<kBf16>(y);
+}
+
+// The same by a warp whose lanes want one position's: each computes two pairs.
+__device__ __forceinline__ void turn_of_warp(const int64_t* turns, int half, int lane, int pos, float gain, Turn& t) {
+  const int g = lane >> 3, l = lane & 7;
+  float c[2], s[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int pair = 8 * l + 2 * g + e;
+    const uint64_t x = pair < half ? (uint64_t)turns[pair] * (uint64_t)(uint32_t)pos : 0;
+    sincospif((float)(int64_t)x * 0x1p-63f, &s[e], &c[e]);
+    c[e] *= gain;
+    s[e] *= gain;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    t.c[e] = __shfl_sync(0xFFFFFFFFu, c[e & 1], (e >> 1) * 8 + l);
+    t.s[e] = __shfl_sync(0xFFFFFFFFu, s[e & 1], (e >> 1) * 8 + l);
+  }
 }
 
 // The mean key of each page that one of 32 tokens fills, for one key/value head:
@@ -158,15 +179,74 @@ __device__ void page_means(const AppendParams& p, int block) {
   }
 }
 
+// The same from the cache alone, for the pages of 32 tokens: a warp a page and head,
+// 32 rows' loads in flight.
+template <bool kBf16>
+__global__ void __launch_bounds__(kAppendThreads) means_kernel(const AppendParams p) {
+  let_next_start();
+  wait_for_previous();
+  const int t0 = 32 * blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 7;
+  const int t = t0 + lane;
+  const int slot = t < p.T && p.ends[t] > 0 ? p.slots[t] : -1;
+  const uint32_t full = __ballot_sync(0xFFFFFFFFu, slot >= 0 && slot < p.slots_n && (slot & (p.page - 1)) == p.page - 1);
+  for (int x = warp; x < __popc(full) * p.kv_heads; x += kAppendThreads / 32) {
+    const int head = x % p.kv_heads;
+    uint32_t rest = full;
+    for (int k = x / p.kv_heads; k > 0; --k) rest &= rest - 1;
+    const int last = __shfl_sync(0xFFFFFFFFu, slot, __ffs(rest) - 1);
+    const char* src = static_cast<const char*>(p.k_cache) +
+                      2 * (((int64_t)(last - (p.page - 1) + (lane >> 3)) * p.kv_heads + head) * kKvDim + 16 * l);
+    float sum[16] = {};
+#pragma unroll 1
+    for (int r0 = 0; r0 < p.page; r0 += 32) {
+      Eight y[8][2];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const char* row = src + (int64_t)(r0 + 4 * u) * p.kv_heads * (2 * kKvDim);
+        const bool in = r0 + 4 * u < p.page;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) y[u][h] = in ? load8(row + 16 * h) : Eight{{0u, 0u, 0u, 0u}};
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[8];
+          unpack8<kBf16>(y[u][h], v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[8 * h + e] += v[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 8);
+      sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 16);
+    }
+    if (lane < 8) {
+      const float inv = 1.f / (float)p.page;  // a power of two
+      char* dst = static_cast<char*>(p.means) + 2 * (((int64_t)(last / p.page) * p.kv_heads + head) * kKvDim + 16 * l);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = sum[8 * h + e] * inv;
+        store8(dst + 16 * h, pack8<kBf16>(v));
+      }
+    }
+  }
+}
+
 // Rows are dealt out four to a warp, so that a row is eight lanes with two
 // 16-byte loads each and the angles of a token are computed once for all its
 // rows that a warp takes.  Bound by HBM for prompt chunks; by latency for a
 // decode step, whose rows go to as many warps as there are groups of four.
-template <bool kBf16>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+template <bool kBf16, bool kMeans>
+__global__ void __launch_bounds__(kAppendThreads, kMeans ? 1 : 4) append_kernel(const AppendParams p) {
+  constexpr int kBatch = kAppendBatch<kMeans>;
   let_next_start();
   wait_for_previous();
-  if ((int)blockIdx.x >= p.row_blocks) {
+  if (kMeans && (int)blockIdx.x >= p.row_blocks) {
     page_means<kBf16>(p, blockIdx.x - p.row_blocks);
     return;
   }
@@ -181,13 +261,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int rows = p.H + 2 * p.kv_heads;
   const int groups = (rows + 3) / 4;
   Turn turn;
-  if (ch.turned) turn_at(p.turns, l, p.neighbours, end - 1, p.gain, turn);
-  for (int g0 = first; g0 < groups; g0 += kAppendBatch * p.parts) {
-    Eight a[kAppendBatch], b[kAppendBatch];
-    char* dst[kAppendBatch];
-    bool spin[kAppendBatch];
+  turn_of_warp(p.turns, p.rotary / 2, lane, end - 1, p.gain, turn);
+  for (int g0 = first; g0 < groups; g0 += kBatch * p.parts) {
+    Eight a[kBatch], b[kBatch];
+    char* dst[kBatch];
+    bool spin[kBatch];
 #pragma unroll
-    for (int u = 0; u < kAppendBatch; ++u) {
+    for (int u = 0; u < kBatch; ++u) {
       const int row = 4 * (g0 + u * p.parts) + (lane >> 3);
       const char* src = nullptr;
       dst[u] = nullptr;
@@ -208,7 +288,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       }
     }
 #pragma unroll
-    for (int u = 0; u < kAppendBatch; ++u) {
+    for (int u = 0; u < kBatch; ++u) {
       if (!dst[u]) continue;
       if (spin[u]) rotate<kBf16>(a[u], b[u], turn, p.neighbours);
       store8(dst[u] + 2 * ch.a, a[u]);
@@ -289,12 +369,17 @@ int dsa_kv_append(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t 
   p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(groups, ((int64_t)sms * 16 + tokens - 1) / tokens));
   const int64_t warps = (int64_t)tokens * p.parts;
   const int64_t rows = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
-  const int64_t blocks = rows + (means ? ((int64_t)tokens + 31) / 32 * cfg->kv_heads : 0);
-  if (blocks > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  // Few tokens: means in the same launch, rotating the rows they need once more.
+  // Many: in a launch after it, from the cache.
+  const bool bf16 = cfg->dtype == DSA_BF16, within = means && tokens <= kMeansWithin;
+  const int64_t groups32 = ((int64_t)tokens + 31) / 32, sums = within ? groups32 * cfg->kv_heads : 0;
+  if (rows + sums > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   p.row_blocks = (int32_t)rows;
-  return cfg->dtype == DSA_BF16
-             ? launch_dependent(append_kernel<true>, blocks, kAppendThreads, 0, 0, stream, p)
-             : launch_dependent(append_kernel<false>, blocks, kAppendThreads, 0, 0, stream, p);
+  const auto kernel = within ? (bf16 ? append_kernel<true, true> : append_kernel<false, true>)
+                             : (bf16 ? append_kernel<true, false> : append_kernel<false, false>);
+  const int st = launch_dependent(kernel, rows + sums, kAppendThreads, 0, 0, stream, p);
+  if (st != DSA_OK || !means || within) return st;
+  return launch_dependent(bf16 ? means_kernel<true> : means_kernel<false>, groups32, kAppendThreads, 0, 0, stream, p);
 }
 
 }  // extern "C"

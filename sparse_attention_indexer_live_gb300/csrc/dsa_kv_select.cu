@@ -137,6 +137,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
 
   if (b - a <= kFewTokens) {
     float* sums = reinterpret_cast<float*>(base);  // [8][128]
+    const int first_j = 32 * (split * 8 + warp) + 8 * (lane & 3) + (lane >> 2);
+    const int first_id = first_j < end ? table[first_j] : -1;
     if (warp < b - a) {
       float f[4] = {}, m[4] = {};
       const char* src = static_cast<const char*>(p.q) + 2 * ((a + warp) * p.q_stride + head * p.n * kKvDim + 4 * lane);
@@ -176,9 +178,14 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
     // 32 pages a warp at a time, four lanes a page: chunks c, c + 4, .. of eight dims,
     // so that a load instruction takes whole sectors
     const int c = lane & 3;
-    for (int x = split * 8 + warp; x < 2 * tiles; x += 8 * p.splits) {
+    auto id_at = [&](int x) {
+      const int j = 32 * x + 8 * c + (lane >> 2);
+      return j < end ? table[j] : -1;
+    };
+    for (int x = split * 8 + warp, next_id = first_id; x < 2 * tiles; x += 8 * p.splits) {
       const int own_j = 32 * x + 8 * c + (lane >> 2);  // the page this lane writes
-      const int own_id = own_j < end ? table[own_j] : -1;
+      const int own_id = next_id;
+      next_id = id_at(x + 8 * p.splits);
       Eight e[4][4];
       float norm = 0.f;
 #pragma unroll
@@ -542,19 +549,9 @@ __global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(cons
   if (tid == 0) x.count = x.open = x.sure = 0;
   const int slot = t / kScoreTokens == rq.a / kScoreTokens ? r : p.R + (t - p.t0) / kScoreTokens;
   const float* norms = p.norms + ((int64_t)slot * p.kv_heads + head) * 2 * p.tiles;
+  const float row_norm = p.row_norm[(int64_t)(t - p.t0) * p.kv_heads + head];
   float norm = 0.f;
   for (int i = tid; 32 * i < end; i += kT) norm = fmaxf(norm, norms[i]);
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) norm = fmaxf(norm, __shfl_xor_sync(0xFFFFFFFFu, norm, o));
-  if (W > 1) {
-    if (lane == 0) x.norm[warp] = norm;
-    sync();
-#pragma unroll
-    for (int w = 0; w < W; ++w) norm = fmaxf(norm, x.norm[w]);
-  }
-  // more than 2^-14.5 of the norms, and of what their squares may have lost below 2^-126
-  const float e = norm * p.row_norm[(int64_t)(t - p.t0) * p.kv_heads + head] * 4.4e-5f + 0x1p-50f;
-  auto fine = [&](float s) { return fabsf(s) < INFINITY && e < INFINITY; };
   const int tiles = (end + kScorePages - 1) / kScorePages;
   const float4* top4 = reinterpret_cast<const float4*>(p.tops) + ((int64_t)(t - p.t0) * p.kv_heads + head) * p.tiles;
   auto is_free = [&](int j) { return j >= p.lead && j < end; };
@@ -565,7 +562,7 @@ __global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(cons
     const float* top1 = reinterpret_cast<const float*>(top4);
     for (int i = tid; i < 4 * tiles; i += kT) {
       const float s = top1[i];
-      if (fine(s)) best[0] = fmaxf(best[0], s - e);
+      if (fabsf(s) < INFINITY) best[0] = fmaxf(best[0], s);
     }
   } else if (2 * tiles >= m) {
     for (int i0 = tid; i0 < tiles; i0 += 2 * kT) {
@@ -576,7 +573,7 @@ __global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(cons
         const float s[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (fine(s[u])) best[4 * h + u] = fmaxf(best[4 * h + u], s[u] - e);
+          if (fabsf(s[u]) < INFINITY) best[4 * h + u] = fmaxf(best[4 * h + u], s[u]);
       }
     }
   } else {
@@ -589,7 +586,7 @@ __global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(cons
         const float s[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (is_free(j + u) && fine(s[u])) best[4 * h + u] = fmaxf(best[4 * h + u], s[u] - e);
+          if (is_free(j + u) && fabsf(s[u]) < INFINITY) best[4 * h + u] = fmaxf(best[4 * h + u], s[u]);
       }
     }
   }
@@ -604,6 +601,17 @@ __global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(cons
   } else {
     sync();
   }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) norm = fmaxf(norm, __shfl_xor_sync(0xFFFFFFFFu, norm, o));
+  if (W > 1) {
+    if (lane == 0) x.norm[warp] = norm;
+    sync();
+#pragma unroll
+    for (int w = 0; w < W; ++w) norm = fmaxf(norm, x.norm[w]);
+  }
+  // more than 2^-14.5 of the norms, and of what their squares may have lost below 2^-126
+  const float e = norm * row_norm * 4.4e-5f + 0x1p-50f;
+  auto fine = [&](float s) { return fabsf(s) < INFINITY && e < INFINITY; };
   // a floor that m of the 256 reach, and few more: by halves between their extremes
   float least;
   {
@@ -629,7 +637,7 @@ __global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(cons
         hi = mid - 1;
       }
     }
-    least = float_of(lo);
+    least = float_of(lo) - e;  // (all bounds are as far below)
   }
   // the groups that may reach it, 32 tiles of a warp at a time, and their pages
   for (int i0 = 32 * warp; i0 < tiles; i0 += 32 * W) {
