@@ -20,7 +20,7 @@
 // one's products while the other's scores are weighed: with two row tiles in the unit
 // a stream is a row tile (pair); with one it is every other tile of positions, and the
 // two are joined at the end.  A selection of pages is walked as the union of the
-// tile's tokens' lists, each row masked to its own.
+// tile's tokens' lists, which a warp of its own merges, each row masked to its own.
 // Every mbarrier wait is bounded by a clock limit.
 
 #include <cuda.h>
@@ -33,7 +33,7 @@
 
 namespace {
 
-constexpr int kThreads = 384;  // warps 0-7 softmax, 8 TMA, 9 scheduler, 10 MMA
+constexpr int kThreads = 384;  // warps 0-7 softmax, 8 TMA, 9 scheduler, 10 MMA, 11 lists
 constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
 // Registers (setmaxnreg): 168 a thread at launch; 256 x 200 + 128 x 104 = 384 x 168.
 constexpr int kLaunchRegs = 168, kSoftRegs = 200, kSideRegs = 104;
@@ -60,7 +60,7 @@ constexpr int kOffDesc = kOffInfo + kInfos * (int)sizeof(Info);
 constexpr int kOffXch = kOffDesc + kDescs * (int)sizeof(Desc);  // [stream][row] maximum and sum
 constexpr int kOffScan = kOffXch;                               // (before the first unit) warps' sums
 constexpr int kOffBars = kOffXch + 2 * 128 * 8;
-constexpr int kNumBars = 4 + 2 * kStages + kInfos + 2 * kDescs + 6 + 3;
+constexpr int kNumBars = 4 + 2 * kStages + kInfos + 2 * kDescs + 6 + 3 + kInfos;
 constexpr int kOffWord = kOffBars + kNumBars * 8;  // tensor memory's address, abort flag
 constexpr int kSmem = kOffWord + 16;
 static_assert(kSmem <= 232448, "shared memory");
@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   uint64_t* ofree = pvdone + 2;            // both outputs of a unit read
   uint64_t* xfull = ofree + 1;             // both streams' maxima and sums are there
   uint64_t* dbar = xfull + 1;              // products in flight when the CTA gives up
+  uint64_t* tfree = dbar + 1;              // [8] sparse: an Info may be written again
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + kOffWord);
   volatile int* abort = reinterpret_cast<volatile int*>(base + kOffWord + 4);
   int* start_req = reinterpret_cast<int*>(base + kOffDesc);                  // before the first unit
@@ -399,10 +400,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       bar_init(&full[i], 1);
       bar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kInfos; ++i) bar_init(&tfull[i], 1);
+    for (int i = 0; i < kInfos; ++i) {
+      bar_init(&tfull[i], 1);
+      bar_init(&tfree[i], 1);
+    }
     for (int i = 0; i < kDescs; ++i) {
       bar_init(&dfull[i], 1);
-      bar_init(&dempty[i], 2 + kSoftWarps);
+      bar_init(&dempty[i], (kSparse ? 3 : 2) + kSoftWarps);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&qfull[i], 1);
@@ -622,19 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       int quse[2] = {0, 0};  // loads of each Q tile
       int asked = 0;         // key and value tiles asked for
       bool ok = true;
-      auto load_pages = [&](int pg, int id, int j, int kvh, bool last) -> bool {
-        // pg: lanes' page numbers (cpt lanes), id: their ids
-        const bool good = pg >= 0 && pg < p.P && id >= 0 && id < p.pages;
-        const uint32_t have = __ballot_sync(0xFFFFFFFFu, good);
-        Info& x = info[tile % kInfos];
-        if (lane < 8) x.page[lane] = lane < cpt ? pg : -1;
-        if (lane == 0) {
-          x.j = j;
-          x.flags = (int)(have & ((1u << cpt) - 1u)) | (last ? kLast : 0);
-        }
-        __syncwarp();
-        if (lane == 0) bar_arrive(&tfull[tile % kInfos]);
-        const uint32_t row = good ? (uint32_t)id << p.shift : nowhere;
+      // the keys and values of a tile; row: the first rows of lanes' pages (cpt lanes)
+      auto load_tile = [&](uint32_t row, int kvh) -> bool {
         const int z = (int)__shfl_sync(0xFFFFFFFFu, row, chunk);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -645,6 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           if (half < 2) tma_load(box + st * kTileBytes, kv ? &L.v : &L.k, &full[st], half * 64, kvh, z);
           ++asked;
         }
+        // The stage of these values held the keys of two tiles before, whose scores
+        // came after the weights of two tiles before that: all have read the Infos up
+        // to there.
+        if (kSparse && lane == 0 && tile >= 5) bar_arrive(&tfree[(tile - 5) % kInfos]);
         ++tile;
         return true;
       };
@@ -664,8 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         if (lane == 0) bar_arrive(&dempty[ds]);
         if (u.stop) break;
         const int32_t* table = p.tables + (int64_t)u.r * p.P;
-        auto id_of = [&](int pg) { return pg >= 0 && pg < p.P ? table[pg] : -1; };
         if (!kSparse) {
+          auto id_of = [&](int pg) { return pg >= 0 && pg < p.P ? table[pg] : -1; };
           // ids 32 at a time, the next 32 on their way
           int at = u.j0 << L.log_cpt;
           int ids = id_of(at + lane), more = id_of(at + 32 + lane);
@@ -673,7 +670,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           int in = 0;
           for (int j = u.j0; ok && j < u.j1; ++j) {
             const int id = __shfl_sync(0xFFFFFFFFu, ids, in + chunk);
-            ok = load_pages(lane < cpt ? (j << L.log_cpt) + lane : -1, id, j, u.kvh, j == u.j1 - 1);
+            const bool good = lane < cpt && (j << L.log_cpt) + lane < p.P && id >= 0 && id < p.pages;
+            const uint32_t have = __ballot_sync(0xFFFFFFFFu, good);
+            if (lane == 0) {
+              info[tile % kInfos].j = j;
+              info[tile % kInfos].flags = (int)have | (j == u.j1 - 1 ? kLast : 0);
+              bar_arrive(&tfull[tile % kInfos]);
+            }
+            ok = load_tile(good ? (uint32_t)id << p.shift : nowhere, u.kvh);
             in += cpt;
             if (in == 32) {
               in = 0;
@@ -683,64 +687,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             }
           }
         } else {
-          // the union of up to 128 lists, smallest page first; a lane has four
-          int e[4], cur[4], nxt[4];
-          const int32_t* list[4] = {};
-          auto entry = [&](int i, int x) {
-            const int v = x < p.select ? list[i][x] : -1;
-            return v < 0 || v >= u.to ? kNever : v;
-          };
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = lane + 32 * i;
-            list[i] = p.idx + ((int64_t)(u.t0 + min(t, u.ntok - 1)) * p.kv_heads + u.kvh) * p.select;
-            e[i] = 0;
-            if (t >= u.ntok) {
-              e[i] = p.select;
-            } else if (u.from > 0) {
-              int lo = 0, hi = p.select;  // the first entry at or past `from`
-              while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                const int v = list[i][mid];
-                if (v >= 0 && v < u.from)
-                  lo = mid + 1;
-                else
-                  hi = mid;
-              }
-              e[i] = lo;
-            }
-            cur[i] = entry(i, e[i]);
-            nxt[i] = cur[i] == kNever ? kNever : entry(i, e[i] + 1);
-          }
           ok = load_q(singles++ & 1, u.kvh, u.t0);
-          auto least = [&]() {
-            return __reduce_min_sync(0xFFFFFFFFu, min(min(cur[0], cur[1]), min(cur[2], cur[3])));
+          // a tile's pages as the lists' warp has them, ids one tile ahead
+          auto id_in = [&](int t) {
+            const Info& x = info[t % kInfos];
+            return lane < cpt && x.flags >> lane & 1 ? table[x.page[lane]] : -1;
           };
-          int low = least();
-          auto pop_tile = [&]() {  // lane c < cpt: the c-th page of the next tile, or -1
-            int pg = -1;
-            for (int c = 0; c < cpt && low != kNever; ++c) {
-              if (lane == c) pg = low;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (cur[i] == low) {
-                  cur[i] = nxt[i];
-                  ++e[i];
-                  nxt[i] = cur[i] == kNever ? kNever : entry(i, e[i] + 1);
-                }
-              low = least();
-            }
-            return pg;
-          };
-          int pg = pop_tile();
-          int id = id_of(pg);
+          ok = ok && wait_all(&tfull[tile % kInfos], (tile / kInfos) & 1, abort);
+          int id = ok ? id_in(tile) : -1;
           while (ok) {
-            const bool last = low == kNever;
-            const int pg1 = last ? -1 : pop_tile();
-            const int id1 = id_of(pg1);
-            ok = load_pages(pg, id, 0, u.kvh, last);
+            const bool last = info[tile % kInfos].flags & kLast;
+            int id1 = -1;
+            if (!last) {
+              ok = wait_all(&tfull[(tile + 1) % kInfos], ((tile + 1) / kInfos) & 1, abort);
+              if (ok) id1 = id_in(tile + 1);
+            }
+            ok = ok && load_tile(id >= 0 ? (uint32_t)id << p.shift : nowhere, u.kvh);
             if (last) break;
-            pg = pg1;
             id = id1;
           }
         }
@@ -869,6 +832,88 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         if (elect_one()) mma_commit(dbar);
         __syncwarp();
         drain(dbar, 0);
+      }
+    } else if (warp == 11 && kSparse) {
+      // ---- lists: the pages of the tiles to come
+      const int cpt = 1 << L.log_cpt;
+      int tile = 0;
+      bool ok = true;
+      for (int units = 0; ok; ++units) {
+        const int ds = units % kDescs;
+        if (!wait_all(&dfull[ds], (units / kDescs) & 1, abort)) break;
+        const Desc u = desc[ds];
+        __syncwarp();
+        if (lane == 0) bar_arrive(&dempty[ds]);
+        if (u.stop) break;
+        const int32_t* table = p.tables + (int64_t)u.r * p.P;
+        auto id_of = [&](int pg) { return pg >= 0 && pg < p.P ? table[pg] : -1; };
+        // the union of up to 128 lists, smallest page first; a lane has four
+        int e[4], cur[4], nxt[4];
+        const int32_t* list[4] = {};
+        auto entry = [&](int i, int x) {
+          const int v = x < p.select ? list[i][x] : -1;
+          return v < 0 || v >= u.to ? kNever : v;
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = lane + 32 * i;
+          list[i] = p.idx + ((int64_t)(u.t0 + min(t, u.ntok - 1)) * p.kv_heads + u.kvh) * p.select;
+          e[i] = 0;
+          if (t >= u.ntok) {
+            e[i] = p.select;
+          } else if (u.from > 0) {
+            int lo = 0, hi = p.select;  // the first entry at or past `from`
+            while (lo < hi) {
+              const int mid = (lo + hi) / 2;
+              const int v = list[i][mid];
+              if (v >= 0 && v < u.from)
+                lo = mid + 1;
+              else
+                hi = mid;
+            }
+            e[i] = lo;
+          }
+          cur[i] = entry(i, e[i]);
+          nxt[i] = cur[i] == kNever ? kNever : entry(i, e[i] + 1);
+        }
+        auto least = [&]() {
+          return __reduce_min_sync(0xFFFFFFFFu, min(min(cur[0], cur[1]), min(cur[2], cur[3])));
+        };
+        int low = least();
+        auto pop_tile = [&]() {  // lane c < cpt: the c-th page of the next tile, or -1
+          int pg = -1;
+          for (int c = 0; c < cpt && low != kNever; ++c) {
+            if (lane == c) pg = low;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (cur[i] == low) {
+                cur[i] = nxt[i];
+                ++e[i];
+                nxt[i] = cur[i] == kNever ? kNever : entry(i, e[i] + 1);
+              }
+            low = least();
+          }
+          return pg;
+        };
+        int pg = pop_tile();
+        int id = id_of(pg);
+        while (ok) {
+          const bool last = low == kNever;
+          const int pg1 = last ? -1 : pop_tile();
+          const int id1 = id_of(pg1);
+          const bool good = pg >= 0 && pg < p.P && id >= 0 && id < p.pages;
+          const uint32_t have = __ballot_sync(0xFFFFFFFFu, good);
+          if (tile >= kInfos && !(ok = wait_all(&tfree[tile % kInfos], ((tile / kInfos) & 1) ^ 1, abort))) break;
+          Info& x = info[tile % kInfos];
+          if (lane < 8) x.page[lane] = lane < cpt ? pg : -1;
+          if (lane == 0) x.flags = (int)have | (last ? kLast : 0);
+          __syncwarp();
+          if (lane == 0) bar_arrive(&tfull[tile % kInfos]);
+          ++tile;
+          if (last) break;
+          pg = pg1;
+          id = id1;
+        }
       }
     }
     __syncwarp();
