@@ -45,16 +45,19 @@ constexpr int kStages = 5, kInfos = 8, kDescs = 2;
 constexpr int kOffKV = 2 * kTileBytes;  // after two Q tiles
 constexpr int kOffInfo = kOffKV + kStages * kTileBytes;
 struct Info {            // of one tile of positions
-  int32_t page[8];       // sparse: its pages, by number in the request (-1: none)
-  int32_t j;             // dense: the tile's number
+  union {
+    int32_t page[8];     // sparse: its pages, by number in the request (-1: none)
+    int32_t j;           // dense: the tile's number
+  };
   int32_t flags;         // bits 0-7: its pages that are there; bit 8: the last of the unit
+  uint32_t tokens[8];    // sparse: of each page the tokens that have it, a bit a token, 32 a word
 };
 constexpr int kLast = 256;
+constexpr int kTokenWords = 8;
 struct Desc {            // of one unit, or of a CTA's share of one
   int32_t stop, r, kvh, t0, ntok, pos0, pair, slot;  // slot: of the workspace, -1: a whole unit
   int32_t j0, j1;        // dense: tiles
   int32_t from, to;      // sparse: page numbers
-  int32_t spare[4];
 };
 constexpr int kOffDesc = kOffInfo + kInfos * (int)sizeof(Info);
 constexpr int kOffXch = kOffDesc + kDescs * (int)sizeof(Desc);  // [stream][row] maximum and sum
@@ -92,6 +95,7 @@ struct Launch {
   KvParams p;
   int32_t tpt;      // tokens a row tile
   int32_t log_cpt;  // log2 of pages a tile of positions
+  int32_t words;    // of 32 tokens, of a row tile's
   int32_t rows;     // of a slot of the workspace
   uint8_t* ws;      // [kMaxCtas] Cut, int32 CTAs with a share | sums | outputs
   int64_t ml_off, o_off;
@@ -850,10 +854,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         // the union of up to 128 lists, smallest page first; a lane has four
         int e[4], cur[4], nxt[4];
         const int32_t* list[4] = {};
-        auto entry = [&](int i, int x) {
-          const int v = x < p.select ? list[i][x] : -1;
-          return v < 0 || v >= u.to ? kNever : v;
-        };
+        // (a value is looked at one pop after it is asked for)
+        auto entry = [&](int i, int x) { return x < p.select ? list[i][x] : -1; };
+        auto page_of = [&](int v) { return v < 0 || v >= u.to ? kNever : v; };
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = lane + 32 * i;
@@ -873,24 +876,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             }
             e[i] = lo;
           }
-          cur[i] = entry(i, e[i]);
-          nxt[i] = cur[i] == kNever ? kNever : entry(i, e[i] + 1);
+          cur[i] = page_of(entry(i, e[i]));
+          nxt[i] = cur[i] == kNever ? -1 : entry(i, e[i] + 1);
         }
         auto least = [&]() {
           return __reduce_min_sync(0xFFFFFFFFu, min(min(cur[0], cur[1]), min(cur[2], cur[3])));
         };
         int low = least();
+        uint32_t has = 0;        // lane c * words + i: tokens 32 i .. of the c-th page
         auto pop_tile = [&]() {  // lane c < cpt: the c-th page of the next tile, or -1
           int pg = -1;
+          has = 0;
           for (int c = 0; c < cpt && low != kNever; ++c) {
             if (lane == c) pg = low;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (cur[i] == low) {
-                cur[i] = nxt[i];
+            for (int i = 0; i < 4; ++i) {
+              if (i >= L.words) break;
+              const bool mine = cur[i] == low;
+              const uint32_t all = __ballot_sync(0xFFFFFFFFu, mine);
+              if (lane == c * L.words + i) has = all;
+              if (mine) {
+                cur[i] = page_of(nxt[i]);
                 ++e[i];
-                nxt[i] = cur[i] == kNever ? kNever : entry(i, e[i] + 1);
+                nxt[i] = cur[i] == kNever ? -1 : entry(i, e[i] + 1);
               }
+            }
             low = least();
           }
           return pg;
@@ -899,6 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         int id = id_of(pg);
         while (ok) {
           const bool last = low == kNever;
+          const uint32_t had = has;
           const int pg1 = last ? -1 : pop_tile();
           const int id1 = id_of(pg1);
           const bool good = pg >= 0 && pg < p.P && id >= 0 && id < p.pages;
@@ -906,6 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           if (tile >= kInfos && !(ok = wait_all(&tfree[tile % kInfos], ((tile / kInfos) & 1) ^ 1, abort))) break;
           Info& x = info[tile % kInfos];
           if (lane < 8) x.page[lane] = lane < cpt ? pg : -1;
+          if (lane < kTokenWords) x.tokens[lane] = had;
           if (lane == 0) x.flags = (int)have | (last ? kLast : 0);
           __syncwarp();
           if (lane == 0) bar_arrive(&tfull[tile % kInfos]);
@@ -946,29 +958,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // a row of no token: nothing of it is masked, nor kept
       const int pos = !real ? kNever : pos0 < 0 ? -1 : pos0 + mytok;
       const int own = pos < 0 ? -1 : pos >> p.shift, own_bits = (pos & (p.page - 1)) + 1;  // its page, positions in it
-      // sparse: where the row's list stands
-      const int32_t* list = nullptr;
-      int e = 0, want = kNever, next = kNever;
-      auto entry = [&](int x) {
-        const int v = x < p.select ? list[x] : -1;
-        return v < 0 ? kNever : v;
-      };
-      if (kSparse && real) {
-        list = p.idx + ((int64_t)t * p.kv_heads + kvh) * p.select;
-        if (from > 0) {
-          int hi = p.select;
-          while (e < hi) {
-            const int mid = (e + hi) / 2;
-            const int v = list[mid];
-            if (v >= 0 && v < from)
-              e = mid + 1;
-            else
-              hi = mid;
-          }
-        }
-        want = entry(e);
-        next = entry(e + 1);
-      }
       float m_used = -INFINITY, l = 0.f;
       bool ok = true, first = true;
       int had = 0;  // streams that had a step
@@ -980,18 +969,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         const Info& x = info[tile % kInfos];
         const int flags = x.flags;
         last = flags & kLast;
+        const int who = pair ? me : turn;  // whose step this tile is
+        if (pair) {
+          had = 3;
+        } else {
+          turn ^= 1;
+          had |= 1 << who;
+          if (who != me) continue;
+        }
         uint32_t words[4] = {0u, 0u, 0u, 0u};  // the positions that the row attends to
         if (kSparse) {
           const int cpt = 1 << L.log_cpt;
           for (int c = 0; c < cpt; ++c) {
             const int pg = x.page[c];
-            if (pg < 0 || (real && pg != want)) continue;
-            if (real) {
-              want = next;
-              ++e;
-              next = want == kNever ? kNever : entry(e + 1);
-            }
-            if (!(flags >> c & 1)) continue;
+            if (!(flags >> c & 1) || (real && !(x.tokens[c * L.words + (tok >> 5)] >> (tok & 31) & 1u))) continue;
             // positions of the page up to the row's own
             const int bits = pg > own ? 0 : pg < own ? p.page : own_bits;
             const int a = c * p.page;
@@ -1033,14 +1024,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             some |= (uint32_t)(g != 0u && g != 0xFFFFu) << i;
           }
           some = __reduce_or_sync(0xFFFFFFFFu, some);
-        }
-        const int who = pair ? me : turn;  // whose step this tile is
-        if (pair) {
-          had = 3;
-        } else {
-          turn ^= 1;
-          had |= 1 << who;
-          if (who != me) continue;
         }
         if (!wait_all(&sfull[me], count++ & 1, abort)) {
           ok = false;
@@ -1416,12 +1399,20 @@ int device_sms() {
   return 0;
 }
 
+// Tokens a row tile: 128 rows of them.  Of a selection no more than an Info's words
+// hold, a bit a token and page of the tile: pages of 32 and less with one or two heads
+// a group have tiles that are not full.
+int32_t tokens_a_tile(const dsa_kv_cfg* cfg, int32_t n, int32_t select) {
+  const int32_t full = 128 / n;
+  return select ? std::min(full, 32 * kTokenWords * cfg->page_size / 128) : full;
+}
+
 // The workspace and the grid, from the shapes: as many CTAs as there may be shares
 // of kLeast, an SM each.
 Sizes sizes_of(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests, int32_t table_width,
                int32_t select, int32_t sms) {
   Sizes s;
-  const int64_t n = heads / cfg->kv_heads, tpt = 128 / n, tpu = select ? tpt : 2 * tpt;
+  const int64_t n = heads / cfg->kv_heads, tpt = tokens_a_tile(cfg, (int32_t)n, select), tpu = select ? tpt : 2 * tpt;
   const int64_t units = (std::min(tokens, requests) + tokens / tpu) * cfg->kv_heads;
   const int64_t keys = select ? (int64_t)select * cfg->page_size : (int64_t)table_width * cfg->page_size;
   const int64_t most = units * (keys + kUnitCost) / kLeast;
@@ -1519,7 +1510,8 @@ int attend(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t request
   p.flip = c < 0.f;
   // not 0: a masked score of -inf times it stays -inf
   p.c2 = std::max(c < 0.f ? -c : c, 1.17549435e-38f);
-  L.tpt = 128 / p.n;
+  L.tpt = tokens_a_tile(cfg, p.n, select);
+  L.words = (L.tpt + 31) / 32;
   L.log_cpt = 7 - p.shift;
   L.rows = sz.rows;
   L.ws = static_cast<uint8_t*>(workspace);
