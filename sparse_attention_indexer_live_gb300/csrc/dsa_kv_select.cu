@@ -57,11 +57,39 @@ __device__ __forceinline__ float2 scale_of(float top) {
   return make_float2(pow2f(e / 2), pow2f(e - e / 2));
 }
 
+// The larger of two pairs' absolute values; of a NaN and a number the number.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  a &= 0x7FFF7FFFu;
+  b &= 0x7FFF7FFFu;
+  if (kBf16)
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// d += A B, 16 x 16 by 16 x 8
+template <bool kBf16>
+__device__ __forceinline__ void mma_sync(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if (kBf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // Scores of up to 128 tokens of one request and key/value head against its pages.
 // The score is linear in q, so the group's heads are summed first, and the sum is
-// scaled by a power of two a row (which no rank sees).  More than eight tokens: on
-// the tensor cores, the sum as the nearest 16-bit numbers and what they leave, 2 x
-// 128 products a page; fewer: in fp32, a page a lane.  A score is off by at most
+// scaled by a power of two a row (which no rank sees).  The products are the tensor
+// cores', the sum taken as the nearest 16-bit numbers and what they leave, 2 x 128
+// products a page: tcgen05 on 128 tokens and tiles of pages in shared memory, and up to
+// eight tokens mma.sync on pages in registers, each read once and by one warp (in fp32
+// on the CUDA cores 32 pages took a warp 5,000 cycles, the reads of them 1,200).  A score is off by at most
 // 2^-14.5 |q| |mean|, |q| the norm of the heads' absolute sums: 2^-18 for what the two
 // parts leave, 2^-17 for the sum of 128 heads, 2^-15 for 256 sums in fp32; row_norm
 // and norms let the next kernel know it.  A score that is not finite, of a page
@@ -175,80 +203,88 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
           make_float4(f[0] * mul.x * mul.y, f[1] * mul.x * mul.y, f[2] * mul.x * mul.y, f[3] * mul.x * mul.y);
     }
     __syncthreads();
-    // 32 pages a warp at a time, four lanes a page: chunks c, c + 4, .. of eight dims,
-    // so that a load instruction takes whole sectors
+    // 32 pages a warp at a time, four lanes a page: lane c of them has chunks c, c + 4, ..
+    // of eight dims, so that a load instruction takes whole sectors.  What a lane has of
+    // its pages are its parts of mma's A (the order of the dims is free, as long as B's
+    // is the same); B is the sums of eight tokens, what is not a token's has no reader.
     const int c = lane & 3;
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(sums + (lane >> 2) * kKvDim + 32 * (i >> 1) + 8 * c + 4 * (i & 1));
+      hi[2 * i] = pair_of<kBf16>(x.x, x.y);
+      hi[2 * i + 1] = pair_of<kBf16>(x.z, x.w);
+      const float2 y0 = pair_f32<kBf16>(hi[2 * i]), y1 = pair_f32<kBf16>(hi[2 * i + 1]);
+      lo[2 * i] = pair_of<kBf16>(x.x - y0.x, x.y - y0.y);
+      lo[2 * i + 1] = pair_of<kBf16>(x.z - y1.x, x.w - y1.y);
+    }
     auto id_at = [&](int x) {
       const int j = 32 * x + 8 * c + (lane >> 2);
       return j < end ? table[j] : -1;
     };
     for (int x = split * 8 + warp, next_id = first_id; x < 2 * tiles; x += 8 * p.splits) {
-      const int own_j = 32 * x + 8 * c + (lane >> 2);  // the page this lane writes
       const int own_id = next_id;
       next_id = id_at(x + 8 * p.splits);
       Eight e[4][4];
-      float norm = 0.f;
+      bool there[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {  // pages 8 g + lane / 4
         const int id = __shfl_sync(0xFFFFFFFFu, own_id, (lane & ~3) + g);
-        const bool ok = id >= 0 && id < p.pages;
-        const char* src = static_cast<const char*>(p.means) + 2 * (((int64_t)(ok ? id : 0) * p.kv_heads + head) * kKvDim + 8 * c);
+        there[g] = id >= 0 && id < p.pages;
+        const char* src =
+            static_cast<const char*>(p.means) + 2 * (((int64_t)(there[g] ? id : 0) * p.kv_heads + head) * kKvDim + 8 * c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[g][i] = ok ? load8(src + 64 * i) : Eight{{0u, 0u, 0u, 0u}};
+        for (int i = 0; i < 4; ++i) e[g][i] = there[g] ? load8(src + 64 * i) : Eight{{0u, 0u, 0u, 0u}};
       }
+      // A bound of the largest norm: of a lane's dims the largest sum over its pages, of
+      // eight dims no more than eight times the largest square.
+      float norm = 0.f;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         float n2 = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float v[8];
-          unpack8<kBf16>(e[g][i], v);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) n2 = fmaf(v[k], v[k], n2);
+          const float2 y = pair_f32<kBf16>(abs_max2<kBf16>(abs_max2<kBf16>(e[g][i].w[0], e[g][i].w[1]),
+                                                           abs_max2<kBf16>(e[g][i].w[2], e[g][i].w[3])));
+          const float top = fmaxf(y.x, y.y);
+          n2 = fmaf(8.f * top, top, n2);
         }
-        n2 += __shfl_xor_sync(0xFFFFFFFFu, n2, 1);
-        n2 += __shfl_xor_sync(0xFFFFFFFFu, n2, 2);
         norm = fmaxf(norm, n2);
       }
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) norm = fmaxf(norm, __shfl_xor_sync(0xFFFFFFFFu, norm, o));
+      norm += __shfl_xor_sync(0xFFFFFFFFu, norm, 1);
+      norm += __shfl_xor_sync(0xFFFFFFFFu, norm, 2);
       if (lane == 0) norms[x] = sqrtf(norm);
-#pragma unroll 1
-      for (int t = a; t < b; ++t) {
-        const float* q = sums + (t - a) * kKvDim + 8 * c;
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+      // d[h]: pages 16 h + lane / 4 and 8 more, tokens 2 c and one more
+      float d[2][4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 x0 = *reinterpret_cast<const float4*>(q + 32 * i), x1 = *reinterpret_cast<const float4*>(q + 32 * i + 4);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float v[8];
-            unpack8<kBf16>(e[g][i], v);
-            d[g] = fmaf(v[0], x0.x, d[g]);
-            d[g] = fmaf(v[1], x0.y, d[g]);
-            d[g] = fmaf(v[2], x0.z, d[g]);
-            d[g] = fmaf(v[3], x0.w, d[g]);
-            d[g] = fmaf(v[4], x1.x, d[g]);
-            d[g] = fmaf(v[5], x1.y, d[g]);
-            d[g] = fmaf(v[6], x1.z, d[g]);
-            d[g] = fmaf(v[7], x1.w, d[g]);
-          }
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t* w0 = &e[2 * h][i >> 1].w[2 * (i & 1)];
+          const uint32_t* w1 = &e[2 * h + 1][i >> 1].w[2 * (i & 1)];
+          mma_sync<kBf16>(d[h], w0[0], w1[0], w0[1], w1[1], hi[2 * i], hi[2 * i + 1]);
+          mma_sync<kBf16>(d[h], w0[0], w1[0], w0[1], w1[1], lo[2 * i], lo[2 * i + 1]);
         }
-        float mine = 0.f;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          d[g] += __shfl_xor_sync(0xFFFFFFFFu, d[g], 1);
-          d[g] += __shfl_xor_sync(0xFFFFFFFFu, d[g], 2);
-          if (c == g) mine = d[g];
-        }
-        if (own_id < 0 || own_id >= p.pages) mine = __int_as_float(0x7FFFFFFF);
+      for (int k = 0; k < 2; ++k) {  // the lane's tokens
+        const int t = a + 2 * c + k, until = t < b ? end_of(t) : 0;
         const int64_t row = row0 + (int64_t)(t - a) * p.kv_heads;
-        p.scores[row * p.tiles * kScorePages + own_j] = mine;
-        float top = own_j < p.lead || own_j >= end_of(t) ? -INFINITY : fabsf(mine) < INFINITY ? mine : INFINITY;
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        if ((lane & ~2) == 0) p.tops[row * p.tiles * 4 + 2 * x + (lane >> 1)] = top;
+        for (int h = 0; h < 2; ++h) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int j = 32 * x + 16 * h + 8 * g + (lane >> 2);
+            const float y = there[2 * h + g] ? d[h][2 * g + k] : __int_as_float(0x7FFFFFFF);
+            if (t < b) p.scores[row * p.tiles * kScorePages + j] = y;
+            if (j >= p.lead && j < until) top = fmaxf(top, fabsf(y) < INFINITY ? y : INFINITY);
+          }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          if (lane < 4 && t < b) p.tops[row * p.tiles * 4 + 2 * x + h] = top;
+        }
       }
     }
     return;
