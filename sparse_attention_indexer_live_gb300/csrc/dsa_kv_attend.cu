@@ -28,6 +28,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dsa_kv_mma.h"
 
@@ -69,8 +70,10 @@ constexpr int kSmem = kOffWord + 16;
 static_assert(kSmem <= 232448, "shared memory");
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;  // S (and P) at 0 and 128, O at 256 and 384
 constexpr int kNever = 0x7FFFFFFF;                 // past every page number
-// A unit costs this many positions besides its own; a CTA takes no share below
-// kLeast; a cut less than kSnap tiles from a unit's end moves there.
+// A unit costs this many positions besides its own (one of two row tiles as much as
+// one of one: 31 decode requests beside three prompts take 143 us so, 168 at costs of
+// 3 : 2 and 149 at 2 : 3); a CTA takes no share below kLeast; a cut less than kSnap
+// tiles from a unit's end moves there.
 constexpr int kUnitCost = 256;
 constexpr int kLeast = 512;
 constexpr int kSnap = 2;
@@ -1298,8 +1301,49 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launc
         make_uint2(pair_of<kBf16>(o.x * inv, o.y * inv), pair_of<kBf16>(o.z * inv, o.w * inv));
     if (lane == 0) p.lse[out] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
   };
-  // As many warps a row as there are four shares for, 1 to 8, each every `split`-th.
-  int split = 1;
+  // Few shares: all of a row's by a warp at once, and of 8 / kShares rows together.
+  auto few = [&](auto shares) {
+    constexpr int kShares = decltype(shares)::value, kRows = 8 / kShares;
+    for (int r0 = 8 * kRows * (int)blockIdx.y; r0 < rows; r0 += 8 * kRows * (int)gridDim.y) {
+      float2 y[kRows][kShares];
+      float4 o[kRows][kShares];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int r = min(r0 + 8 * k + warp, rows - 1);
+#pragma unroll
+        for (int x = 0; x < kShares; ++x) {
+          const int slot = x < n ? slots[x] : -1;
+          const int64_t at = (int64_t)slot * L.rows + r;
+          y[k][x] = slot < 0 ? make_float2(-INFINITY, 0.f) : ml[at];
+          o[k][x] = slot < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : po[at * 32 + lane];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        float m = y[k][0].x;
+#pragma unroll
+        for (int x = 1; x < kShares; ++x) m = fmaxf(m, y[k][x].x);
+        if (m == -INFINITY) m = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+#pragma unroll
+        for (int x = 0; x < kShares; ++x) {
+          if (y[k][x].y == 0.f) continue;  // nothing attended to
+          const float a = ex2(y[k][x].x - m);
+          l += a * y[k][x].y;
+          acc.x += a * o[k][x].x;
+          acc.y += a * o[k][x].y;
+          acc.z += a * o[k][x].z;
+          acc.w += a * o[k][x].w;
+        }
+        finish(r0 + 8 * k + warp, m, l, acc);
+      }
+    }
+  };
+  if (n <= 2) return few(std::integral_constant<int, 2>());
+  if (n <= 4) return few(std::integral_constant<int, 4>());
+  // As many warps a row as there are four shares for, 2 to 8, each every `split`-th.
+  int split = 2;
   while (split < 8 && n > 4 * split) split *= 2;
   const int rows_at = 8 / split, part_of = warp % split, mine = warp / split;
   for (int r0 = rows_at * (int)blockIdx.y; r0 < rows; r0 += rows_at * gridDim.y) {
@@ -1333,10 +1377,6 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launc
         acc.z += a * o[i].z;
         acc.w += a * o[i].w;
       }
-    }
-    if (split == 1) {
-      finish(r0 + mine, m, l, acc);
-      continue;
     }
     *reinterpret_cast<float4*>(&part[warp][4 * lane]) = acc;
     if (lane == 0) part_l[warp] = l;
