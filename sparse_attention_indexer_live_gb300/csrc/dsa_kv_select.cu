@@ -37,7 +37,10 @@ struct SelectParams {
   const void *means, *q;
   const int32_t *first, *lens, *tables;
   int32_t* idx;
-  float* scores;    // [tokens in work, kv_heads, 64 tiles]
+  // [kv_heads, 4 tiles, tokens in work, 16]: side by side a warp's tokens are written in
+  // half lines (2,048 tokens take 64 us, 68 with each one's scores in a row of their own)
+  float* scores;
+  int64_t by_head, by_group;
   float* tops;      // [tokens in work, kv_heads, tiles, 4]: of 16 pages, those a token may take
   float* row_norm;  // [tokens in work, kv_heads]
   float* norms;     // [slots, kv_heads, tiles, 2]: of 32 pages
@@ -50,6 +53,11 @@ struct SelectParams {
 
 // The last page of a token at position pos (pages past the table: its last), or -1.
 __device__ __forceinline__ int own_page(int pos, int shift, int P) { return pos < 0 ? -1 : min(pos >> shift, P - 1); }
+
+// The scores of token t (of those in work): of its page j.
+__device__ __forceinline__ float* score_at(const SelectParams& p, int head, int t, int j) {
+  return p.scores + head * p.by_head + (int64_t)t * 16 + (j >> 4) * p.by_group + (j & 15);
+}
 
 // The power of two that brings a largest element of `top` to 2^14, in two factors.
 __device__ __forceinline__ float2 scale_of(float top) {
@@ -218,6 +226,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
       lo[2 * i] = pair_of<kBf16>(x.x - y0.x, x.y - y0.y);
       lo[2 * i + 1] = pair_of<kBf16>(x.z - y1.x, x.w - y1.y);
     }
+    float* const out = score_at(p, head, a - p.t0 + 2 * c, lane >> 2);
     auto id_at = [&](int x) {
       const int j = 32 * x + 8 * c + (lane >> 2);
       return j < end ? table[j] : -1;
@@ -274,11 +283,12 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float top = -INFINITY;
+          float* to = out + k * 16 + (int64_t)(2 * x + h) * p.by_group;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const int j = 32 * x + 16 * h + 8 * g + (lane >> 2);
             const float y = there[2 * h + g] ? d[h][2 * g + k] : __int_as_float(0x7FFFFFFF);
-            if (t < b) p.scores[row * p.tiles * kScorePages + j] = y;
+            if (t < b) to[8 * g] = y;
             if (j >= p.lead && j < until) top = fmaxf(top, fabsf(y) < INFINITY ? y : INFINITY);
           }
 #pragma unroll
@@ -366,7 +376,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
     const int row = threadIdx.x, t = a + row;
     const bool real = t < b;
     const int mine = real ? end_of(t) : 0;
-    float* out = p.scores + (row0 + (int64_t)row * p.kv_heads) * p.tiles * kScorePages;
+    float* const out = score_at(p, head, t - p.t0, 0);
     float4* out4 = reinterpret_cast<float4*>(p.tops) + (row0 + (int64_t)row * p.kv_heads) * p.tiles;
     int i = 0;
     for (int tile = split; tile < tiles; tile += p.splits, ++i) {
@@ -409,8 +419,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
       }
       if (real) {
 #pragma unroll
-        for (int k = 0; k < 64; k += 8)  // whole sectors
-          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + j0 + k), "r"(sc[k >> 5][k & 31]),
+        for (int k = 0; k < 64; k += 8)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + (4 * tile + k / 16) * p.by_group + k % 16), "r"(sc[k >> 5][k & 31]),
                        "r"(sc[k >> 5][(k & 31) + 1]), "r"(sc[k >> 5][(k & 31) + 2]), "r"(sc[k >> 5][(k & 31) + 3]),
                        "r"(sc[k >> 5][(k & 31) + 4]), "r"(sc[k >> 5][(k & 31) + 5]), "r"(sc[k >> 5][(k & 31) + 6]),
                        "r"(sc[k >> 5][(k & 31) + 7])
@@ -580,7 +590,8 @@ __global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(cons
   for (int i = tid; i < p.lead; i += kT) out[i] = i;
   for (int i = tid; i < p.trail; i += kT) out[p.select - p.trail + i] = end + i;
   if (m <= 0) return;
-  const float* scores = p.scores + ((int64_t)(t - p.t0) * p.kv_heads + head) * p.tiles * kScorePages;
+  const float* const scores = score_at(p, head, t - p.t0, 0);
+  auto score = [&](int j) { return scores + (j >> 4) * p.by_group + (j & 15); };
   const int32_t* table = p.tables + (int64_t)r * p.P;
   if (tid == 0) x.count = x.open = x.sure = 0;
   const int slot = t / kScoreTokens == rq.a / kScoreTokens ? r : p.R + (t - p.t0) / kScoreTokens;
@@ -618,7 +629,7 @@ __global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(cons
       for (int h = 0; h < 2; ++h) {
         const int j = j0 + 4 * kT * h;
         if (j >= end) break;
-        const float4 g = *reinterpret_cast<const float4*>(scores + j);
+        const float4 g = *reinterpret_cast<const float4*>(score(j));
         const float s[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -700,7 +711,7 @@ __global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(cons
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         j[u] = k0 + 2 * u < n16 ? 16 * x.groups[warp][k0 + 2 * u] + (lane & 15) : end;
-        v[u] = j[u] < end ? scores[j[u]] : 0.f;
+        v[u] = j[u] < end ? *score(j[u]) : 0.f;
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -844,7 +855,7 @@ __global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(cons
 // of the pages, those of each slot of score_kernel (each sees pages up to its last
 // token).
 struct SelectSizes {
-  int64_t tiles, tokens, top_off, norm_off, page_off, bytes;
+  int64_t tiles, tokens, held, top_off, norm_off, page_off, bytes;
 };
 SelectSizes select_sizes(const dsa_kv_cfg* cfg, int32_t tokens, int32_t requests, int32_t table_width) {
   SelectSizes s;
@@ -855,7 +866,7 @@ SelectSizes select_sizes(const dsa_kv_cfg* cfg, int32_t tokens, int32_t requests
   const int64_t most = std::max<int64_t>(1, kScoreBytes / row / kScoreTokens);
   const int64_t parts = std::max<int64_t>(1, (blocks + most - 1) / most);
   s.tokens = (blocks + parts - 1) / parts * kScoreTokens;
-  const int64_t held = std::min<int64_t>(s.tokens, tokens);
+  const int64_t held = s.held = std::min<int64_t>(s.tokens, tokens);
   s.top_off = fused_align16(held * row);
   s.norm_off = s.top_off + fused_align16(held * cfg->kv_heads * s.tiles * 16);
   s.page_off = s.norm_off + fused_align16(held * cfg->kv_heads * 4);
@@ -961,6 +972,8 @@ int dsa_kv_select(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t 
   p.lead = lead;
   p.trail = trail;
   p.tiles = (int32_t)sz.tiles;
+  p.by_head = sz.tiles * 4 * sz.held * 16;
+  p.by_group = sz.held * 16;
   for (int64_t t0 = 0; t0 < tokens; t0 += sz.tokens) {
     p.t0 = (int32_t)t0;
     p.t1 = (int32_t)std::min<int64_t>(tokens, t0 + sz.tokens);
