@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         ++d;
         return true;
       };
-      if (lane == 0 && has && blockIdx.x > 0 && x0 >= all) {  // nothing left for it
+      if (lane == 0 && has && blockIdx.x > 0) {  // (none, should nothing be left for it or the CTA give up)
         Cut c = {};
         c.r = -1;
         reinterpret_cast<Cut*>(L.ws)[blockIdx.x] = c;
