@@ -621,8 +621,11 @@ int dsa_kv_append(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t 
  *              zero.  Calls that may run at the same time need one each.
  * Scores, sums and outputs are held in f32; the softmax weights are rounded to
  * cfg's type for the second product.  What a row does not attend to -- later
- * positions, stale rows of a page -- has no effect on it, whatever it holds.
- * Results repeat bit for bit.
+ * positions, stale rows of a page -- has no effect on it, whatever it holds (but
+ * on the time: a row is computed a second time, by one warp, where a NaN or an
+ * infinity stands in a tile it attends to part of).  A NaN score makes a row's o
+ * and lse NaN, one of +infinity its o NaN and its lse +infinity.  Results repeat
+ * bit for bit.
  */
 int dsa_kv_attention_workspace(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests,
                                int32_t table_width, size_t* bytes);
@@ -640,7 +643,8 @@ int dsa_kv_attention(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32
  * the best, select pages in all (all there are, if fewer).
  *   idx     int32 [tokens, kv_heads, select]: page numbers within the request,
  *           ascending, then -1
- *   select  1 .. 256;  lead >= 0, trail >= 1, lead + trail <= select
+ *   select  1 .. 256;  lead >= 0, trail >= 1, lead + trail <= select.  The own page
+ *           of a position past the table is the table's last.
  *   workspace  as above, dsa_kv_select_workspace() bytes
  * Ranks are those of the scores in exact arithmetic (f64 where f32 cannot tell
  * two apart); among equal scores the lower page wins; a NaN score ranks below
@@ -669,7 +673,7 @@ int dsa_kv_block_attention(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads,
                            const int32_t* lens, const int32_t* tables, float scale, void* workspace,
                            size_t workspace_bytes, void* o, float* lse, struct CUstream_st* stream);
 
-/* DSA_ERR_TIMEOUT once after a launch of dsa_kv_attention or
+/* DSA_ERR_TIMEOUT once after a launch of dsa_kv_attention, dsa_kv_select or
  * dsa_kv_block_attention on the current device gave up a wait (then cleared),
  * else DSA_OK; synchronises the device, every stream of it. */
 int dsa_kv_status(void);

@@ -246,7 +246,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 // exponent, so a row whose sum or output is not finite may owe that to a position
 // that it does not attend to: such a row is computed again from those that it does.
 // (Without a selection: if one of the positions after its own, up to the end of the
-// unit's tiles, is to blame.)
+// unit's tiles, is to blame, or a score is infinite, which makes lse so.)
 struct Again {
   float4 o;
   float m, l;
@@ -284,8 +284,8 @@ struct RowAgain {
 #pragma unroll
         for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
         const float next = fmaxf(m, top);
-        base = next == -INFINITY ? 0.f : next;
-        const float alpha = m == -INFINITY ? 0.f : ex2(m - base);
+        base = fabsf(next) == INFINITY ? 0.f : next;  // (an infinite score's weight is infinite, as the sum then is)
+        const float alpha = m == -INFINITY ? 0.f : ex2((m == INFINITY ? 0.f : m) - base);
         m = next;
         l *= alpha;
 #pragma unroll
@@ -1224,7 +1224,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         const float rm = __shfl_sync(0xFFFFFFFFu, m, src), rs = __shfl_sync(0xFFFFFFFFu, sum, src);
         const bool whole_row = !(rs - rs == 0.f);  // its sum too
         const Share d = {req, kvh, jbeg, jend, from, to};
-        if (!kSparse && !odd_after<kBf16>(L, d, rp)) continue;
+        if (!kSparse && rm != INFINITY && !odd_after<kBf16>(L, d, rp)) continue;
         const Again y = row_again<kBf16, kSparse>(L, d, rt, kvh * p.n + rh, rp, whole_row ? __int_as_float(0x7FFFFFFF) : rm);
         const float rl = whole_row ? y.l : rs, top = whole_row ? y.m : rm;
         const int64_t at = (int64_t)rt * p.H + kvh * p.n + rh;
@@ -1323,7 +1323,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launc
         float m = y[k][0].x;
 #pragma unroll
         for (int x = 1; x < kShares; ++x) m = fmaxf(m, y[k][x].x);
-        if (m == -INFINITY) m = 0.f;
+        if (fabsf(m) == INFINITY) m = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float l = 0.f;
 #pragma unroll
@@ -1353,7 +1353,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Launc
       if (slots[x] >= 0) m = fmaxf(m, ml[(int64_t)slots[x] * L.rows + r].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (m == -INFINITY) m = 0.f;
+    if (fabsf(m) == INFINITY) m = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     for (int x0 = part_of; x0 < n; x0 += 8 * split) {
