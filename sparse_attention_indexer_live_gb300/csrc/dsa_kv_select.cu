@@ -867,7 +867,7 @@ SelectSizes select_sizes(const dsa_kv_cfg* cfg, int32_t tokens, int32_t requests
   const int64_t parts = std::max<int64_t>(1, (blocks + most - 1) / most);
   s.tokens = (blocks + parts - 1) / parts * kScoreTokens;
   const int64_t held = s.held = std::min<int64_t>(s.tokens, tokens);
-  s.top_off = fused_align16(held * row);
+  s.top_off = fused_align16(held * row);  // (row: a multiple of 256)
   s.norm_off = s.top_off + fused_align16(held * cfg->kv_heads * s.tiles * 16);
   s.page_off = s.norm_off + fused_align16(held * cfg->kv_heads * 4);
   s.bytes = s.page_off + fused_align16((requests + s.tokens / kScoreTokens) * cfg->kv_heads * s.tiles * 8) + 16;
@@ -953,7 +953,8 @@ int dsa_kv_select(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t 
   p.lens = lens;
   p.tables = tables;
   p.idx = idx;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  // (stores of 32 bytes: from its first multiple of 32, the 16 bytes more are in its size)
+  uint8_t* ws = reinterpret_cast<uint8_t*>(((uintptr_t)workspace + 31) & ~(uintptr_t)31);
   p.scores = reinterpret_cast<float*>(ws);
   p.tops = reinterpret_cast<float*>(ws + sz.top_off);
   p.row_norm = reinterpret_cast<float*>(ws + sz.norm_off);

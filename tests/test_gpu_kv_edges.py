@@ -14,7 +14,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tests import kv_ref as ref  # noqa: E402
-from tests.test_gpu_kv import BF16, F16, _append, _attend, _lists, _select  # noqa: E402
+from tests.test_gpu_kv import (BF16, F16, _all, _append, _attend, _copy, _dsa, _lists, _same, _select,  # noqa: E402
+                               _state)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
 
@@ -98,6 +99,27 @@ def test_select_for_drafts(new, dtype):
 def test_append_of_long_steps(lens, new, page, dtype):
     step = ref.Step(lens, new, H=8, Hk=2, page=page, dtype=dtype, seed=page, pad=2)
     _append(step, 8, 128, page == 16)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_memory_on_16_byte_boundaries(new):
+    """Everything a multiple of 16 bytes, and of no more, from an address of many."""
+    dsa = _dsa()
+    step = ref.Step([900, 2500], [new, 1], H=8, Hk=2, page=16, dtype=BF16, seed=41)
+
+    def odd(x):
+        y = torch.zeros(x.numel() + 16 // x.element_size(), dtype=x.dtype, device=x.device)[16 // x.element_size():]
+        assert y.data_ptr() % 32 == 16
+        return y.copy_(x.reshape(-1)).view(x.shape)
+    s, t = _state(step), _state(step)
+    for x in ("q", "kn", "vn", "k", "v", "means"):
+        t[x] = odd(s[x])
+    for x in ("qr", "o", "ob", "ws"):
+        t[x] = odd(t[x])
+    _all(step, s)
+    _all(step, t)
+    _same(_copy(s), _copy(t))
+    assert dsa.dsa_kv_status() == dsa.DSA_OK
 
 
 def test_first_calls_inside_a_capture():
