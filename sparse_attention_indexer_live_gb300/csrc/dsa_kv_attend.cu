@@ -868,8 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           if (t >= u.ntok) {
             e[i] = p.select;
           } else if (u.from > 0) {
-            int lo = 0, hi = p.select;  // the first entry at or past `from`
-            while (lo < hi) {
+            // the first entry at or past `from`: by halves to sixteen entries, those at once
+            int lo = 0, hi = p.select;
+            while (hi - lo > 16) {
               const int mid = (lo + hi) / 2;
               const int v = list[i][mid];
               if (v >= 0 && v < u.from)
@@ -877,7 +878,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               else
                 hi = mid;
             }
-            e[i] = lo;
+            int before = 0;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const int v = lo + x < hi ? list[i][lo + x] : -1;
+              before += v >= 0 && v < u.from;
+            }
+            e[i] = lo + before;
           }
           cur[i] = page_of(entry(i, e[i]));
           nxt[i] = cur[i] == kNever ? -1 : entry(i, e[i] + 1);
