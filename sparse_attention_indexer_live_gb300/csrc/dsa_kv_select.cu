@@ -549,6 +549,10 @@ struct Pick {
   int count, open, sure;
 };
 
+// Rows a CTA: few, so that a row that has to be settled in fp64 holds up no other.
+template <int W>
+constexpr int kPickRows = W == 1 ? 2 : 1;
+
 // The order of floats as unsigned numbers; no NaN.
 __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t u = __float_as_uint(x);
@@ -559,9 +563,9 @@ __device__ __forceinline__ float float_of(uint32_t o) {
 }
 
 template <bool kBf16, int W>
-__global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows<W> : 2) pick_kernel(const SelectParams p) {
   constexpr int kT = 32 * W;  // threads a row
-  __shared__ Pick<W> rows[kPickThreads / kT];
+  __shared__ Pick<W> rows[kPickRows<W>];
   let_next_start();
   wait_for_previous();
   const int tid = threadIdx.x % kT, warp = tid >> 5, lane = tid & 31;
@@ -572,7 +576,7 @@ __global__ void __launch_bounds__(kPickThreads, W == 1 ? 4 : 2) pick_kernel(cons
     else
       __syncthreads();
   };
-  const int64_t row_id = (int64_t)blockIdx.x * (kPickThreads / kT) + threadIdx.x / kT;
+  const int64_t row_id = (int64_t)blockIdx.x * kPickRows<W> + threadIdx.x / kT;
   const int t = (int)min((int64_t)p.t1, p.t0 + row_id / p.kv_heads), head = (int)(row_id % p.kv_heads);
   const int r = t < p.t1 ? request_of_token(p.first, p.R, t) : -1;
   if (r < 0) return;
@@ -1005,10 +1009,10 @@ int dsa_kv_select(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t 
     // lists are short; else eight
     const int64_t rows = (int64_t)(p.t1 - p.t0) * cfg->kv_heads;
     const bool one = select - lead - trail <= Pick<1>::kMost && rows >= 16 * (int64_t)sms && table_width <= 8192;
-    const int64_t blocks = one ? (rows + 7) / 8 : rows;
+    const int64_t blocks = one ? (rows + kPickRows<1> - 1) / kPickRows<1> : rows;
     if (one)
-      st = cfg->dtype == DSA_BF16 ? launch_dependent(pick_kernel<true, 1>, blocks, kPickThreads, 0, 0, stream, p)
-                                  : launch_dependent(pick_kernel<false, 1>, blocks, kPickThreads, 0, 0, stream, p);
+      st = cfg->dtype == DSA_BF16 ? launch_dependent(pick_kernel<true, 1>, blocks, 32 * kPickRows<1>, 0, 0, stream, p)
+                                  : launch_dependent(pick_kernel<false, 1>, blocks, 32 * kPickRows<1>, 0, 0, stream, p);
     else
       st = cfg->dtype == DSA_BF16 ? launch_dependent(pick_kernel<true, 8>, blocks, kPickThreads, 0, 0, stream, p)
                                   : launch_dependent(pick_kernel<false, 8>, blocks, kPickThreads, 0, 0, stream, p);
