@@ -21,9 +21,16 @@ struct AppendParams {
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kMeansWithin = 512;  // tokens
+// Means of up to this many tokens' pages are made beside the rows, in the same launch,
+// from the keys as they come (48 requests of two tokens take 3.3 us, 6.1 with a launch
+// more); of more they are read back from the cache, which holds them in the L2 by then,
+// so that the rows' kernel needs fewer registers (8,192 tokens 40.0 us, 55.8 in one
+// launch; 1,041 tokens 9.5 and 11.4).
+constexpr int kMeansWithin = 512;
+// Groups of four rows whose loads a warp has in flight (8,192 tokens: 42.0 us with one
+// fewer, 43.4 with one more).
 template <bool kMeans>
-constexpr int kAppendBatch = kMeans ? 3 : 2;  // groups of four rows whose loads a warp has in flight
+constexpr int kAppendBatch = kMeans ? 3 : 2;
 
 // One row is two 16-byte chunks in each of eight lanes.  Pairs of dims half a
 // rotation apart lie in chunks l and l + rotary / 16 of the same lane, neighbours
@@ -239,8 +246,11 @@ __global__ void __launch_bounds__(kAppendThreads) means_kernel(const AppendParam
 
 // Rows are dealt out four to a warp, so that a row is eight lanes with two
 // 16-byte loads each and the angles of a token are computed once for all its
-// rows that a warp takes.  Bound by HBM for prompt chunks; by latency for a
-// decode step, whose rows go to as many warps as there are groups of four.
+// rows that a warp takes, two a lane and handed on (sincospi is a tenth of the
+// instructions so).  Bound by HBM for prompt chunks: 8,192 tokens of 32 + 8 + 8 heads
+// move 202 MB in 40.0 us with their means, 0.75 of the copy rate (half the bytes are
+// writes, of which the L2 keeps some past the end).  Bound by latency for a decode
+// step, whose rows go to as many warps as there are groups of four: 3.3 us for 96 tokens.
 template <bool kBf16, bool kMeans>
 __global__ void __launch_bounds__(kAppendThreads, kMeans ? 1 : 4) append_kernel(const AppendParams p) {
   constexpr int kBatch = kAppendBatch<kMeans>;
