@@ -94,7 +94,7 @@ constexpr int kNever = 0x7FFFFFFF;                 // past every page number
 constexpr int kUnitCost = 256;
 constexpr int kLeast = 512;
 constexpr int kSnap = 2;
-constexpr int kMaxCtas = 1024;
+constexpr int kMaxCtas = 160;  // SMs that are made use of
 #ifdef DSA_KV_TEST_WAIT_CYCLES
 constexpr uint32_t kPArrivals = 129;  // one more than there are
 #else
