@@ -4,12 +4,13 @@
 // Two kernels: scores, approximate and with a bound of their error, into the
 // workspace; and the choice, which settles what the bound leaves open in fp64.
 //
-// 64 requests' tokens over up to 2,048 pages (58 MB of mean keys): 34 us, 8.5 by the
-// bytes.  The longest request's warps read eight lots of 32 pages one after another, then
-// the choice's chain follows.  2,048 tokens over 2,048 pages: 61 us.  67 MB of scores are
-// written and their best read back; scores 28 us (heads' sums 8, the rest bound by the
-// loaders' and writers' work on a tile), choice 26 us (15,000 cycles a row: tops, floor,
-// candidates, ranks; issue slots and latency alike).
+// 64 requests' tokens over up to 2,048 pages, 58 MB of mean keys that no cache holds: 42
+// us, 8.5 by the bytes.  The longest request's warps read eight lots of 32 pages, two on
+// their way into the L2 ahead of the one they load (46 us without, and 34 against 37 when
+// the L2 holds all of it); then the choice's chain follows, some 10 us.  2,048 tokens over
+// 2,048 pages: 60 us.  67 MB of scores are written and their best read back; scores 28 us
+// (heads' sums 8, the rest bound by the loaders' and writers' work on a tile), then the
+// choice (tops, floor, candidates, ranks; issue slots and latency alike).
 
 #include <algorithm>
 
@@ -182,8 +183,22 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
 
   if (b - a <= kFewTokens) {
     float* sums = reinterpret_cast<float*>(base);  // [8][128]
-    const int first_j = 32 * (split * 8 + warp) + 8 * (lane & 3) + (lane >> 2);
-    const int first_id = first_j < end ? table[first_j] : -1;
+    // a lane's page of the warp's lot x, and its row on its way into the L2
+    auto id_at = [&](int x) {
+      const int j = 32 * x + 8 * (lane & 3) + (lane >> 2);
+      return j < end ? table[j] : -1;
+    };
+    auto ask = [&](int id) {
+      if (id < 0 || id >= p.pages) return;
+      const char* row = static_cast<const char*>(p.means) + 2 * ((int64_t)id * p.kv_heads + head) * kKvDim;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 128));
+    };
+    const int x0 = split * 8 + warp, dx = 8 * p.splits;
+    const int first_id = id_at(x0);
+    int second_id = id_at(x0 + dx), third_id = id_at(x0 + 2 * dx);
+    ask(first_id);
+    ask(second_id);
     if (warp < b - a) {
       float f[4] = {}, m[4] = {};
       const char* src = static_cast<const char*>(p.q) + 2 * ((a + warp) * p.q_stride + head * p.n * kKvDim + 4 * lane);
@@ -223,26 +238,29 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
     // 32 pages a warp at a time, four lanes a page: lane c of them has chunks c, c + 4, ..
     // of eight dims, so that a load instruction takes whole sectors.  What a lane has of
     // its pages are its parts of mma's A (the order of the dims is free, as long as B's
-    // is the same); B is the sums of eight tokens, what is not a token's has no reader.
-    const int c = lane & 3;
-    uint32_t hi[16], lo[16];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 x = *reinterpret_cast<const float4*>(sums + (lane >> 2) * kKvDim + 32 * (i >> 1) + 8 * c + 4 * (i & 1));
-      hi[2 * i] = pair_of<kBf16>(x.x, x.y);
-      hi[2 * i + 1] = pair_of<kBf16>(x.z, x.w);
-      const float2 y0 = pair_f32<kBf16>(hi[2 * i]), y1 = pair_f32<kBf16>(hi[2 * i + 1]);
-      lo[2 * i] = pair_of<kBf16>(x.x - y0.x, x.y - y0.y);
-      lo[2 * i + 1] = pair_of<kBf16>(x.z - y1.x, x.w - y1.y);
-    }
-    float* const out = score_at(p, head, a - p.t0 + 2 * c, lane >> 2);
-    auto id_at = [&](int x) {
-      const int j = 32 * x + 8 * c + (lane >> 2);
-      return j < end ? table[j] : -1;
+    // is the same).  B's eight columns are four tokens' sums and what those left, so that
+    // up to four tokens take sixteen products a lot; eight have the others' columns made
+    // again for each lot (both in registers cost the loads their room: 53 us for 42).
+    const int c = lane & 3, many = (b - a + 3) / 4;
+    auto words = [&](int u, int i, uint32_t& b0, uint32_t& b1) {  // of B, of tokens 4 u ..
+      const float4 x =
+          *reinterpret_cast<const float4*>(sums + (4 * u + (lane >> 2 & 3)) * kKvDim + 32 * (i >> 1) + 8 * c + 4 * (i & 1));
+      b0 = pair_of<kBf16>(x.x, x.y);
+      b1 = pair_of<kBf16>(x.z, x.w);
+      const float2 y0 = pair_f32<kBf16>(b0), y1 = pair_f32<kBf16>(b1);
+      if (lane >= 16) {
+        b0 = pair_of<kBf16>(x.x - y0.x, x.y - y0.y);
+        b1 = pair_of<kBf16>(x.z - y1.x, x.w - y1.y);
+      }
     };
-    for (int x = split * 8 + warp, next_id = first_id; x < 2 * tiles; x += 8 * p.splits) {
-      const int own_id = next_id;
-      next_id = id_at(x + 8 * p.splits);
+    uint32_t bw[16];  // of the first four; the others' are made again for each lot
+#pragma unroll
+    for (int i = 0; i < 8; ++i) words(0, i, bw[2 * i], bw[2 * i + 1]);
+    const int half = c >> 1;  // the 16 of 32 pages whose scores the lane writes, of tokens 4 u + mine and one more
+    const int mine = 2 * (c & 1);
+    float* const out = score_at(p, head, a - p.t0 + mine, lane >> 2);
+    for (int x = x0, own_id = first_id; x < 2 * tiles; x += dx) {
+      ask(third_id);
       Eight e[4][4];
       bool there[4];
 #pragma unroll
@@ -254,6 +272,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[g][i] = there[g] ? load8(src + 64 * i) : Eight{{0u, 0u, 0u, 0u}};
       }
+      own_id = second_id;
+      second_id = third_id;
+      third_id = id_at(x + 3 * dx);
       // A bound of the largest norm: of a lane's dims the largest sum over its pages, of
       // eight dims no more than eight times the largest square.
       float norm = 0.f;
@@ -274,35 +295,39 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
       norm += __shfl_xor_sync(0xFFFFFFFFu, norm, 1);
       norm += __shfl_xor_sync(0xFFFFFFFFu, norm, 2);
       if (lane == 0) norms[x] = sqrtf(norm);
-      // d[h]: pages 16 h + lane / 4 and 8 more, tokens 2 c and one more
-      float d[2][4] = {};
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
+#pragma unroll 1
+      for (int u = 0; u < many; ++u) {
+        // d[h]: pages 16 h + lane / 4 and 8 more; columns 2 c and one more
+        float d[2][4] = {};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t* w0 = &e[2 * h][i >> 1].w[2 * (i & 1)];
-          const uint32_t* w1 = &e[2 * h + 1][i >> 1].w[2 * (i & 1)];
-          mma_sync<kBf16>(d[h], w0[0], w1[0], w0[1], w1[1], hi[2 * i], hi[2 * i + 1]);
-          mma_sync<kBf16>(d[h], w0[0], w1[0], w0[1], w1[1], lo[2 * i], lo[2 * i + 1]);
+          uint32_t b0 = bw[2 * i], b1 = bw[2 * i + 1];
+          if (u) words(u, i, b0, b1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t* w0 = &e[2 * h][i >> 1].w[2 * (i & 1)];
+            const uint32_t* w1 = &e[2 * h + 1][i >> 1].w[2 * (i & 1)];
+            mma_sync<kBf16>(d[h], w0[0], w1[0], w0[1], w1[1], b0, b1);
+          }
         }
+        float y[4];  // both parts' sum
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {  // the lane's tokens
-        const int t = a + 2 * c + k, until = t < b ? end_of(t) : 0;
-        const int64_t row = row0 + (int64_t)(t - a) * p.kv_heads;
+        for (int k = 0; k < 4; ++k) y[k] = (half ? d[1][k] : d[0][k]) + __shfl_xor_sync(0xFFFFFFFFu, half ? d[0][k] : d[1][k], 2);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int k = 0; k < 2; ++k) {  // the lane's tokens
+          const int t = a + 4 * u + mine + k, until = t < b ? end_of(t) : 0;
           float top = -INFINITY;
-          float* to = out + k * 16 + (int64_t)(2 * x + h) * p.by_group;
+          float* to = out + (4 * u + k) * 16 + (int64_t)(2 * x + half) * p.by_group;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const int j = 32 * x + 16 * h + 8 * g + (lane >> 2);
-            const float y = there[2 * h + g] ? d[h][2 * g + k] : __int_as_float(0x7FFFFFFF);
-            if (t < b) to[8 * g] = y;
-            if (j >= p.lead && j < until) top = fmaxf(top, fabsf(y) < INFINITY ? y : INFINITY);
+            const int j = 32 * x + 16 * half + 8 * g + (lane >> 2);
+            const float s = (half ? there[2 + g] : there[g]) ? y[2 * g + k] : __int_as_float(0x7FFFFFFF);
+            if (t < b) to[8 * g] = s;
+            if (j >= p.lead && j < until) top = fmaxf(top, fabsf(s) < INFINITY ? s : INFINITY);
           }
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-          if (lane < 4 && t < b) p.tops[row * p.tiles * 4 + 2 * x + h] = top;
+          if (lane < 4 && t < b) p.tops[(row0 + (int64_t)(t - a) * p.kv_heads) * p.tiles * 4 + 2 * x + half] = top;
         }
       }
     }
@@ -575,6 +600,7 @@ __device__ __forceinline__ float float_of(uint32_t o) {
 template <bool kBf16, int W>
 __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows<W> : 2) pick_kernel(const SelectParams p) {
   constexpr int kT = 32 * W;  // threads a row
+  constexpr int kAhead = 4;   // groups whose scores a half warp reads at once
   __shared__ Pick<W> rows[kPickRows<W>];
   let_next_start();
   wait_for_previous();
@@ -673,9 +699,21 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
   // more than 2^-14.5 of the norms, and of what their squares may have lost below 2^-126
   const float e = norm * row_norm * 4.4e-5f + 0x1p-50f;
   auto fine = [&](float s) { return fabsf(s) < INFINITY && e < INFINITY; };
-  // a floor that m of the 256 reach, and few more: by halves between their extremes
+  // a floor that m of the 256 reach, and few more: few, the m-th of the lanes' largest;
+  // else by halves between their extremes
   float least;
-  {
+  if (m <= 32) {
+    float v = best[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v = fmaxf(v, best[i]);
+    int above = 0;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float y = __shfl_sync(0xFFFFFFFFu, v, k);
+      above += y > v || (y == v && k < lane);
+    }
+    least = __shfl_sync(0xFFFFFFFFu, v, __ffs(__ballot_sync(0xFFFFFFFFu, above == m - 1)) - 1) - e;
+  } else {
     uint32_t o[8], hi = 0, lo = 0xFFFFFFFFu;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -700,11 +738,13 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
     }
     least = float_of(lo) - e;  // (all bounds are as far below)
   }
-  // the groups that may reach it, 32 tiles of a warp at a time, and their pages
-  for (int i0 = 32 * warp; i0 < tiles; i0 += 32 * W) {
+  // the groups that may reach it, 32 tiles of a warp at a time (warps' in turn), and
+  // their pages
+  for (int i0 = warp; i0 < tiles; i0 += 32 * W) {
     float s[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    if (i0 + lane < tiles) {
-      const float4 g = top4[i0 + lane];
+    const int tile = i0 + lane * W;
+    if (tile < tiles) {
+      const float4 g = top4[tile];
       s[0] = g.x;
       s[1] = g.y;
       s[2] = g.z;
@@ -715,20 +755,20 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
     for (int u = 0; u < 4; ++u) {
       const bool in = s[u] > -INFINITY && (!fine(s[u]) || s[u] + e >= least);
       const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-      if (in) x.groups[warp][n16 + __popc(who & ((1u << lane) - 1u))] = 4 * (i0 + lane) + u;
+      if (in) x.groups[warp][n16 + __popc(who & ((1u << lane) - 1u))] = 4 * tile + u;
       n16 += __popc(who);
     }
     __syncwarp();
-    for (int k0 = lane >> 4; k0 - (lane >> 4) < n16; k0 += 8) {
-      int j[4];
-      float v[4];
+    for (int k0 = lane >> 4; k0 - (lane >> 4) < n16; k0 += 2 * kAhead) {
+      int j[kAhead];
+      float v[kAhead];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         j[u] = k0 + 2 * u < n16 ? 16 * x.groups[warp][k0 + 2 * u] + (lane & 15) : end;
         v[u] = j[u] < end ? *score(j[u]) : 0.f;
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < kAhead; ++u)
         if (is_free(j[u]) && (!fine(v[u]) || v[u] + e >= least)) {
           const int at = atomicAdd(&x.count, 1);
           if (at < Pick<W>::kList) {
@@ -743,23 +783,25 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
   const int count = x.count;
   // the group's sum in fp64, when a score has to be told exactly
   auto sum_heads = [&]() {
-    for (int d = tid; d < kKvDim / 2; d += kT) {
-      double y = 0.0, z = 0.0;
-      const char* src = static_cast<const char*>(p.q) + 2 * (t * p.q_stride + head * p.n * kKvDim + 2 * d);
+    if (tid < kKvDim / 4) {
+      double y[4] = {};
+      const char* src = static_cast<const char*>(p.q) + 2 * (t * p.q_stride + head * p.n * kKvDim + 4 * tid);
       for (int h0 = 0; h0 < p.n; h0 += 8) {
-        uint32_t w[8];
+        uint2 w[8];
 #pragma unroll
         for (int h = 0; h < 8; ++h)
-          w[h] = h0 + h < p.n ? *reinterpret_cast<const uint32_t*>(src + 2 * (h0 + h) * kKvDim) : 0u;
+          w[h] = h0 + h < p.n ? *reinterpret_cast<const uint2*>(src + 2 * (h0 + h) * kKvDim) : make_uint2(0u, 0u);
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
-          const float2 g = pair_f32<kBf16>(w[h]);
-          y += (double)g.x;
-          z += (double)g.y;
+          const float2 f = pair_f32<kBf16>(w[h].x), g = pair_f32<kBf16>(w[h].y);
+          y[0] += (double)f.x;
+          y[1] += (double)f.y;
+          y[2] += (double)g.x;
+          y[3] += (double)g.y;
         }
       }
-      x.qs[2 * d] = y;
-      x.qs[2 * d + 1] = z;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.qs[4 * tid + i] = y[i];
     }
     sync();
   };
