@@ -26,9 +26,10 @@
 // What bounds it, 32 heads on 8 unless said otherwise:
 //   * single tokens: HBM.  64 requests of up to 16K positions 281 us, 1.83 GB at 0.95 of
 //     the copy rate;
-//   * one token of 128K positions, 8 heads on 1 (67 MB, 9.9 us): 23.3 us.  6 us to the
-//     first scores (launch, shares, lengths, first tile), six tiles an SM, their join;
-//   * chunks: 4,096 tokens over 32K positions 1,337 us, 1.54 PFLOP/s of the 1.98 that a
+//   * one token of 128K positions, 8 heads on 1 (67 MB, 9.9 us): 29.4 us, 23.3 when the L2
+//     holds them.  6 us to the first scores (launch, shares, lengths, first tile), six
+//     tiles an SM, their join;
+//   * chunks: 4,096 tokens over 32K positions 1,340 us, 1.54 PFLOP/s of the 1.98 that a
 //     large product reaches.  3,000 cycles a pair of tiles of which the products are
 //     2,200: the tensor cores wait for weights where a stream's softmax (1,360 cycles and
 //     two waits) is not hidden by the other's products.  One stream a row tile and one
