@@ -50,6 +50,12 @@ def test_lists_of_every_layout(lens, new, H, Hk, page, dtype, select):
     _attend(step, *step.rows(), idx=_lists(step, select, share=0.9 if select == 3 else 0.2))
 
 
+@pytest.mark.parametrize("select", [1000, 4096])
+def test_the_longest_lists(select):
+    step = ref.Step([70000, 200], [3, 20], H=8, Hk=1, page=16, dtype=BF16, seed=select)
+    _attend(step, *step.rows(), idx=_lists(step, select))
+
+
 @pytest.mark.parametrize("sparse", [False, True])
 @pytest.mark.parametrize("n,new", [(60000, 1), (20000, 40)])
 def test_not_finite_beside_long_shares(n, new, sparse):
