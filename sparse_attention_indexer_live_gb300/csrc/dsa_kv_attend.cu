@@ -84,6 +84,7 @@ constexpr int kNumBars = 4 + 2 * kStages + kInfos + 2 * kDescs + 6 + 3 + kInfos;
 constexpr int kOffWord = kOffBars + kNumBars * 8;  // tensor memory's address, abort flag
 constexpr int kSmem = kOffWord + 16;
 static_assert(kSmem <= 232448, "shared memory");
+static_assert(sizeof(Desc) % 8 == 0, "barriers on 8-byte boundaries");
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;  // S (and P) at 0 and 128, O at 256 and 384
 constexpr int kNever = 0x7FFFFFFF;                 // past every page number
 // A unit costs this many positions besides its own (one of two row tiles as much as
@@ -118,6 +119,7 @@ struct Launch {
   int32_t log_cpt;  // log2 of pages a tile of positions
   int32_t words;    // of 32 tokens, of a row tile's
   int32_t rows;     // of a slot of the workspace
+  int32_t wide;     // o lies on a 32-byte boundary
   uint8_t* ws;      // [kMaxCtas] Cut, int32 CTAs with a share | sums | outputs
   int64_t ml_off, o_off;
 };
@@ -159,6 +161,13 @@ __device__ __forceinline__ void tld16(uint32_t addr, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
+}
+// 32 bytes a lane: the lanes' rows are lines of their own, and a store takes the longer
+// the more of them there are, not the wider they are.
+__device__ __forceinline__ void store32(void* at, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
 }
 __device__ __forceinline__ void tst16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -1218,17 +1227,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         if (real) {
           if (slot >= 0) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4*>(po + col + j) = make_uint4(ov[j], ov[j + 1], ov[j + 2], ov[j + 3]);
+            for (int j = 0; j < 32; j += 8) store32(po + col + j, &ov[j]);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out * kKvDim + col);
+            uint16_t* dst = static_cast<uint16_t*>(p.o) + out * kKvDim + col;
+            uint32_t y[16];
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint32_t y[4];
+            for (int i = 0; i < 16; ++i) y[i] = pair_of<kBf16>(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1]));
+            if (L.wide) {
+              store32(dst, y);
+              store32(dst + 16, y + 8);
+            } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                y[i] = pair_of<kBf16>(__uint_as_float(ov[j + 2 * i]), __uint_as_float(ov[j + 2 * i + 1]));
-              dst[j / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
             }
           }
         }
@@ -1484,9 +1495,10 @@ Sizes sizes_of(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t req
   const int64_t most = units * (keys + kUnitCost) / kLeast;
   s.ctas = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxCtas), most));
   s.rows = (int32_t)(tokens * n <= 128 || select ? std::min<int64_t>(tokens * n, 128) : 256);
-  s.ml_off = fused_align16(kMaxCtas * (int64_t)sizeof(Cut) + 16);
-  s.o_off = s.ml_off + fused_align16((int64_t)2 * s.ctas * s.rows * 8);
-  s.bytes = s.o_off + (int64_t)2 * s.ctas * s.rows * kKvDim * 4;
+  // (of 32 bytes each, from the workspace's first multiple of 32)
+  s.ml_off = kMaxCtas * (int64_t)sizeof(Cut) + 32;
+  s.o_off = s.ml_off + ((int64_t)2 * s.ctas * s.rows * 8 + 31) / 32 * 32;
+  s.bytes = s.o_off + (int64_t)2 * s.ctas * s.rows * kKvDim * 4 + 16;
   return s;
 }
 
@@ -1580,7 +1592,8 @@ int attend(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t request
   L.words = (L.tpt + 31) / 32;
   L.log_cpt = 7 - p.shift;
   L.rows = sz.rows;
-  L.ws = static_cast<uint8_t*>(workspace);
+  L.ws = reinterpret_cast<uint8_t*>(((uintptr_t)workspace + 31) & ~(uintptr_t)31);
+  L.wide = !misaligned(o, 32);
   L.ml_off = sz.ml_off;
   L.o_off = sz.o_off;
   // a cache of no pages: a map of one row that no box touches
