@@ -26,16 +26,16 @@
 // What bounds it, 32 heads on 8 unless said otherwise:
 //   * single tokens: HBM.  64 requests of up to 16K positions 281 us, 1.83 GB at 0.95 of
 //     the copy rate;
-//   * one token of 128K positions, 8 heads on 1 (67 MB, 9.9 us): 29.4 us, 23.3 when the L2
+//   * one token of 128K positions, 8 heads on 1 (67 MB, 9.9 us): 28.6 us, 23.5 when the L2
 //     holds them.  6 us to the first scores (launch, shares, lengths, first tile), six
 //     tiles an SM, their join;
-//   * chunks: 4,096 tokens over 32K positions 1,340 us, 1.54 PFLOP/s of the 1.98 that a
+//   * chunks: 4,096 tokens over 32K positions 1,328 us, 1.55 PFLOP/s of the 1.98 that a
 //     large product reaches.  3,000 cycles a pair of tiles of which the products are
 //     2,200: the tensor cores wait for weights where a stream's softmax (1,360 cycles and
 //     two waits) is not hidden by the other's products.  One stream a row tile and one
 //     issuing warp; 16 softmax warps took 2,035 us;
 //   * a selection: 2,048 tokens of 32 heads on 4, 16 pages of 64 each, 16 tokens a tile:
-//     215 us.  Neighbours share 12 pages and have 4 of their own, so that a tile's union
+//     211 us.  Neighbours share 12 pages and have 4 of their own, so that a tile's union
 //     is 80 pages: 1.7 GB through the L2 at 8 TB/s (8.9 is what single row tiles reach
 //     on pages that all stay there).
 
@@ -88,7 +88,7 @@ static_assert(sizeof(Desc) % 8 == 0, "barriers on 8-byte boundaries");
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;  // S (and P) at 0 and 128, O at 256 and 384
 constexpr int kNever = 0x7FFFFFFF;                 // past every page number
 // A unit costs this many positions besides its own (one of two row tiles as much as
-// one of one: 31 decode requests beside three prompts take 143 us so, 168 at costs of
+// one of one: 31 decode requests beside three prompts took 143 us so, 168 at costs of
 // 3 : 2 and 149 at 2 : 3; 64 requests 275 us, 282 at a cost of 0 and 276 of 512); a CTA
 // takes no share below kLeast (one token of 128K 23.9 us, 31 at 2,048); a cut less than
 // kSnap tiles from a unit's end moves there (lists of 2,048 tokens 217 us, 220 at 1 and

@@ -8,7 +8,7 @@
 // us, 8.5 by the bytes.  The longest request's warps read eight lots of 32 pages, two on
 // their way into the L2 ahead of the one they load (46 us without, and 34 against 37 when
 // the L2 holds all of it); then the choice's chain follows, some 10 us.  2,048 tokens over
-// 2,048 pages: 60 us.  67 MB of scores are written and their best read back; scores 28 us
+// 2,048 pages: 59 us.  67 MB of scores are written and their best read back; scores 28 us
 // (heads' sums 8, the rest bound by the loaders' and writers' work on a tile), then the
 // choice (tops, floor, candidates, ranks; issue slots and latency alike).
 
