@@ -699,13 +699,12 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
   // more than 2^-14.5 of the norms, and of what their squares may have lost below 2^-126
   const float e = norm * row_norm * 4.4e-5f + 0x1p-50f;
   auto fine = [&](float s) { return fabsf(s) < INFINITY && e < INFINITY; };
-  // a floor that m of the 256 reach, and few more: few, the m-th of the lanes' largest;
-  // else by halves between their extremes
-  float least;
-  if (m <= 32) {
-    float v = best[0];
+  // a floor that m of the 256 reach, and few more: where twice as many lanes have any, the
+  // m-th of the lanes' largest; else by halves between their extremes
+  float least, v = best[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v = fmaxf(v, best[i]);
+  for (int i = 1; i < 8; ++i) v = fmaxf(v, best[i]);
+  if (__popc(__ballot_sync(0xFFFFFFFFu, v > -INFINITY)) >= 2 * m) {
     int above = 0;
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
