@@ -563,7 +563,8 @@ __device__ __forceinline__ int64_t rank_key(double x) {
 
 // The best pages of one token and key/value head, by W warps.  Scores are known to
 // within e: the m-th best is not below the m-th largest of 256 sets' largest lower
-// bounds (sets of whole groups of 16, or of pages where there are few groups),
+// bounds (sets of whole groups of 16, or of pages where there are few groups; with eight
+// warps, whose m may be 255, of 512: each thread's two largest),
 // whatever may reach that goes on a short list, and of that list those that e leaves
 // open are scored again in fp64.  A list that does not fit (many equal scores) is
 // taken a part at a time, all in fp64, against the best so far.
@@ -575,7 +576,7 @@ struct Pick {
   int64_t key[kList];
   float score[kList];
   int page[kList];
-  float group[W == 1 ? 1 : kPickThreads];
+  float group[W == 1 ? 1 : 2 * kPickThreads];
   float norm[W];
   int groups[W][128];  // of 16 pages, those that may reach the floor
   uint16_t open_list[kList];
@@ -642,14 +643,16 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
   const int tiles = (end + kScorePages - 1) / kScorePages;
   const float4* top4 = reinterpret_cast<const float4*>(p.tops) + ((int64_t)(t - p.t0) * p.kv_heads + head) * p.tiles;
   auto is_free = [&](int j) { return j >= p.lead && j < end; };
-  float best[8];  // of eight sets (of one, with more warps)
+  constexpr int kSets = W == 1 ? 8 : 16;  // a lane's, of 256 or 512
+  float best[kSets];  // of eight sets
 #pragma unroll
-  for (int i = 0; i < 8; ++i) best[i] = -INFINITY;
+  for (int i = 0; i < kSets; ++i) best[i] = -INFINITY;
   if (2 * tiles >= m && W > 1) {
     const float* top1 = reinterpret_cast<const float*>(top4);
-    for (int i = tid; i < 4 * tiles; i += kT) {
-      const float s = top1[i];
+    for (int i = tid; i < 4 * tiles; i += 2 * kT) {
+      const float s = top1[i], u = i + kT < 4 * tiles ? top1[i + kT] : -INFINITY;
       if (fabsf(s) < INFINITY) best[0] = fmaxf(best[0], s);
+      if (fabsf(u) < INFINITY) best[1] = fmaxf(best[1], u);
     }
   } else if (2 * tiles >= m) {
     for (int i0 = tid; i0 < tiles; i0 += 2 * kT) {
@@ -678,13 +681,18 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
     }
   }
   if (W > 1) {
-    float top = best[0];
+    // the two largest of a thread's
+    float top = best[0], next = -INFINITY;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, best[i]);
+    for (int i = 1; i < 8; ++i) {
+      next = fmaxf(next, fminf(top, best[i]));
+      top = fmaxf(top, best[i]);
+    }
     x.group[tid] = top;
+    x.group[kT + tid] = next;
     sync();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) best[i] = x.group[lane + 32 * i];
+    for (int i = 0; i < kSets; ++i) best[i] = x.group[lane + 32 * i];
   } else {
     sync();
   }
@@ -699,11 +707,11 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
   // more than 2^-14.5 of the norms, and of what their squares may have lost below 2^-126
   const float e = norm * row_norm * 4.4e-5f + 0x1p-50f;
   auto fine = [&](float s) { return fabsf(s) < INFINITY && e < INFINITY; };
-  // a floor that m of the 256 reach, and few more: where twice as many lanes have any, the
+  // a floor that m of the sets' reach, and few more: where twice as many lanes have any, the
   // m-th of the lanes' largest; else by halves between their extremes
   float least, v = best[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) v = fmaxf(v, best[i]);
+  for (int i = 1; i < kSets; ++i) v = fmaxf(v, best[i]);
   if (__popc(__ballot_sync(0xFFFFFFFFu, v > -INFINITY)) >= 2 * m) {
     int above = 0;
 #pragma unroll
@@ -713,9 +721,9 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
     }
     least = __shfl_sync(0xFFFFFFFFu, v, __ffs(__ballot_sync(0xFFFFFFFFu, above == m - 1)) - 1) - e;
   } else {
-    uint32_t o[8], hi = 0, lo = 0xFFFFFFFFu;
+    uint32_t o[kSets], hi = 0, lo = 0xFFFFFFFFu;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kSets; ++i) {
       o[i] = order_of(best[i]);
       hi = max(hi, o[i]);
       lo = min(lo, o[i]);
@@ -726,7 +734,7 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
       const uint32_t mid = lo + (hi - lo + 1) / 2;
       int reach = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) reach += o[i] >= mid;
+      for (int i = 0; i < kSets; ++i) reach += o[i] >= mid;
       reach = __reduce_add_sync(0xFFFFFFFFu, reach);
       if (reach >= m) {
         lo = mid;
