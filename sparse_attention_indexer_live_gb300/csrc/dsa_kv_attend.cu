@@ -109,7 +109,7 @@ struct Cut {
 };
 struct Sizes {
   int64_t ml_off, o_off, bytes;
-  int32_t ctas, rows;
+  int32_t ctas, rows, joins;
 };
 
 struct Launch {
@@ -1478,10 +1478,15 @@ int device_sms() {
 
 // Tokens a row tile: 128 rows of them.  Of a selection no more than an Info's words
 // hold, a bit a token and page of the tile: pages of 32 and less with one or two heads
-// a group have tiles that are not full.
-int32_t tokens_a_tile(const dsa_kv_cfg* cfg, int32_t n, int32_t select) {
-  const int32_t full = 128 / n;
-  return select ? std::min(full, 32 * kTokenWords * cfg->page_size / 128) : full;
+// a group have tiles that are not full.  And fewer, where there would be fewer units than
+// SMs: a unit's union is walked by one CTA (25 tokens of 10 heads on 2, 8 pages each: 81 us
+// in tiles of 25).
+int32_t tokens_a_tile(const dsa_kv_cfg* cfg, int32_t tokens, int32_t n, int32_t select) {
+  int32_t t = 128 / n;
+  if (!select) return t;
+  t = std::min(t, 32 * kTokenWords * cfg->page_size / 128);
+  while (t > 1 && (int64_t)tokens / t * cfg->kv_heads < kMaxCtas) t /= 2;
+  return t;
 }
 
 // The workspace and the grid, from the shapes: as many CTAs as there may be shares
@@ -1489,12 +1494,14 @@ int32_t tokens_a_tile(const dsa_kv_cfg* cfg, int32_t n, int32_t select) {
 Sizes sizes_of(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests, int32_t table_width,
                int32_t select, int32_t sms) {
   Sizes s;
-  const int64_t n = heads / cfg->kv_heads, tpt = tokens_a_tile(cfg, (int32_t)n, select), tpu = select ? tpt : 2 * tpt;
+  const int64_t n = heads / cfg->kv_heads, tpt = tokens_a_tile(cfg, tokens, (int32_t)n, select), tpu = select ? tpt : 2 * tpt;
   const int64_t units = (std::min(tokens, requests) + tokens / tpu) * cfg->kv_heads;
   const int64_t keys = select ? (int64_t)select * cfg->page_size : (int64_t)table_width * cfg->page_size;
   const int64_t most = units * (keys + kUnitCost) / kLeast;
   s.ctas = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxCtas), most));
-  s.rows = (int32_t)(tokens * n <= 128 || select ? std::min<int64_t>(tokens * n, 128) : 256);
+  s.rows = (int32_t)(select ? tpt * n : tokens * n <= 128 ? tokens * n : 256);
+  // cut units are few where their shares are many: their rows to more CTAs then
+  s.joins = (int32_t)std::min<int64_t>(s.rows, std::max<int64_t>(8, std::min<int64_t>(64, 1024 / std::max<int64_t>(1, units))));
   // (of 32 bytes each, from the workspace's first multiple of 32)
   s.ml_off = kMaxCtas * (int64_t)sizeof(Cut) + 32;
   s.o_off = s.ml_off + ((int64_t)2 * s.ctas * s.rows * 8 + 31) / 32 * 32;
@@ -1525,7 +1532,7 @@ int launch(const Launch& L, const Sizes& sz, cudaStream_t stream) {
   const int rc = launch_dependent(attend_kernel<kBf16, kSparse>, sz.ctas, kThreads, kSmem, 0, stream, L);
   if (rc != DSA_OK || sz.ctas == 1) return rc;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)(sz.ctas - 1), (unsigned)std::min(8, sz.rows));
+  lc.gridDim = dim3((unsigned)(sz.ctas - 1), (unsigned)sz.joins);
   lc.blockDim = dim3(256);
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1588,7 +1595,7 @@ int attend(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t request
   p.flip = c < 0.f;
   // not 0: a masked score of -inf times it stays -inf
   p.c2 = std::max(c < 0.f ? -c : c, 1.17549435e-38f);
-  L.tpt = tokens_a_tile(cfg, p.n, select);
+  L.tpt = tokens_a_tile(cfg, tokens, p.n, select);
   L.words = (L.tpt + 31) / 32;
   L.log_cpt = 7 - p.shift;
   L.rows = sz.rows;

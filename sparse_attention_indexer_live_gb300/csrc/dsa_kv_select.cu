@@ -743,7 +743,11 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
         hi = mid - 1;
       }
     }
-    least = float_of(lo) - e;  // (all bounds are as far below)
+    uint32_t at = 0xFFFFFFFFu;  // the least that reaches lo: where there are few, lo may lie far below it
+#pragma unroll
+    for (int i = 0; i < kSets; ++i)
+      if (o[i] >= lo) at = min(at, o[i]);
+    least = float_of(__reduce_min_sync(0xFFFFFFFFu, at)) - e;  // (all bounds are as far below)
   }
   // the groups that may reach it, 32 tiles of a warp at a time (warps' in turn), and
   // their pages
