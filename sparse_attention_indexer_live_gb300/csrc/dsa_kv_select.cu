@@ -730,6 +730,11 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
     }
     hi = __reduce_max_sync(0xFFFFFFFFu, hi);
     lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    int sets = 0;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) sets += best[i] > -INFINITY;
+    // (of few sets one more may be a single page, and far below the others)
+    const int enough = __reduce_add_sync(0xFFFFFFFFu, sets) >= 4 * m ? m + 4 : m;
     while (lo < hi) {  // at least m reach lo
       const uint32_t mid = lo + (hi - lo + 1) / 2;
       int reach = 0;
@@ -738,7 +743,7 @@ __global__ void __launch_bounds__(32 * W * kPickRows<W>, W == 1 ? 32 / kPickRows
       reach = __reduce_add_sync(0xFFFFFFFFu, reach);
       if (reach >= m) {
         lo = mid;
-        if (reach <= m + 4) break;
+        if (reach <= enough) break;
       } else {
         hi = mid - 1;
       }
