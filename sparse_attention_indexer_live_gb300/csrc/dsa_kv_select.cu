@@ -1075,10 +1075,10 @@ int dsa_kv_select(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t 
       }
     }
     // a warp a row, where there are rows enough to fill the SMs with warps and their
-    // lists are short (8,192 rows 61 us, 130 with eight warps each); else eight (256 rows
-    // 34.5 us, 38.8 with one)
+    // lists are short (8,192 rows 61 us, 130 with eight warps each; 1,280 rows 28.8 and
+    // 33.7); else eight (256 rows 34.5 us, 38.8 with one)
     const int64_t rows = (int64_t)(p.t1 - p.t0) * cfg->kv_heads;
-    const bool one = select - lead - trail <= Pick<1>::kMost && rows >= 16 * (int64_t)sms && table_width <= 8192;
+    const bool one = select - lead - trail <= Pick<1>::kMost && rows >= 4 * (int64_t)sms && table_width <= 8192;
     const int64_t blocks = one ? (rows + kPickRows<1> - 1) / kPickRows<1> : rows;
     if (one)
       st = cfg->dtype == DSA_BF16 ? launch_dependent(pick_kernel<true, 1>, blocks, 32 * kPickRows<1>, 0, 0, stream, p)
