@@ -1253,7 +1253,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           p.lse[out] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
       }
       __syncwarp();
-      for (uint32_t again = __ballot_sync(0xFFFFFFFFu, real && pos >= 0 && (odd || !(sum - sum == 0.f))); again;
+      // (rows without a position among them: their tile is that of position 0)
+      for (uint32_t again = __ballot_sync(0xFFFFFFFFu, real && (odd || !(sum - sum == 0.f))); again;
            again &= again - 1) {
         const int src = __ffs(again) - 1;
         const int rt = __shfl_sync(0xFFFFFFFFu, t, src), rh = __shfl_sync(0xFFFFFFFFu, head, src);
