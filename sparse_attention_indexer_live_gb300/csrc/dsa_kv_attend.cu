@@ -269,10 +269,10 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 
 // One row's share of a unit by a warp, four dims a lane: sum_j 2^(s_j - m) v_j over
 // its positions; m is given, or (a NaN) found on the way with the sum of the weights.
-// 0 times a NaN or an infinity is a NaN in the tensor cores' product and in a masked
-// exponent, so a row whose sum or output is not finite may owe that to a position
-// that it does not attend to: such a row is computed again from those that it does.
-// (Without a selection: if one of the positions after its own, up to the end of the
+// 0 times a NaN or an infinity is a NaN in the tensor cores' product, and with lists a
+// masked exponent may be one, so a row whose output (sum) is not finite may owe that to
+// a position that it does not attend to: such a row is computed again from those that
+// it does.  (Without lists: if a value after its own position, up to the end of the
 // unit's tiles, is to blame, or a score is infinite, which makes lse so.)
 struct Again {
   float4 o;
@@ -348,6 +348,7 @@ struct RowAgain {
 struct Share {  // of a unit
   int32_t r, kvh, j0, j1, from, to;
 };
+// Whether a value after position pos, of the share's tiles, is not finite.
 template <bool kBf16>
 __device__ __noinline__ bool odd_after(const Launch& L, const Share& d, int pos) {
   const KvParams& p = L.p;
@@ -360,10 +361,9 @@ __device__ __noinline__ bool odd_after(const Launch& L, const Share& d, int pos)
     if (id >= 0 && id < p.pages) {
       const int64_t at = 2 * kKvDim * ((((int64_t)id << p.shift) + (x & (p.page - 1))) * p.kv_heads + d.kvh);
       for (int c = 0; c < kKvDim / 8; ++c) {
-        const Eight e = load8(static_cast<const char*>(p.k) + at + 16 * c), f = load8(static_cast<const char*>(p.v) + at + 16 * c);
+        const Eight e = load8(static_cast<const char*>(p.v) + at + 16 * c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          odd |= (e.w[i] & top) == top || (e.w[i] >> 16 & top) == top || (f.w[i] & top) == top || (f.w[i] >> 16 & top) == top;
+        for (int i = 0; i < 4; ++i) odd |= (e.w[i] & top) == top || (e.w[i] >> 16 & top) == top;
       }
     }
     if (__any_sync(0xFFFFFFFFu, odd)) return true;
@@ -1048,18 +1048,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                 if (!(flags >> ((32 * w + b) >> p.shift) & 1)) words[w] &= ~(0xFFFFu << b);
           }
         }
-        // Sixteen positions at a time: where none of them is attended to their exponents
-        // get -inf for a base; where some are, they are told apart.  (A NaN among the
-        // first stays one: the row then has no finite sum and is computed again.)
+        // Sixteen positions at a time, those not attended to get a score of -inf.  Of
+        // lists, which most rows have few of a tile's pages on, a group with none of
+        // them attended to has its exponents' base at -inf instead.  (A score there that
+        // is a NaN or +inf leaves a NaN: the row then has no finite sum and is computed
+        // again.)
         auto group = [&](int i) { return words[i >> 1] >> (16 * (i & 1)) & 0xFFFFu; };
         const bool whole = __all_sync(0xFFFFFFFFu, (words[0] & words[1] & words[2] & words[3]) == 0xFFFFFFFFu);
-        uint32_t none = 0, some = 0;  // groups without a position of the row's; with some, of any row of the warp
+        uint32_t none = 0, some = 0;  // groups whose base is -inf; those told apart, of any row of the warp
         if (!whole) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t g = group(i);
-            none |= (uint32_t)(g == 0u) << i;
-            some |= (uint32_t)(g != 0u && g != 0xFFFFu) << i;
+            if (kSparse) none |= (uint32_t)(g == 0u) << i;
+            some |= (uint32_t)((!kSparse || g != 0u) && g != 0xFFFFu) << i;
           }
           some = __reduce_or_sync(0xFFFFFFFFu, some);
         }
@@ -1262,7 +1264,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         const float rm = __shfl_sync(0xFFFFFFFFu, m, src), rs = __shfl_sync(0xFFFFFFFFu, sum, src);
         const bool whole_row = !(rs - rs == 0.f);  // its sum too
         const Share d = {req, kvh, jbeg, jend, from, to};
-        if (!kSparse && rm != INFINITY && !odd_after<kBf16>(L, d, rp)) continue;
+        if (!kSparse && (whole_row ? rm != INFINITY : !odd_after<kBf16>(L, d, rp))) continue;
         const Again y = row_again<kBf16, kSparse>(L, d, rt, kvh * p.n + rh, rp, whole_row ? __int_as_float(0x7FFFFFFF) : rm);
         const float rl = whole_row ? y.l : rs, top = whole_row ? y.m : rm;
         const int64_t at = (int64_t)rt * p.H + kvh * p.n + rh;

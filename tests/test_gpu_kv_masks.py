@@ -1,6 +1,7 @@
 """The 16-bit cache's attentions beside what a row does not attend to: requests
-whose length is below the step's own tokens.  Against the plain 64-bit forms
-(tests/kv_ref.py, which derives the tolerances)."""
+whose length is below the step's own tokens, pages without an id under queries
+that are not finite, finite keys whose scores pass f32's range.  Against the
+plain 64-bit forms (tests/kv_ref.py, which derives the tolerances)."""
 import math
 
 import pytest
@@ -38,3 +39,59 @@ def test_rows_without_a_position(H, new, dtype, sparse):
         o, lse = _attend(step, q, k, v, 0.1, idx)
         few = step.first_list[2]
         assert (o[:few] == 0).all() and (lse[:few] == -math.inf).all()
+
+
+def _odd_queries(step, q):
+    """Rows whose scores against zeros are NaN: a NaN, infinities of either sign."""
+    q[0::4, 0, 3] = math.nan
+    q[1::4, :, 0] = math.inf
+    q[2::4, :, 1] = -math.inf
+    return q
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("H,new", [(8, 5), (8, 70), (1, 300)])
+def test_queries_that_are_not_finite_over_pages_without_an_id(H, new, dtype):
+    """Pages without an id are not attended to: no score of theirs reaches a row."""
+    step = ref.Step([500, 700], [new, new], H=H, Hk=1, page=64, dtype=dtype, seed=H + new, pad=1)
+    q, k, v = step.rows()
+    _odd_queries(step, q)
+    k[..., :2] = 1.0  # an infinite query has scores of its own sign
+    step.tables[0, :] = -1
+    step.tables[1, 1:3] = -1
+    step.tables[1, 7] = step.pages
+    o, lse = _attend(step, q, k, v)
+    assert (o[:new] == 0).all() and (lse[:new] == -math.inf).all()
+    # (a NaN query over pages that are there has no other result)
+    live = slice(step.first_list[1], step.first_list[2])
+    t = torch.arange(2 * new, device=o.device)[live]
+    assert torch.isnan(lse[live][t % 4 == 0, 0]).all() and (lse[live][t % 4 == 2] == -math.inf).all()
+    idx = _lists(step, 6)
+    o, lse = _attend(step, q, k, v, idx=idx)
+    assert (o[:new] == 0).all() and (lse[:new] == -math.inf).all()
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+@pytest.mark.parametrize("lens,new,H,page", [
+    ([5, 77], [1, 3], 8, 16),              # a tile of rows each
+    ([300, 1030], [200, 1030], 8, 64),     # two
+    ([40000, 20], [1, 20], 8, 64),         # shared by many CTAs
+    ([20000, 50], [100, 50], 32, 128)])
+def test_finite_keys_whose_scores_are_not(lens, new, H, page, sparse):
+    """bf16 keys so large that their scores pass f32's range, where no row attends to them: the last page's stale rows,
+    pages of no list, and the chunk's later positions."""
+    step = ref.Step(lens, new, H=H, Hk=1, page=page, dtype=BF16, seed=lens[0], pad=1)
+    q, k, v = step.rows()
+    idx = _lists(step, 4) if sparse else None
+    ids = step.tables.cpu()
+    sign = torch.where(torch.arange(128) % 3 == 0, -3e38, 3e38).to(BF16).to(k.device)
+    for r, n in enumerate(lens):
+        last = (n - 1) // page
+        k[ids[r, last], n - last * page:] = sign if r else 3e38
+    _attend(step, q, k, v, 0.1, idx)
+    # a late position; the rows that attend to it have no score but 0
+    at = lens[0] - 1 - new[0] // 3
+    k[ids[0, at // page], at % page] = sign
+    q[new[0] - 1 - new[0] // 3:new[0]] = 0
+    _attend(step, q, k, v, 0.1, idx)
+    _attend(step, q, k, v, -30.0, idx)
