@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const int cpt = 1 << L.log_cpt;
       const int chunk = lane & (cpt - 1), half = lane >> L.log_cpt;
       const uint32_t box = sb + kOffKV + (half & 1) * kHalf + chunk * p.page * 128;
-      const uint32_t nowhere = (uint32_t)p.pages << p.shift;  // past the cache: zeros
+      const uint32_t nowhere = p.pages ? (uint32_t)p.pages << p.shift : 1u;  // past the cache (its map): zeros
       int tile = 0, units = 0, singles = 0;
       int quse[2] = {0, 0};  // loads of each Q tile
       int asked = 0;         // key and value tiles asked for
@@ -1606,7 +1606,7 @@ int attend(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t request
   L.wide = !misaligned(o, 32);
   L.ml_off = sz.ml_off;
   L.o_off = sz.o_off;
-  // a cache of no pages: a map of one row that no box touches
+  // a cache of no pages: a map of one row, which boxes begin behind
   const uint64_t slots = std::max<uint64_t>(1, (uint64_t)cfg->pages * cfg->page_size);
   const void* kp = cfg->pages ? k_cache : q;
   const void* vp = cfg->pages ? v_cache : q;

@@ -9,7 +9,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tests import kv_ref as ref  # noqa: E402
-from tests.test_gpu_kv import BF16, F16, _attend, _lists  # noqa: E402
+from tests.test_gpu_kv import BF16, F16, _attend, _dsa, _lists  # noqa: E402
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
 
@@ -95,3 +95,27 @@ def test_finite_keys_whose_scores_are_not(lens, new, H, page, sparse):
     q[new[0] - 1 - new[0] // 3:new[0]] = 0
     _attend(step, q, k, v, 0.1, idx)
     _attend(step, q, k, v, -30.0, idx)
+
+
+@pytest.mark.parametrize("P", [0, 3])
+def test_a_pool_of_no_pages_and_odd_queries(P):
+    """Nothing is attended to, whatever the first token's queries hold."""
+    dsa, dev = _dsa(), "cuda:0"
+    i32 = dict(dtype=torch.int32, device=dev)
+    cfg = dsa.kv_cfg(pages=0, page_size=64, kv_heads=2)
+    none = torch.empty(0, 64, 2, 128, dtype=BF16, device=dev)
+    first, lens, tables = torch.tensor([0, 2, 70], **i32), torch.tensor([2, 150], **i32), torch.zeros(2, P, **i32)
+    idx = torch.zeros(70, 2, 3, **i32)
+    for bad in (math.nan, math.inf):
+        q = torch.randn(70, 8, 128, device=dev).to(BF16)
+        q[0] = bad
+        q[40, 5, 7] = -bad
+        for lists in (None, idx):
+            o, lse = torch.full_like(q, 3.0), torch.zeros(70, 8, device=dev)
+            if lists is None:
+                ws = torch.empty(dsa.dsa_kv_attention_workspace(cfg, q, tables), dtype=torch.uint8, device=dev)
+                dsa.dsa_kv_attention(cfg, none, none, q, first, lens, tables, 0.1, ws, o, lse)
+            else:
+                ws = torch.empty(dsa.dsa_kv_block_attention_workspace(cfg, q, idx, tables), dtype=torch.uint8, device=dev)
+                dsa.dsa_kv_block_attention(cfg, none, none, q, idx, first, lens, tables, 0.1, ws, o, lse)
+            assert (o == 0).all() and (lse == -math.inf).all()
