@@ -81,7 +81,7 @@ constexpr int kOffXch = kOffDesc + kDescs * (int)sizeof(Desc);  // [stream][row]
 constexpr int kOffScan = kOffXch;                               // (before the first unit) warps' sums
 constexpr int kOffBars = kOffXch + 2 * 128 * 8;
 constexpr int kNumBars = 4 + 2 * kStages + kInfos + 2 * kDescs + 6 + 3 + kInfos;
-constexpr int kOffWord = kOffBars + kNumBars * 8;  // tensor memory's address, abort flag
+constexpr int kOffWord = kOffBars + kNumBars * 8;  // tensor memory's address, the waits' limit
 constexpr int kSmem = kOffWord + 16;
 static_assert(kSmem <= 232448, "shared memory");
 static_assert(sizeof(Desc) % 8 == 0, "barriers on 8-byte boundaries");
@@ -97,7 +97,7 @@ constexpr int kUnitCost = 256;
 constexpr int kLeast = 512;
 constexpr int kSnap = 2;
 constexpr int kMaxCtas = 160;  // SMs that are made use of
-#ifdef DSA_KV_TEST_WAIT_CYCLES
+#if defined(DSA_KV_TEST_WAIT_CYCLES) && !defined(DSA_KV_TEST_FED)
 constexpr uint32_t kPArrivals = 129;  // one more than there are
 #else
 constexpr uint32_t kPArrivals = 128;
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   uint64_t* dbar = xfull + 1;              // products in flight when the CTA gives up
   uint64_t* tfree = dbar + 1;              // [8] sparse: an Info may be written again
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + kOffWord);
-  volatile int* abort = reinterpret_cast<volatile int*>(base + kOffWord + 4);
+  volatile int* limit = reinterpret_cast<volatile int*>(base + kOffWord + 4);
   int* start_req = reinterpret_cast<int*>(base + kOffDesc);                  // before the first unit
   int64_t* start_x = reinterpret_cast<int64_t*>(base + kOffDesc + 8);        // (the scheduler reads them first)
   int64_t* warp_sum = reinterpret_cast<int64_t*>(base + kOffScan);
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   let_next_start();
   if (threadIdx.x == 0) {
-    *abort = 0;
+    *limit = kWaitLimit;
     *start_req = -1;
     for (int i = 0; i < kStages; ++i) {
       bar_init(&full[i], 1);
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       bool ok = true;
       auto publish = [&](const Desc& u) {
         const int s = d % kDescs;
-        if (d >= kDescs && !wait_all(&dempty[s], ((d / kDescs) & 1) ^ 1, abort)) return false;
+        if (d >= kDescs && !wait_all(&dempty[s], ((d / kDescs) & 1) ^ 1, limit)) return false;
         if (lane == 0) {
           desc[s] = u;
           bar_arrive(&dfull[s]);
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const int n = 2 * tile + kv, st = n % kStages, use = n / kStages;
-          if (use > 0 && !wait_all(&empty[st], (use & 1) ^ 1, abort)) return false;
+          if (use > 0 && !wait_all(&empty[st], (use & 1) ^ 1, limit)) return false;
           if (lane == 0) bar_expect(&full[st], kTileBytes);
           __syncwarp();
           if (half < 2) tma_load(box + st * kTileBytes, kv ? &L.v : &L.k, &full[st], half * 64, kvh, z);
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         return true;
       };
       auto load_q = [&](int slot, int kvh, int t) -> bool {
-        if (quse[slot] > 0 && !wait_all(&qempty[slot], (quse[slot] & 1) ^ 1, abort)) return false;
+        if (quse[slot] > 0 && !wait_all(&qempty[slot], (quse[slot] & 1) ^ 1, limit)) return false;
         ++quse[slot];
         if (lane == 0) bar_expect(&qfull[slot], (uint32_t)(L.tpt * p.n * 256));
         __syncwarp();
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       };
       for (; ok; ++units) {
         const int ds = units % kDescs;
-        if (!wait_all(&dfull[ds], (units / kDescs) & 1, abort)) break;
+        if (!wait_all(&dfull[ds], (units / kDescs) & 1, limit)) break;
         const Desc u = desc[ds];
         __syncwarp();
         if (lane == 0) bar_arrive(&dempty[ds]);
@@ -728,13 +728,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             const Info& x = info[t % kInfos];
             return lane < cpt && x.flags >> lane & 1 ? table[x.page[lane]] : -1;
           };
-          ok = ok && wait_all(&tfull[tile % kInfos], (tile / kInfos) & 1, abort);
+          ok = ok && wait_all(&tfull[tile % kInfos], (tile / kInfos) & 1, limit);
           int id = ok ? id_in(tile) : -1;
           while (ok) {
             const bool last = info[tile % kInfos].flags & kLast;
             int id1 = -1;
             if (!last) {
-              ok = wait_all(&tfull[(tile + 1) % kInfos], ((tile + 1) / kInfos) & 1, abort);
+              ok = wait_all(&tfull[(tile + 1) % kInfos], ((tile + 1) / kInfos) & 1, limit);
               if (ok) id1 = id_in(tile + 1);
             }
             ok = ok && load_tile(id >= 0 ? (uint32_t)id << p.shift : nowhere, u.kvh);
@@ -743,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
         }
       }
-      if (__any_sync(0xFFFFFFFFu, *abort)) {  // what is still on its way lands before the CTA ends
+      if (__any_sync(0xFFFFFFFFu, gave_up(limit))) {  // what is still on its way lands before the CTA ends
         for (int n = max(0, asked - kStages); n < asked; ++n) drain(&full[n % kStages], (n / kStages) & 1);
         for (int i = 0; i < 2; ++i)
           if (quse[i] > 0) drain(&qfull[i], (quse[i] - 1) & 1);
@@ -759,9 +759,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       int quse0 = 0, quse1 = 0;    // units of each Q tile
       int count0 = 0, count1 = 0;  // steps of each stream
       bool ok = true;
-      auto k_full = [&](int t) { return wait_all(&full[(2 * t) % kStages], ((2 * t) / kStages) & 1, abort); };
-      auto v_full = [&](int t) { return wait_all(&full[(2 * t + 1) % kStages], ((2 * t + 1) / kStages) & 1, abort); };
-      auto p_full = [&](int s) { return wait_all(&pfull[s], (s ? count1 : count0) & 1, abort); };
+      auto k_full = [&](int t) { return wait_all(&full[(2 * t) % kStages], ((2 * t) / kStages) & 1, limit); };
+      auto v_full = [&](int t) { return wait_all(&full[(2 * t + 1) % kStages], ((2 * t + 1) / kStages) & 1, limit); };
+      auto p_full = [&](int s) { return wait_all(&pfull[s], (s ? count1 : count0) & 1, limit); };
       auto issue_s = [&](int s, int slot, int st, bool free_k, bool free_q) {
         fence_after();
         if (elect_one()) {
@@ -785,15 +785,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       };
       for (int unit = 0; ok; ++unit) {
         const int ds = unit % kDescs;
-        if (!(ok = wait_all(&dfull[ds], (unit / kDescs) & 1, abort))) break;
+        if (!(ok = wait_all(&dfull[ds], (unit / kDescs) & 1, limit))) break;
         const bool stop = desc[ds].stop, pair = desc[ds].pair;
         __syncwarp();
         if (lane == 0) bar_arrive(&dempty[ds]);
         if (stop) break;
-        auto outputs_free = [&]() { return unit == 0 || wait_all(ofree, (unit & 1) ^ 1, abort); };
+        auto outputs_free = [&]() { return unit == 0 || wait_all(ofree, (unit & 1) ^ 1, limit); };
         // (a tile's Info is written before its keys are asked for)
         if (pair) {
-          ok = wait_all(&qfull[0], quse0++ & 1, abort) && wait_all(&qfull[1], quse1++ & 1, abort) && k_full(tile);
+          ok = wait_all(&qfull[0], quse0++ & 1, limit) && wait_all(&qfull[1], quse1++ & 1, limit) && k_full(tile);
           if (!ok) break;
           bool last = info[tile % kInfos].flags & kLast;
           issue_s(0, 0, (2 * tile) % kStages, false, last);
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
         } else {
           const int slot = singles++ & 1;
-          if (!(ok = wait_all(&qfull[slot], (slot ? quse1 : quse0) & 1, abort))) break;
+          if (!(ok = wait_all(&qfull[slot], (slot ? quse1 : quse0) & 1, limit))) break;
           if (slot)
             ++quse1;
           else
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             // with one S ahead, whichever comes first: its weights, or the next S's keys
             if (more && ahead - tile == 1 &&
                 !__all_sync(0xFFFFFFFFu, bar_test(&pfull[turn], (turn ? count1 : count0) & 1)) &&
-                !__any_sync(0xFFFFFFFFu, *abort || clock64() - t0 > kWaitCycles))
+                !__any_sync(0xFFFFFFFFu, gave_up(limit) || clock64() - t0 > kWaitCycles))
               continue;
             if (!(ok = v_full(tile) && (had || outputs_free()) && p_full(turn))) break;
             const bool add = had >> turn & 1;
@@ -863,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
         }
       }
-      if (__any_sync(0xFFFFFFFFu, *abort)) {
+      if (__any_sync(0xFFFFFFFFu, gave_up(limit))) {
         if (elect_one()) mma_commit(dbar);
         __syncwarp();
         drain(dbar, 0);
@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       bool ok = true;
       for (int units = 0; ok; ++units) {
         const int ds = units % kDescs;
-        if (!wait_all(&dfull[ds], (units / kDescs) & 1, abort)) break;
+        if (!wait_all(&dfull[ds], (units / kDescs) & 1, limit)) break;
         const Desc u = desc[ds];
         __syncwarp();
         if (lane == 0) bar_arrive(&dempty[ds]);
@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           const int id1 = id_of(pg1);
           const bool good = pg >= 0 && pg < p.P && id >= 0 && id < p.pages;
           const uint32_t have = __ballot_sync(0xFFFFFFFFu, good);
-          if (tile >= kInfos && !(ok = wait_all(&tfree[tile % kInfos], ((tile / kInfos) & 1) ^ 1, abort))) break;
+          if (tile >= kInfos && !(ok = wait_all(&tfree[tile % kInfos], ((tile / kInfos) & 1) ^ 1, limit))) break;
           Info& x = info[tile % kInfos];
           if (lane < 8) x.page[lane] = lane < cpt ? pg : -1;
           if (lane < kTokenWords) x.tokens[lane] = had;
@@ -982,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     int singles = 0;         // units of one row tile
     for (int units = 0;; ++units) {
       const int ds = units % kDescs;
-      if (!wait_all(&dfull[ds], (units / kDescs) & 1, abort)) break;
+      if (!wait_all(&dfull[ds], (units / kDescs) & 1, limit)) break;
       const bool stop = desc[ds].stop, pair = desc[ds].pair;
       const int t0 = desc[ds].t0, ntok = desc[ds].ntok, pos0 = desc[ds].pos0, slot = desc[ds].slot;
       const int kvh = desc[ds].kvh, req = desc[ds].r, jend = desc[ds].j1, jbeg = desc[ds].j0;
@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       bool ok = true, first = true;
       int had = 0;  // streams that had a step
       for (bool last = false; !last; ++tile) {
-        if (!wait_all(&tfull[tile % kInfos], (tile / kInfos) & 1, abort)) {
+        if (!wait_all(&tfull[tile % kInfos], (tile / kInfos) & 1, limit)) {
           ok = false;
           break;
         }
@@ -1065,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
           some = __reduce_or_sync(0xFFFFFFFFu, some);
         }
-        if (!wait_all(&sfull[me], count++ & 1, abort)) {
+        if (!wait_all(&sfull[me], count++ & 1, limit)) {
           ok = false;
           break;
         }
@@ -1173,16 +1173,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
       if (!ok) break;
       // ---- the unit's end
-      if ((pair ? me == 0 : had & 1) && !wait_all(&pvdone[0], ends[0] & 1, abort)) break;
-      if ((pair ? me == 1 : had & 2) && !wait_all(&pvdone[1], ends[1] & 1, abort)) break;
+      if ((pair ? me == 0 : had & 1) && !wait_all(&pvdone[0], ends[0] & 1, limit)) break;
+      if ((pair ? me == 1 : had & 2) && !wait_all(&pvdone[1], ends[1] & 1, limit)) break;
       ends[0] += had & 1;
       ends[1] += had >> 1;
       float m = m_used, sum = l, w0 = 1.f, w1 = 0.f;
       if (!pair) {  // the two streams' shares of the row, in the same order by both
-        if (units > 0 && !wait_all(ofree, (units & 1) ^ 1, abort)) break;  // the unit before is done with xch
+        if (units > 0 && !wait_all(ofree, (units & 1) ^ 1, limit)) break;  // the unit before is done with xch
         xch[me * 128 + row] = make_float2(m, l);
         bar_arrive(xfull);
-        if (!wait_all(xfull, singles++ & 1, abort)) break;
+        if (!wait_all(xfull, singles++ & 1, limit)) break;
         const float2 a = xch[row], b = xch[128 + row];
         m = fmaxf(a.x, b.x);
         const float top = m == -INFINITY ? 0.f : m;
@@ -1256,8 +1256,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
       __syncwarp();
       // (rows without a position among them: their tile is that of position 0)
-      for (uint32_t again = __ballot_sync(0xFFFFFFFFu, real && (odd || !(sum - sum == 0.f))); again;
-           again &= again - 1) {
+      uint32_t again = __ballot_sync(0xFFFFFFFFu, real && (odd || !(sum - sum == 0.f)));
+      if (!again) continue;
+      const long long begun = lane == 0 ? long_work_begins(limit) : 0;  // the products' warp waits for this one
+      for (; again; again &= again - 1) {
         const int src = __ffs(again) - 1;
         const int rt = __shfl_sync(0xFFFFFFFFu, t, src), rh = __shfl_sync(0xFFFFFFFFu, head, src);
         const int rp = __shfl_sync(0xFFFFFFFFu, pos, src), pr = __shfl_sync(0xFFFFFFFFu, prow, src);
@@ -1282,6 +1284,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           reinterpret_cast<uint2*>(p.o)[at * 32 + lane] =
               make_uint2(pair_of<kBf16>(y.o.x * inv, y.o.y * inv), pair_of<kBf16>(y.o.z * inv, y.o.w * inv));
       }
+      __syncwarp();
+      if (lane == 0) long_work_ends(limit, begun);
     }
   }
   fence_before();

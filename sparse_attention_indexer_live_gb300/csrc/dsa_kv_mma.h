@@ -5,7 +5,8 @@
 
 #include "dsa_kv.h"
 
-#ifdef DSA_KV_TEST_WAIT_CYCLES  // test builds shorten the waits and starve one barrier of each kernel
+// Test builds shorten the waits, and (but with DSA_KV_TEST_FED) starve one barrier of each kernel.
+#ifdef DSA_KV_TEST_WAIT_CYCLES
 constexpr long long kWaitCycles = DSA_KV_TEST_WAIT_CYCLES;
 #else
 constexpr long long kWaitCycles = 8000000000ll;  // ~4 s
@@ -49,25 +50,36 @@ __device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {  // wit
       : "memory");
   return ok != 0;
 }
-// Bounded wait; false when the phase has not completed in time (the error word and
-// the CTA's flag are then set, and the CTA's other waits fail at once).
-__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
+// How long a wait may take, one word a CTA, in 2^16 cycles; kGaveUp and thereabouts once one
+// took longer.  What a warp does while others wait, however long, is added to it (from its
+// beginning on, as if it had no end).
+constexpr int kWaitLimit = (int)(kWaitCycles >> 16), kGaveUp = INT32_MIN / 2, kNoEnd = 1 << 24;
+__device__ __forceinline__ bool gave_up(const volatile int* limit) { return *limit < 0; }
+__device__ __forceinline__ long long long_work_begins(volatile int* limit) {
+  atomicAdd(const_cast<int*>(limit), kNoEnd);
+  return clock64();
+}
+__device__ __forceinline__ void long_work_ends(volatile int* limit, long long begun) {
+  atomicAdd(const_cast<int*>(limit), (int)((clock64() - begun) >> 16) + 1 - kNoEnd);
+}
+// Bounded wait; false when the phase has not completed in time (the error word is then
+// set, and the CTA's other waits fail at once).
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* limit) {
   if (bar_try(b, parity)) return true;
   const long long t0 = clock64();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (bar_try(b, parity)) return true;
-    if (*abort) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *abort = 1;
+    if ((int)((clock64() - t0) >> 16) > *limit) {
+      *limit = kGaveUp;
       atomicExch(&g_kv_error, 1);
       return false;
     }
   }
 }
-__device__ __forceinline__ bool wait_all(uint64_t* b, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xFFFFFFFFu, bar_wait(b, parity, abort));
+__device__ __forceinline__ bool wait_all(uint64_t* b, uint32_t parity, volatile int* limit) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(b, parity, limit));
 }
 // For what is still in flight when a CTA gives up: bounded, whatever the flag says.
 __device__ __forceinline__ void drain(uint64_t* b, uint32_t parity) {

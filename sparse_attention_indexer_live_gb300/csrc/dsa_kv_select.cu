@@ -28,7 +28,7 @@ constexpr int kMeanHalf = kScorePages * 128;
 constexpr int kOffMeans = 4 * kSumHalf;              // the sums' two parts of two halves | two tiles of means
 constexpr int kOffScoreBars = kOffMeans + 2 * 2 * kMeanHalf;
 struct ScoreSide {
-  int piece[3], abort;
+  int piece[3], limit;
   uint32_t tmem;
   alignas(8) uint8_t there[4][8];   // by tile: its pages with an id, eight a byte
   float sq[4][2][4];     // and the largest squares of 32 pages, of a loader warp each
@@ -37,7 +37,7 @@ constexpr int kOffScoreSide = kOffScoreBars + 9 * 8;
 constexpr int kScoreSmem = kOffScoreSide + (int)sizeof(ScoreSide);
 constexpr int kPickThreads = 256;
 constexpr int64_t kScoreBytes = 96 << 20;            // scores of the tokens in work: most of them stay in L2
-#ifdef DSA_KV_TEST_WAIT_CYCLES
+#if defined(DSA_KV_TEST_WAIT_CYCLES) && !defined(DSA_KV_TEST_FED)
 constexpr uint32_t kMeanArrivals = 129;  // one more than there are
 #else
 constexpr uint32_t kMeanArrivals = 128;
@@ -124,12 +124,12 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
   uint64_t* acc_full = empty + 2;  // [2] its scores are in tensor memory
   uint64_t* acc_free = acc_full + 2;
   uint64_t* dbar = acc_free + 2;   // products in flight when the CTA gives up
-  volatile int* abort = &side.abort;
+  volatile int* limit = &side.limit;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.y % p.kv_heads, split = blockIdx.y / p.kv_heads;
   let_next_start();
   if (threadIdx.x == 0) {
-    side.abort = 0;
+    side.limit = kWaitLimit;
     bar_init(dbar, 1);
     for (int i = 0; i < 2; ++i) {
       bar_init(&full[i], kMeanArrivals);
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
     float4* out4 = reinterpret_cast<float4*>(p.tops) + (row0 + (int64_t)row * p.kv_heads) * p.tiles;
     int i = 0;
     for (int tile = split; tile < tiles; tile += p.splits, ++i) {
-      if (!wait_all(&acc_full[i & 1], (i >> 1) & 1, abort)) break;
+      if (!wait_all(&acc_full[i & 1], (i >> 1) & 1, limit)) break;
       fence_after();
       uint32_t sc[2][32];
 #pragma unroll
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
     int i = 0;
     for (int tile = split; tile < tiles; tile += p.splits, ++i) {
       const int st = i & 1;
-      if (i >= 2 && !wait_all(&empty[st], ((i >> 1) & 1) ^ 1, abort)) break;
+      if (i >= 2 && !wait_all(&empty[st], ((i >> 1) & 1) ^ 1, limit)) break;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int page = 32 * u + (lt >> 2);
@@ -524,8 +524,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
         next[u] = id_of(tile + 2 * p.splits, u);
       }
       if (warp == 4) {
-        if (!wait_all(&full[st], (i >> 1) & 1, abort)) break;
-        if (i >= 2 && !wait_all(&acc_free[st], ((i >> 1) & 1) ^ 1, abort)) break;
+        if (!wait_all(&full[st], (i >> 1) & 1, limit)) break;
+        if (i >= 2 && !wait_all(&acc_free[st], ((i >> 1) & 1) ^ 1, limit)) break;
         fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
         __syncwarp();
       }
     }
-    if (warp == 4 && __any_sync(0xFFFFFFFFu, *abort)) {  // products in flight end before the CTA does
+    if (warp == 4 && __any_sync(0xFFFFFFFFu, gave_up(limit))) {  // products in flight end before the CTA does
       if (elect_one()) mma_commit(dbar);
       __syncwarp();
       drain(dbar, 0);
