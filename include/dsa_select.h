@@ -561,8 +561,10 @@ int dsa_cache_attention_status(void);
  *
  * A step (dsa_kv_attention, dsa_kv_select, dsa_kv_block_attention).  Tokens
  * first[r] .. first[r + 1] - 1 are request r's newest, lens[r] its length with
- * them: token i has position p = lens[r] - first[r + 1] + i.  Rows of tokens at
- * or past first[requests] are left as they were.  heads = kv_heads * n, n = 1 ..
+ * them: token i has position p = lens[r] - first[r + 1] + i.  A request whose length
+ * is below its tokens here (or negative) has none: its tokens attend to nothing and
+ * have no pages (no plan makes such a step).  Rows of tokens at or past
+ * first[requests] are left as they were.  heads = kv_heads * n, n = 1 ..
  * 128; query head h belongs to key/value head h / n.
  *   requests   1 .. 8192 (tokens 0: nothing is read);  table_width >= 0
  *   q          [tokens, heads, 128] with q_stride elements (a multiple of 8)

@@ -9,7 +9,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tests import kv_ref as ref  # noqa: E402
-from tests.test_gpu_kv import BF16, F16, _attend, _dsa, _lists  # noqa: E402
+from tests.test_gpu_kv import BF16, F16, _attend, _dsa, _lists, _select  # noqa: E402
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
 
@@ -119,3 +119,13 @@ def test_a_pool_of_no_pages_and_odd_queries(P):
                 ws = torch.empty(dsa.dsa_kv_block_attention_workspace(cfg, q, idx, tables), dtype=torch.uint8, device=dev)
                 dsa.dsa_kv_block_attention(cfg, none, none, q, idx, first, lens, tables, 0.1, ws, o, lse)
             assert (o == 0).all() and (lse == -math.inf).all()
+
+
+def test_no_pages_for_rows_without_a_position():
+    """The selection's side of it: none of a request's tokens has a page where its length is below them."""
+    step = ref.Step([300, 300, 400], [40, 5, 40], H=8, Hk=2, page=16, dtype=BF16, seed=3, pad=1)
+    q, means = step.normal(step.T, 8, 128), step.normal(step.pages, 2, 128)
+    for n in (39, 1, 0, -1, -2 ** 31):
+        _shorten(step, 0, n)
+        idx = _select(step, means, q, 6, 1, 1)
+        assert (idx[:40] == -1).all() and (idx[40:85] >= 0).any(-1).all()
