@@ -373,8 +373,9 @@ class PagedKV:
         refusal(self.status)
 
     def append(self, q, k, v):
-        """Store the step's rows k and v [tokens, kv_heads, 128]; the rotated q [tokens, heads, 128]."""
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        """Store the step's rows k and v [tokens, kv_heads, 128]; the rotated q
+        [tokens, heads, 128], zeros in rows past the step's last token."""
+        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
         dsa_kv_append(self.cfg, q, k, v, self.ends, self.slots, self.turns, self.neighbours, self.gain, out, self.k,
                       self.v, self.means)
         return out
