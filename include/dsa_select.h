@@ -621,13 +621,14 @@ int dsa_kv_append(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t 
  *   workspace  device memory, 16-byte aligned, of at least
  *              dsa_kv_attention_workspace() bytes; nothing in it has to start at
  *              zero.  Calls that may run at the same time need one each.
- * Scores, sums and outputs are held in f32; the softmax weights are rounded to
- * cfg's type for the second product.  What a row does not attend to -- later
- * positions, stale rows of a page -- has no effect on it, whatever it holds (but
- * on the time: a row is computed a second time, by one warp, where a NaN or an
- * infinity stands in a tile it attends to part of).  A NaN score makes a row's o
- * and lse NaN, one of +infinity its o NaN and its lse +infinity.  Results repeat
- * bit for bit.
+ * Scores, sums and outputs are held in f32; the softmax weights, the largest of them
+ * between 2^7 and 2^15, are rounded to cfg's type for the second product (bf16 values of
+ * more than 2^112 / positions pass the sums' range).  What a row does not attend to --
+ * later positions, stale rows of a page -- has no effect on it, whatever it holds (but
+ * on the time: a row is computed a second time, by one warp, where a value in a tile
+ * that it attends to part of is a NaN or infinite, or, with lists, a score there).  A
+ * NaN score makes a row's o and lse NaN, one of +infinity its o NaN and its lse
+ * +infinity.  Results repeat bit for bit.
  */
 int dsa_kv_attention_workspace(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests,
                                int32_t table_width, size_t* bytes);
@@ -648,9 +649,11 @@ int dsa_kv_attention(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32
  *   select  1 .. 256;  lead >= 0, trail >= 1, lead + trail <= select.  The own page
  *           of a position past the table is the table's last.
  *   workspace  as above, dsa_kv_select_workspace() bytes
- * Ranks are those of the scores in exact arithmetic (f64 where f32 cannot tell
- * two apart); among equal scores the lower page wins; a NaN score ranks below
- * every other.  A page without a valid id has no score and ranks as a NaN does.
+ * Ranks are those of the scores in f64 (which are computed where f32 cannot tell two
+ * apart); among equal scores the lower page wins; a NaN score ranks below every
+ * other.  A page without a valid id has no score and ranks as a NaN does.  A token
+ * for which hundreds of pages come close to its last place takes many times as long
+ * as others.
  */
 int dsa_kv_select_workspace(const dsa_kv_cfg* cfg, int32_t tokens, int32_t heads, int32_t requests,
                             int32_t table_width, size_t* bytes);

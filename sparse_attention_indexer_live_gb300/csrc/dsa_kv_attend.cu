@@ -29,8 +29,9 @@
 //   * one token of 128K positions, 8 heads on 1 (67 MB, 9.9 us): 28.6 us, 23.5 when the L2
 //     holds them.  6 us to the first scores (launch, shares, lengths, first tile), six
 //     tiles an SM, their join;
-//   * chunks: 4,096 tokens over 32K positions 1,328 us, 1.55 PFLOP/s of the 1.98 that a
-//     large product reaches.  3,000 cycles a pair of tiles of which the products are
+//   * chunks: 4,096 tokens over 32K positions 1,328 us in a burst, 1.55 PFLOP/s of the 1.98
+//     that a large product reaches; 1,510 us, 1.36 of 1.70, held for seconds under the
+//     power cap.  3,000 cycles a pair of tiles of which the products are
 //     2,200: the tensor cores wait for weights where a stream's softmax (1,360 cycles and
 //     two waits) is not hidden by the other's products.  One stream a row tile and one
 //     issuing warp; 16 softmax warps took 2,035 us;
@@ -87,12 +88,12 @@ static_assert(kSmem <= 232448, "shared memory");
 static_assert(sizeof(Desc) % 8 == 0, "barriers on 8-byte boundaries");
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;  // S (and P) at 0 and 128, O at 256 and 384
 constexpr int kNever = 0x7FFFFFFF;                 // past every page number
-// A unit costs this many positions besides its own (one of two row tiles as much as
-// one of one: 31 decode requests beside three prompts took 143 us so, 168 at costs of
-// 3 : 2 and 149 at 2 : 3; 64 requests 275 us, 282 at a cost of 0 and 276 of 512); a CTA
-// takes no share below kLeast (one token of 128K 23.9 us, 31 at 2,048); a cut less than
-// kSnap tiles from a unit's end moves there (lists of 2,048 tokens 217 us, 220 at 1 and
-// 226 at 4; of 64 tokens 46.7, 46.8 and 42.4).
+// A unit costs this many positions besides its own (64 requests 270 us, 279 at a cost of
+// 0 and 272 of 512; 31 drafts beside three prompts 137, 137 and 139), one of two row tiles
+// as much as one of one (the drafts and prompts took 143 us then, 168 at costs of 3 : 2 and
+// 149 at 2 : 3); a CTA takes no share below kLeast (one token of 128K 28.4 us, 32.4 at
+// 2,048); a cut less than kSnap tiles from a unit's end moves there (lists of 2,048 tokens
+// 210 us, 211 at 1 and 224 at 4; of 64 tokens 48, 48 and 45).
 constexpr int kUnitCost = 256;
 constexpr int kLeast = 512;
 constexpr int kSnap = 2;
@@ -1128,7 +1129,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             }
           }
           // scores so large that the fused exponent is off by more than the maximum's
-          // rounding (2^-24 of it): their products are rounded as the maximum's was
+          // rounding (2^-24 of it): their products are rounded as the maximum's was (so are
+          // those of a warp with a row that has attended to nothing yet: its base is -inf)
           if (__any_sync(0xFFFFFFFFu, fabsf(m_used) > 65536.f)) {
             mul = 1.f;
 #pragma unroll

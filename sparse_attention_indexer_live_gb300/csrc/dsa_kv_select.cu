@@ -566,8 +566,11 @@ __device__ __forceinline__ int64_t rank_key(double x) {
 // bounds (sets of whole groups of 16, or of pages where there are few groups; with eight
 // warps, whose m may be 255, of 512: each thread's two largest),
 // whatever may reach that goes on a short list, and of that list those that e leaves
-// open are scored again in fp64.  A list that does not fit (many equal scores) is
-// taken a part at a time, all in fp64, against the best so far.
+// open are scored again in fp64.  A list that does not fit (many equal scores, or pages
+// so like their neighbours that whole sets of them are among the best) gives way to all
+// pages a part at a time, in fp64, against the best so far: 2,048 tokens over 2,048 pages,
+// 59 us where pages are independent, take 2.1 ms where neighbours' means are correlated 0.9,
+// 2.6 where they are those of rotated keys with a shared part, 14.5 at 0.98.
 template <int W>
 struct Pick {
   static constexpr int kList = W == 1 ? 128 : 512;
